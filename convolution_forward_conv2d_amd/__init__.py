@@ -1,5 +1,5 @@
 """Python binding of libmiconv, the MI355X 2-D convolution forward pass and
-its data gradient.
+its data gradient, and the feed-forward operators.
 
 Argument marshalling only: every step of the convolution runs in the HIP
 kernels of ``libmiconv.so`` behind the C ABI declared in
@@ -7,7 +7,9 @@ kernels of ``libmiconv.so`` behind the C ABI declared in
 The ``mic_*`` functions mirror the C calls one for one (descriptors are
 ctypes handles); ``conv2d_forward`` / ``ConvPlan`` and
 ``conv2d_backward_data`` / ``DgradPlan`` and ``conv2d_backward_filter`` /
-``WgradPlan`` wrap them for torch tensors.
+``WgradPlan`` wrap them for torch tensors.  The feed-forward operators'
+tensor functions (``rms_norm``, ``linear``, ``gated_linear`` and their
+``_backward``) are in ``feed_forward.py`` and exported here.
 
 There is no fallback: if the library is missing the import fails.
 """
@@ -32,6 +34,7 @@ MIC_STATUS_ALLOC_FAILED = 5
 MIC_DTYPE_F32 = 0
 MIC_DTYPE_F64 = 1
 MIC_DTYPE_BF16 = 2
+MIC_DTYPE_F8_E4M3 = 3
 
 MIC_LAYOUT_NCHW = 0
 MIC_LAYOUT_NHWC = 1
@@ -41,6 +44,14 @@ MIC_POOL_AVG_INCLUDE_PAD = 1
 MIC_POOL_AVG_EXCLUDE_PAD = 2
 POOL_MODES = {"max": MIC_POOL_MAX, "avg_include_pad": MIC_POOL_AVG_INCLUDE_PAD,
               "avg_exclude_pad": MIC_POOL_AVG_EXCLUDE_PAD}
+
+MIC_ACT_NONE = 0
+MIC_ACT_RELU = 1
+MIC_ACT_GELU = 2
+MIC_ACT_GELU_TANH = 3
+MIC_ACT_SILU = 4
+ACTIVATIONS = {"none": MIC_ACT_NONE, "relu": MIC_ACT_RELU, "gelu": MIC_ACT_GELU, "gelu_tanh": MIC_ACT_GELU_TANH,
+               "silu": MIC_ACT_SILU}
 
 _TORCH_DTYPE = {torch.float32: MIC_DTYPE_F32, torch.float64: MIC_DTYPE_F64,
                 torch.bfloat16: MIC_DTYPE_BF16}
@@ -61,6 +72,7 @@ _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _ip = ctypes.POINTER(ctypes.c_int)
 _i64p = ctypes.POINTER(ctypes.c_int64)
+_szp = ctypes.POINTER(ctypes.c_size_t)
 
 _SIGS = {
     "mic_status_string": ([_i], ctypes.c_char_p),
@@ -109,6 +121,23 @@ _SIGS = {
                     ctypes.c_double, _vp, _i64, _i64], _i),
     "mic_brgemm_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
                                 ctypes.c_char_p, ctypes.c_size_t], _i),
+    "mic_rms_norm": ([_vp, _i, _i, _i, _i, ctypes.c_double, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp,
+                      _vp], _i),
+    "mic_rms_norm_backward_workspace": ([_vp, _i, _i, _szp], _i),
+    "mic_rms_norm_backward": ([_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                               ctypes.c_size_t], _i),
+    "mic_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
+                            _vp, _i64, _vp, ctypes.c_size_t], _i),
+    "mic_linear_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_backward": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                             _i64, _vp, _vp, ctypes.c_size_t], _i),
+    "mic_gated_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_gated_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                  _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t], _i),
+    "mic_gated_linear_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_gated_linear_backward": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                   _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t], _i),
 }
 
 
@@ -352,6 +381,58 @@ def mic_brgemm_kernel_name(handle, dtype, m, n, k, batch, a_stride_batch, a_stri
                                         b_stride_batch, b_stride_k, b_stride_n, c_stride_m, c_stride_n, buf,
                                         len(buf)), "mic_brgemm_kernel_name")
     return buf.value.decode()
+
+
+def _bytes(fn, where, *args):
+    n = ctypes.c_size_t()
+    _check(fn(*args, ctypes.byref(n)), where)
+    return n.value
+
+
+def mic_rms_norm(*args):
+    _check(lib().mic_rms_norm(*args), "mic_rms_norm")
+
+
+def mic_rms_norm_backward_workspace(handle, rows, cols):
+    return _bytes(lib().mic_rms_norm_backward_workspace, "mic_rms_norm_backward_workspace", handle, rows, cols)
+
+
+def mic_rms_norm_backward(*args):
+    _check(lib().mic_rms_norm_backward(*args), "mic_rms_norm_backward")
+
+
+def mic_linear_forward_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_forward_workspace, "mic_linear_forward_workspace", handle, dtype, m, n, k)
+
+
+def mic_linear_forward(*args):
+    _check(lib().mic_linear_forward(*args), "mic_linear_forward")
+
+
+def mic_linear_backward_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_backward_workspace, "mic_linear_backward_workspace", handle, dtype, m, n, k)
+
+
+def mic_linear_backward(*args):
+    _check(lib().mic_linear_backward(*args), "mic_linear_backward")
+
+
+def mic_gated_linear_forward_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_gated_linear_forward_workspace, "mic_gated_linear_forward_workspace", handle, dtype, m,
+                  n, k)
+
+
+def mic_gated_linear_forward(*args):
+    _check(lib().mic_gated_linear_forward(*args), "mic_gated_linear_forward")
+
+
+def mic_gated_linear_backward_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_gated_linear_backward_workspace, "mic_gated_linear_backward_workspace", handle, dtype, m,
+                  n, k)
+
+
+def mic_gated_linear_backward(*args):
+    _check(lib().mic_gated_linear_backward(*args), "mic_gated_linear_backward")
 
 
 # ---------------------------------------------------------------- torch-facing helpers
@@ -798,3 +879,7 @@ class BlockedConvPlan(ConvPlan):
         mic_conv_desc_set(self.cd, *padding, *stride)
         self.shapes = (xs, ws, ys)
         self.flops = 2.0 * ys[0] * ys[1] * ys[2] * ys[3] * ws[1] * ws[2] * ws[3]
+
+
+from .feed_forward import (RmsNorm, gated_linear, gated_linear_backward, linear, linear_backward,  # noqa: E402,F401
+                           rms_norm, rms_norm_backward)

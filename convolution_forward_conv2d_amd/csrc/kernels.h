@@ -168,4 +168,77 @@ hipError_t launch_bwd_data_subpixel(DType dt, const ConvParams& p, hipStream_t s
 bool bwd_filter_rows_fits(Variant v, const ConvParams& p);
 hipError_t launch_bwd_filter_rows(Variant v, const ConvParams& p, hipStream_t stream);
 
+// ---------------------------------------------------------------- feed-forward operators
+//
+// A product with its epilogue (linear_common.h): x W^T of a linear or gated
+// layer, dz W for dx, dz^T x for dW.
+enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD };
+// Operands, and the outputs where they differ; SHORT: e4m3's own matrix
+// instruction (its sums are short, see linear_common.h).
+enum class ProductType : int { F32, BF16, E4M3_BF16, E4M3_F32, E4M3_BF16_SHORT, E4M3_F32_SHORT };
+
+struct ProductArgs;
+// Any sizes, pitches and alignments (linear_any.hip); tile 64 or 128.
+hipError_t launch_product_any(Product kind, ProductType type, const ProductArgs& p, int tile, hipStream_t stream);
+// Joins p.splits partial products and finishes them.
+hipError_t launch_product_join(Product kind, ProductType type, const ProductArgs& p, hipStream_t stream);
+
+// The gradient that reaches the products, dz, from dy and what the forward
+// pass kept (linear_grad.hip).  dz rows of `dz_pitch` elements: the layer's n
+// columns (gated: the gate's, then at `up_at` the other product's), zero up
+// to the pitch.
+struct SlopeArgs {
+    int rows, cols, act;
+    const void* dy;
+    int64_t lddy;
+    const void* pre;          // z, or a gated layer's gate; null: no activation
+    int64_t ldp;
+    const void* up;           // gated layers only
+    int64_t ldu;
+    void* dz;                 // null: only the column sums
+    int64_t dz_pitch, up_at;
+    float* sums;              // [row groups][cols] partial column sums, or null
+    void* dbias;
+};
+int slope_row_groups(int rows, int cols);
+hipError_t launch_slope(DType dt, const SlopeArgs& p, hipStream_t stream);
+
+// Root-mean-square norm of s = x + residual (rms_norm.hip).
+struct NormArgs {
+    int rows, cols;
+    float eps;
+    const void* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    const void* weight;
+    void* y;
+    int64_t ldy;
+    void* sum;
+    int64_t lds;
+    float* rstd;
+    float* scale;             // e4m3 output only
+};
+struct NormGradArgs {
+    int rows, cols;
+    const void* dy;
+    int64_t lddy;
+    const void* sum;
+    int64_t lds;
+    const void* weight;
+    const float* rstd;
+    const void* dsum;
+    int64_t ldd;
+    void* dx;
+    int64_t lddx;
+    void* dweight;
+    float* partial;           // [groups][cols]
+    int groups;
+};
+hipError_t launch_rms_norm(DType dt, bool e4m3, const NormArgs& p, hipStream_t stream);
+int rms_norm_grad_groups(int rows, int cols, int num_cu);
+hipError_t launch_rms_norm_grad(DType dt, const NormGradArgs& p, hipStream_t stream);
+// out[c] = sum over `groups` of partial[g][c], in out's type.
+hipError_t launch_column_join(DType dt, const float* partial, int groups, int cols, void* out, hipStream_t stream);
+
 }  // namespace miconv

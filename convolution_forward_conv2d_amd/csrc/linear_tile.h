@@ -1,0 +1,141 @@
+// linear_tile.h -- one workgroup's tile of a product in LDS: its layouts, the
+// fragments the matrix instructions take from it, and the epilogue.
+//
+// A k step of a tile is 128 bytes of each of its rows, R x 128 bytes in LDS:
+//  * k-major operand: row r's 128 bytes together, its 16-byte pieces permuted
+//    by (r / 2) % 8, so that sixteen rows read at one k meet all 64 banks;
+//  * operand stored across k: panels of 128 bytes of rows (64 bf16, 32 fp32),
+//    each with one 128-byte line per k.  bf16 is read with the LDS's
+//    transposing loads, four lines at a time: the two 64-byte halves of a line
+//    swap places where k & 2 is set, so four lines' halves meet all 64 banks.
+// Either way eight lines of 128 bytes are 1 KB, one load instruction's worth.
+#pragma once
+
+#include "linear_common.h"
+
+namespace miconv {
+
+// byte offset in the tile of the 16-byte piece `piece` of line `line` (k-major:
+// line = row; across k: line = panel * lines per panel + k)
+template <int E, bool ACROSS> __device__ __forceinline__ int tile_piece(int line, int piece)
+{
+    if constexpr (!ACROSS) return line * 128 + 16 * (piece ^ ((line >> 1) & 7));
+    if constexpr (E == 2) return line * 128 + 16 * (piece ^ ((line & 2) << 1));
+    return line * 128 + 16 * piece;
+}
+
+// Fragment of rows r0 .. r0 + 31 (r0 a multiple of 32), half `s` of the step.
+template <int E, bool ACROSS>
+__device__ __forceinline__ void read_fragment(const uint8_t* tile, int r0, int s, int lane, u32x4 (&f)[2])
+{
+    if constexpr (!ACROSS) {
+        const int r = r0 + (lane & 31);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            f[t] = *reinterpret_cast<const u32x4*>(tile + tile_piece<E, false>(r, 4 * s + 2 * t + (lane >> 5)));
+    } else if constexpr (E == 2) {
+        // sixteen lanes fetch 4 k x 16 rows, 8 bytes each, and get one row's four k
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* lds4;
+        const int j = lane & 15;
+        const int k = 8 * (lane >> 5) + (j >> 2);
+        const int byte = ((r0 & 32) << 1) + ((lane & 16) << 1) + 8 * (j & 3);
+        const uint8_t* at = tile + (r0 >> 6) * 8192 + (32 * s + k) * 128 + (byte ^ ((k & 2) << 5));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + t * 2048)));
+            const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + t * 2048 + 512)));
+            f[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        }
+    } else {
+        const uint8_t* at = tile + (r0 >> 5) * 4096 + (16 * s + 4 * (lane >> 5)) * 128 + 4 * (lane & 31);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[t][e] = *reinterpret_cast<const uint32_t*>(at + (8 * t + e) * 128);
+    }
+}
+
+// Lanes exchange data through LDS next: the wave's DS instructions execute in
+// order, this keeps the compiler from moving them across.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Epilogue of one wave: its FM x FN blocks of 32 rows x 32 raw columns, first
+// row m0, first raw column j0.  acc holds columns along its registers, so a
+// lane writes four columns of a row at once into the wave's own LDS stage and
+// then takes eight of a row from it: 16-byte accesses to every tensor, whole
+// 64- or 128-byte lines per row.  The caller has passed a barrier after the
+// last read of the operand tiles.
+template <class Out, int EPI, int FM, int FN>
+__device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, f32x16 (&acc)[FM][FN], int m0, int j0,
+                                            int split, int lane)
+{
+    constexpr int W = 32 * FN, PITCH = W + 4;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(stage + (lane & 31) * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
+                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        wave_order();
+        if (p.splits > 1) {
+            constexpr int PER = W / 8;
+#pragma unroll 2
+            for (int it = lane; it < 32 * PER; it += 64) {
+                const int r = it / PER, c = it % PER * 8, m = m0 + 32 * i + r;
+                if (m >= p.M) continue;
+                float* out = p.part + ((int64_t)split * p.M + m) * p.part_ld + j0 + c;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    reinterpret_cast<f32x4*>(out)[h] = reinterpret_cast<const f32x4*>(stage + r * PITCH + c)[h];
+            }
+        } else if constexpr (EPI == EPI_GATED) {
+            constexpr int PER = W / 16;                       // 16 of 32 raw columns are the gate's
+#pragma unroll 1
+            for (int it = lane; it < 32 * PER; it += 64) {
+                const int r = it / PER, g = it % PER;         // group g: block g / 2, its half g % 2
+                const float* at = stage + r * PITCH + (g >> 1) * 32 + (g & 1) * 8;
+                float v[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = at[e], u[e] = at[16 + e];
+                finish8<Out, EPI>(p, m0 + 32 * i + r, j0 / 2 + g * 8, v, u);
+            }
+        } else {
+            constexpr int PER = W / 8;
+#pragma unroll 1
+            for (int it = lane; it < 32 * PER; it += 64) {
+                const int r = it / PER, c = it % PER * 8;
+                float v[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = stage[r * PITCH + c + e];
+                finish8<Out, EPI>(p, m0 + 32 * i + r, j0 + c, v, u);
+            }
+        }
+        wave_order();
+    }
+}
+
+// Which tile a workgroup takes.  Workgroups go round the eight XCDs in launch
+// order, each with its own L2: an XCD gets a contiguous run of tiles, and the
+// run walks GROUP row tiles down before it moves to the next column tile, so
+// the 32 tiles an XCD computes at one time share operand rows in its L2.
+__device__ __forceinline__ void pick_tile(int id, int mt, int nt, int& tm, int& tn)
+{
+    constexpr int XCDS = 8, GROUP = 8;
+    const int total = mt * nt, per = total / XCDS, rest = total % XCDS;
+    const int x = id % XCDS, y = id / XCDS;
+    const int t = x * per + (x < rest ? x : rest) + y;
+    const int band = t / (GROUP * nt), first = band * GROUP;
+    const int rows = mt - first < GROUP ? mt - first : GROUP;
+    const int in = t - first * nt;
+    tm = first + in % rows;
+    tn = in / rows;
+}
+
+}  // namespace miconv

@@ -18,13 +18,8 @@
 
 #include "miconv.h"
 #include "conv_params.h"
+#include "handle.h"
 #include "kernels.h"
-
-struct mic_handle_st {
-    int device;
-    int num_cu;
-    hipStream_t stream;
-};
 
 struct mic_tensor_desc_st {
     bool set;
@@ -74,6 +69,7 @@ size_t dtype_size(mic_dtype d)
     case MIC_DTYPE_F32: return 4;
     case MIC_DTYPE_F64: return 8;
     case MIC_DTYPE_BF16: return 2;
+    case MIC_DTYPE_F8_E4M3: return 1;
     }
     return 0;
 }
