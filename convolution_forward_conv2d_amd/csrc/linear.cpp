@@ -56,39 +56,171 @@ mic_status launched(hipError_t e) { return e == hipSuccess ? MIC_STATUS_SUCCESS 
 
 // How a product runs.
 struct Plan {
-    int tile;
+    bool fast;               // linear_fast.h, else linear_any.hip
+    miconv::FastTile fast_tile;
+    int tile;                // linear_any.hip's
     int splits;
     int64_t part_ld;
-    size_t bytes;            // workspace
+    int64_t pack_a, pack_b;  // bytes of a packed operand's row, 0: read where it is
+    size_t a_bytes, b_bytes; // of the packed copies (b_bytes: each of a gated layer's two)
+    size_t bytes;            // workspace: the copies, then the partial sums
+    double us;
 };
 
-Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments)
+int element_bytes(ProductType t) { return t == ProductType::F32 ? 4 : t == ProductType::BF16 ? 2 : 1; }
+
+// Operands' rows (as they lie in memory) and their lengths in elements.
+struct Extent {
+    int a_rows, a_cols, b_rows, b_cols;
+};
+
+Extent extent_of(Product kind, int m, int n, int k)
 {
-    Plan pl = {};
+    switch (kind) {
+    case Product::INPUT_GRAD: return {m, k, k, n};             // dz (m, k), w (k, n)
+    case Product::WEIGHT_GRAD: return {k, m, k, n};            // dz (k, m), x (k, n)
+    default: return {m, k, n, k};
+    }
+}
+
+// The measured cost of a step (128 bytes of k) of each kernel's tile with every
+// CU busy, microseconds, and of a tile's start and epilogue; a launch; memory's
+// rate for the copies and partial sums.  Only their ratios decide.
+constexpr double kLaunchUs = 4.0, kBytesPerUs = 4.0e6;
+struct TileCost {
+    int bm, bn;
+    double step, tile;
+};
+constexpr TileCost kFast[] = {{256, 256, 2.00, 3.0}, {256, 192, 1.38, 2.3}, {192, 256, 1.30, 2.3},
+                              {256, 128, 1.05, 1.6}, {128, 256, 1.05, 1.6}, {128, 128, 0.55, 1.0}};
+
+// The cheapest way through a product of m x n outputs and k_segments * k terms.
+// `aligned_a` / `aligned_b`: the operand's rows can be read 16 bytes at a time.
+Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, bool aligned_a,
+                  bool aligned_b)
+{
     const int raw_n = kind == Product::GATED ? miconv::gated_raw_columns(n) : n;
-    auto tiles = [&](int t) { return (int64_t)((m + t - 1) / t) * ((raw_n + t - 1) / t); };
-    pl.tile = tiles(128) >= num_cu / 2 ? 128 : 64;
-    const int line = type == ProductType::F32 ? 32 : type == ProductType::BF16 ? 64 : 128;
-    const int64_t steps = (int64_t)((k + line - 1) / line) * k_segments;
-    const int64_t t = tiles(pl.tile);
-    // a second wave of workgroups per CU hides the first one's loads; a part has at least eight steps
-    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2 * num_cu / std::max<int64_t>(t, 1), steps / 8));
-    pl.part_ld = align_up(raw_n, pl.tile);
-    pl.bytes = pl.splits > 1 ? (size_t)pl.splits * m * pl.part_ld * 4 : 0;
-    return pl;
+    const int e = element_bytes(type);
+    const int64_t steps = (int64_t)((k + 128 / e - 1) / (128 / e)) * k_segments;
+    auto tiles = [&](int bm, int bn) { return (int64_t)((m + bm - 1) / bm) * ((raw_n + bn - 1) / bn); };
+    // a reduction is split where tiles leave CUs idle: parts of at least four steps, no more than fill the CUs twice
+    auto most_splits = [&](int64_t t) {
+        return (int)std::max<int64_t>(1, std::min<int64_t>({2 * num_cu / std::max<int64_t>(t, 1), steps / 4, 32}));
+    };
+    auto join_us = [&](int splits) {
+        return splits > 1 ? kLaunchUs + (double)m * raw_n * 4 * 2 * splits / kBytesPerUs : 0.0;
+    };
+    auto rounds = [&](int64_t t, int slots) { return (double)((t + slots - 1) / slots); };
+    Plan best = {};
+    best.us = 1e30;
+    auto consider = [&](Plan pl, int64_t t, int bn, int slots, double step, double tile) {
+        for (int s = 1, most = most_splits(t); s <= most; ++s) {
+            const double us = rounds(t * s, slots) * ((steps + s - 1) / s * step + tile) + join_us(s) + pl.us;
+            if (us < best.us) {
+                best = pl;
+                best.splits = s;
+                best.us = us;
+                best.part_ld = align_up(raw_n, bn);
+            }
+        }
+    };
+    // linear_any.hip: two workgroups per CU on 128 x 128 tiles, four on 64 x 64; fp32's matrix instructions take
+    // sixteen times bf16's time for the same bytes
+    const double slow = type == ProductType::F32 ? 4.0 : type == ProductType::BF16 ? 1.0 : 1.8;
+    Plan any = {};
+    any.tile = 128;
+    consider(any, tiles(128, 128), 128, 2 * num_cu, 1.45 * slow, 2.0);
+    any.tile = 64;
+    consider(any, tiles(64, 64), 64, 4 * num_cu, 1.10 * slow, 1.5);
+
+    const Extent x = extent_of(kind, m, n, k);
+    const bool short_rows = (int64_t)std::max(x.a_cols, x.b_cols) * e < kMaxPitchBytes / 2 - 64;
+    // two k segments are one matrix, laid out by the library and aligned
+    if ((type == ProductType::BF16 || type == ProductType::E4M3_BF16_SHORT || type == ProductType::E4M3_F32_SHORT)
+        && short_rows && (aligned_a || k_segments == 1)) {
+        Plan pl = {};
+        pl.fast = true;
+        if (!aligned_a) {
+            pl.pack_a = align_up((int64_t)x.a_cols * e, 16);
+            pl.a_bytes = (size_t)align_up(pl.pack_a * x.a_rows, 256);
+            pl.us += kLaunchUs + 2.0 * pl.a_bytes / kBytesPerUs;
+        }
+        if (!aligned_b) {
+            const int copies = kind == Product::GATED ? 2 : k_segments;
+            pl.pack_b = align_up((int64_t)x.b_cols * e, 16);
+            pl.b_bytes = (size_t)align_up(pl.pack_b * x.b_rows, 256);
+            pl.us += copies * (kLaunchUs + 2.0 * pl.b_bytes / kBytesPerUs);
+        }
+        for (int i = 0; i < (int)miconv::FastTile::COUNT; ++i) {
+            const TileCost& c = kFast[i];
+            pl.fast_tile = (miconv::FastTile)i;
+            consider(pl, tiles(c.bm, c.bn), c.bn, num_cu, c.step, c.tile);
+        }
+    }
+    const int copies = kind == Product::GATED ? 2 : k_segments;
+    best.bytes = best.a_bytes + copies * best.b_bytes
+                 + (best.splits > 1 ? (size_t)best.splits * m * best.part_ld * 4 : 0);
+    return best;
+}
+
+// Workspace for any alignment of the operands.
+size_t product_bytes(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments)
+{
+    if (!m || !n) return 0;
+    size_t most = 0;
+    for (int a = 0; a < 2; ++a)
+        for (int b = 0; b < 2; ++b)
+            most = std::max(most, plan_product(num_cu, kind, type, m, n, k, k_segments, a != 0, b != 0).bytes);
+    return most;
+}
+
+bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes)
+{
+    return aligned(p, 16) && ld % 16 == 0 && bytes % 16 == 0 && ld < kMaxPitchBytes / 2;
 }
 
 mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes)
 {
     if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
-    const Plan pl = plan_product(num_cus(h), kind, type, p.M, p.N, p.K, p.k_segments);
+    const int e = element_bytes(type);
+    const bool a_across = kind == Product::WEIGHT_GRAD, b_across = a_across || kind == Product::INPUT_GRAD;
+    if (p.a_K < p.K) p.a_K = p.K;
+    if (p.a_rows < p.M) p.a_rows = p.M;
+    p.b_rows = p.N;
+    const bool two_b = kind == Product::GATED || p.k_segments > 1;
+    bool aligned_a = fast_rows(p.a, p.lda, (int64_t)(a_across ? p.a_rows : p.a_K) * e);
+    bool aligned_b = fast_rows(p.b, p.ldb, (int64_t)(b_across ? p.N : p.K) * e);
+    if (two_b) aligned_b = aligned_b && fast_rows(p.b2, p.ldb2, (int64_t)(b_across ? p.N : p.K) * e);
+    if (p.k_segments > 1) aligned_b = aligned_b && p.ldb == p.ldb2;
+    const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b);
     if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Extent x = extent_of(kind, p.M, p.N, p.K);
+    if (pl.pack_a) {
+        MIC_TRY(launched(miconv::launch_pack(p.a, p.lda, x.a_rows, (int64_t)x.a_cols * e, ws, pl.pack_a, h->stream)));
+        p.a = ws, p.lda = pl.pack_a;
+        if (a_across) p.a_rows = (int)(pl.pack_a / e);
+        ws += pl.a_bytes;
+    }
+    if (pl.pack_b) {
+        const int64_t row = (int64_t)x.b_cols * e;
+        MIC_TRY(launched(miconv::launch_pack(p.b, p.ldb, x.b_rows, row, ws, pl.pack_b, h->stream)));
+        p.b = ws, p.ldb = pl.pack_b;
+        ws += pl.b_bytes;
+        if (two_b) {
+            MIC_TRY(launched(miconv::launch_pack(p.b2, p.ldb2, x.b_rows, row, ws, pl.pack_b, h->stream)));
+            p.b2 = ws, p.ldb2 = pl.pack_b;
+            ws += pl.b_bytes;
+        }
+        if (b_across) p.b_rows = (int)(pl.pack_b / e);
+    }
     p.splits = pl.splits;
-    p.part = static_cast<float*>(workspace);
+    p.part = reinterpret_cast<float*>(ws);
     p.part_ld = pl.part_ld;
-    hipError_t e = miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
-    if (e == hipSuccess && pl.splits > 1) e = miconv::launch_product_join(kind, type, p, h->stream);
-    return launched(e);
+    hipError_t err = pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
+                             : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
+    if (err == hipSuccess && pl.splits > 1) err = miconv::launch_product_join(kind, type, p, h->stream);
+    return launched(err);
 }
 
 mic_status product_type(mic_dtype in, mic_dtype out, ProductType* type, bool fast = false)
@@ -105,9 +237,10 @@ mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m,
 {
     if (!bytes) return MIC_STATUS_BAD_PARAM;
     MIC_TRY(check_sizes(m, n, k));
-    ProductType type;
+    ProductType type, fast;
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &type));
-    *bytes = m && n ? plan_product(num_cus(h), kind, type, m, n, k, 1).bytes : 0;
+    MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &fast, true));
+    *bytes = std::max(product_bytes(num_cus(h), kind, type, m, n, k, 1), product_bytes(num_cus(h), kind, fast, m, n, k, 1));
     return MIC_STATUS_SUCCESS;
 }
 
@@ -124,8 +257,8 @@ GradLayout grad_layout(mic_handle h, ProductType type, int m, int n, int k, bool
     g.pitch = align_up(n, 64);
     g.dz = (size_t)align_up((int64_t)m * g.pitch * two * (type == ProductType::F32 ? 4 : 2), 256);
     g.sums = bias ? (size_t)align_up((int64_t)miconv::slope_row_groups(m, n) * n * 4, 256) : 0;
-    const size_t a = m && k ? plan_product(num_cus(h), Product::INPUT_GRAD, type, m, k, n, two).bytes : 0;
-    const size_t b = n && k ? plan_product(num_cus(h), Product::WEIGHT_GRAD, type, (int)(gated ? 2 * g.pitch : n), k, m, 1).bytes : 0;
+    const size_t a = product_bytes(num_cus(h), Product::INPUT_GRAD, type, m, k, n, two);
+    const size_t b = product_bytes(num_cus(h), Product::WEIGHT_GRAD, type, (int)(gated ? 2 * g.pitch : n), k, m, 1);
     g.product = std::max(a, b);
     g.total = g.dz + g.sums + g.product;
     return g;
@@ -143,9 +276,10 @@ mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k
     return MIC_STATUS_SUCCESS;
 }
 
-// dx = dz w (+ dz2 w2) and dw = dz^T x (dw2 = dz2^T x)
+// dx = dz w (+ dz2 w2) and dw = dz^T x (dw2 = dz2^T x).  dz has dz_cols >= n columns, zeros from n on (and the
+// second layer's from up_at on).
 mic_status grad_products(mic_handle h, ProductType type, int m, int n, int k, const void* dz, int64_t dz_pitch,
-                         int64_t up_at, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* w2,
+                         int64_t dz_cols, int64_t up_at, const void* x, int64_t ldx, const void* w, int64_t ldw, const void* w2,
                          int64_t ldw2, void* dx, int64_t lddx, void* dw, int64_t lddw, void* dw2, int64_t lddw2,
                          void* workspace, size_t bytes)
 {
@@ -156,7 +290,7 @@ mic_status grad_products(mic_handle h, ProductType type, int m, int n, int k, co
         p.a = static_cast<const uint8_t*>(dz), p.lda = dz_pitch * e;
         p.b = static_cast<const uint8_t*>(w), p.ldb = ldw * e;
         p.b2 = static_cast<const uint8_t*>(w2), p.ldb2 = ldw2 * e;
-        p.M = m, p.N = k, p.K = n;
+        p.M = m, p.N = k, p.K = n, p.a_K = (int)dz_cols;
         p.k_segments = gated ? 2 : 1, p.k_pitch = (int)up_at;
         p.m_pitch = INT32_MAX, p.m_valid = m;
         p.y = dx, p.ldy = lddx;
@@ -166,7 +300,7 @@ mic_status grad_products(mic_handle h, ProductType type, int m, int n, int k, co
         ProductArgs p = {};
         p.a = static_cast<const uint8_t*>(dz), p.lda = dz_pitch * e;
         p.b = static_cast<const uint8_t*>(x), p.ldb = ldx * e;
-        p.M = gated ? (int)(2 * up_at) : n, p.N = k, p.K = m;
+        p.M = gated ? (int)(2 * up_at) : n, p.N = k, p.K = m, p.a_rows = gated ? p.M : (int)dz_cols;
         p.k_segments = 1;
         p.m_pitch = gated ? (int)up_at : INT32_MAX, p.m_valid = n;
         p.y = dw, p.ldy = lddw;
@@ -314,7 +448,7 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
         s.dbias = dbias;
         MIC_TRY(launched(miconv::launch_slope(device_type(dtype), s, handle->stream)));
     }
-    return grad_products(handle, type, m, n, k, own ? ws : dy, own ? g.pitch : lddy, 0, x, ldx, w, ldw, nullptr, 0,
+    return grad_products(handle, type, m, n, k, own ? ws : dy, own ? g.pitch : lddy, own ? g.pitch : n, 0, x, ldx, w, ldw, nullptr, 0,
                          dx, lddx, dw, lddw, nullptr, 0, ws + g.dz + g.sums, g.product);
 }
 
@@ -413,7 +547,7 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
     }
     // n == 0: dx is a sum of nothing, and the weights are never read
     const void* w2 = w_up ? w_up : ws;
-    return grad_products(handle, type, m, n, k, ws, 2 * g.pitch, g.pitch, x, ldx, w_gate, ldg, w2, ldu, dx, lddx,
+    return grad_products(handle, type, m, n, k, ws, 2 * g.pitch, g.pitch, g.pitch, x, ldx, w_gate, ldg, w2, ldu, dx, lddx,
                          dw_gate, lddg, dw_up, lddu, ws + g.dz + g.sums, g.product);
 }
 

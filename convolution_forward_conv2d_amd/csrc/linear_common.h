@@ -155,6 +155,9 @@ struct ProductArgs {
     int M;                    // rows of A
     int N;                    // output columns
     int K;                    // reduction length of one segment
+    // linear_fast.h reads whole 16-byte pieces: the lengths its operands are padded to, zeros past the real ones
+    int a_K;                  // columns of k-major operands, >= K
+    int a_rows, b_rows;       // columns of operands stored across k, >= M and >= N
     int k_segments;           // 1, or 2: A's columns [k_pitch, k_pitch + K) meet b2
     int k_pitch;
     int m_pitch;              // rows at or past m_pitch are rows of the second output y2 (EPI_PLAIN)
@@ -268,7 +271,7 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, floa
 // value i of lane l is D[8 (i/4) + 4 (l/32) + i%4][l % 32].
 
 struct MulBf16 {
-    static constexpr int E = 2;
+    static constexpr int E = 2, PER_HALF = 2;                  // bytes per element, instructions per block and half
     using Out = Bf16;
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
@@ -281,7 +284,7 @@ struct MulBf16 {
 };
 
 struct MulF32 {
-    static constexpr int E = 4;
+    static constexpr int E = 4, PER_HALF = 8;
     using Out = float;
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
@@ -302,7 +305,7 @@ struct MulF32 {
 // (exact) in registers and adds in fp32; SHORT takes the e4m3 instruction, for
 // callers that ask for its rate.
 template <class OutT, bool SHORT> struct MulE4m3 {
-    static constexpr int E = 1;
+    static constexpr int E = 1, PER_HALF = SHORT ? 1 : 4;
     using Out = OutT;
     __device__ static bf16x8 widen(uint32_t lo, uint32_t hi)
     {

@@ -142,6 +142,69 @@ def test_gated_backward(m, n, k, dtype):
         R.check(g, want, "%s %s" % (what, name))
 
 
+# past one tile of every shape, reductions of one, few and many steps, aligned rows and not
+LARGE = [(256, 4096, 64), (512, 2048, 136), (1031, 1544, 264), (777, 2056, 520), (2048, 1100, 1032), (1500, 1501, 333),
+         (300, 4100, 2056)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large_products(m, n, k):
+    """Every product of bf16 and e4m3 on the large tiles; sampled rows and columns against 64 bits."""
+    g = torch.Generator().manual_seed(m + n + k)
+    rows = torch.cat([torch.tensor([0, m - 1]), torch.randint(0, m, (30,), generator=g)]).to(dev())
+    cols = torch.cat([torch.tensor([0, n - 1]), torch.randint(0, n, (30,), generator=g)]).to(dev())
+    kcols = torch.cat([torch.tensor([0, k - 1]), torch.randint(0, k, (30,), generator=g)]).to(dev())
+
+    def at(t, r, c):
+        return t[r][:, c]
+
+    x, w, wu = values(1, m, k, dtype=BF16), values(2, n, k, std=k ** -0.5, dtype=BF16), \
+        values(3, n, k, std=k ** -0.5, dtype=BF16)
+    bias, res = values(4, n, dtype=BF16), values(5, m, n, dtype=BF16)
+    y, z = mic.linear(x, w, bias=bias, residual=res, activation="gelu", return_preact=True)
+    ref = R.linear(x[rows], w[cols], bias[cols], at(res, rows, cols), "gelu", BF16)
+    R.check(at(y, rows, cols), ref[0], "y")
+    R.check(at(z, rows, cols), ref[1], "preact")
+    h, gate, up = mic.gated_linear(x, w, wu, return_products=True)
+    ref = R.gated(x[rows], w[cols], wu[cols], "silu", BF16)
+    for got, want, what in zip((h, gate, up), ref, ("h", "gate", "up")):
+        R.check(at(got, rows, cols), want, what)
+
+    dy, wb, wub = res, w * k ** 0.5, wu * k ** 0.5
+    dx, dw, db = mic.linear_backward(dy, x, wb, preact=z, activation="gelu", bias=True)
+    R.check(at(dx, rows, kcols), R.linear_backward(dy[rows], x[rows], wb[:, kcols], z[rows], "gelu")[0], "dx")
+    ref = R.linear_backward(dy[:, cols], x[:, kcols], wb[cols][:, kcols], z[:, cols], "gelu")
+    R.check(at(dw, cols, kcols), ref[1], "dw")
+    R.check(db[cols], ref[2], "dbias")
+    dx, dw, _ = mic.linear_backward(dy, x, wb)
+    R.check(at(dx, rows, kcols), R.linear_backward(dy[rows], x[rows], wb[:, kcols], None, "none")[0], "dx, dz = dy")
+    R.check(at(dw, cols, kcols), R.linear_backward(dy[:, cols], x[:, kcols], wb[cols][:, kcols], None, "none")[1],
+            "dw, dz = dy")
+    dx, dg, du = mic.gated_linear_backward(dy, x, wb, wub, gate, up)
+    R.check(at(dx, rows, kcols), R.gated_backward(dy[rows], x[rows], wb[:, kcols], wub[:, kcols], gate[rows], up[rows],
+                                                  "silu")[0], "gated dx")
+    ref = R.gated_backward(dy[:, cols], x[:, kcols], wb[cols][:, kcols], wub[cols][:, kcols], gate[:, cols],
+                           up[:, cols], "silu")
+    R.check(at(dg, cols, kcols), ref[1], "dw_gate")
+    R.check(at(du, cols, kcols), ref[2], "dw_up")
+
+    (x8, xs), (w8, ws), (u8, us) = quantised(6, m, k), quantised(7, n, k, std=k ** -0.5), quantised(8, n, k, std=k ** -0.5)
+    for fast in (False, True):
+        def short(v, scale):
+            top = (R.d(x8[rows]) * R.d(xs[rows])[:, None]).abs().amax(1)[:, None] \
+                * (R.d(v[cols]) * R.d(scale[cols])[:, None]).abs().amax(1)
+            return -(-k // 64) * 2.0 ** -11 * top if fast else 0.0
+        for out in (BF16, F32):
+            z = mic.linear(x8, w8, x_scale=xs, w_scale=ws, out_dtype=out, fast_sums=fast)
+            value, bound = R.linear(x8[rows], w8[cols], None, None, "none", out, xs[rows], ws[cols])[0]
+            R.check(at(z, rows, cols), (value, bound + 1.01 * short(w8, ws)), "e4m3")
+        _, gate, up = mic.gated_linear(x8, w8, u8, x_scale=xs, w_gate_scale=ws, w_up_scale=us, return_products=True,
+                                       fast_sums=fast)
+        ref = R.gated(x8[rows], w8[cols], u8[cols], "silu", BF16, xs[rows], ws[cols], us[cols])
+        R.check(at(gate, rows, cols), (ref[1][0], ref[1][1] + 1.01 * short(w8, ws)), "e4m3 gate")
+        R.check(at(up, rows, cols), (ref[2][0], ref[2][1] + 1.01 * short(u8, us)), "e4m3 up")
+
+
 NORM = [(1, 1), (1, 4096), (3, 7), (5, 63), (2, 64), (7, 511), (4, 512), (9, 513), (3, 2048), (5, 2049), (2, 4096),
         (3, 4097), (2, 8192), (3, 8200), (2, 16384), (2, 20001), (700, 264), (300, 1000)]
 
