@@ -152,7 +152,7 @@ __global__ __launch_bounds__(THREADS) void linear_any_kernel(const ProductArgs p
         if (t + 1 < last) store(buf ^ 1);
         __syncthreads();
     }
-    finish_wave<typename Mul::Out, EPI, FM, FN>(p, reinterpret_cast<float*>(smem) + wave * 32 * (32 * FN + 4), acc,
+    finish_wave<typename Mul::Out, EPI>(p, reinterpret_cast<float*>(smem) + wave * 32 * (32 * FN + 4), acc,
                                                 m0 + wm, j0 + wn, blockIdx.z, lane);
 }
 

@@ -271,7 +271,7 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, floa
 // value i of lane l is D[8 (i/4) + 4 (l/32) + i%4][l % 32].
 
 struct MulBf16 {
-    static constexpr int E = 2, PER_HALF = 2;                  // bytes per element, instructions per block and half
+    static constexpr int E = 2;                                // bytes per element
     using Out = Bf16;
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
@@ -281,10 +281,18 @@ struct MulBf16 {
                                                         __builtin_bit_cast(bf16x8, cols[t]), c, 0, 0, 0);
         return c;
     }
+    // for 16 rows and one half, lane l holds one vector: the bytes 16 (l / 16) of the half of row l % 16
+    using Block = f32x4;
+    static constexpr int T = 16;                               // large tiles' blocks: T x T
+    __device__ static f32x4 block(const u32x4* rows, const u32x4* cols, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, rows[0]),
+                                                       __builtin_bit_cast(bf16x8, cols[0]), c, 0, 0, 0);
+    }
 };
 
 struct MulF32 {
-    static constexpr int E = 4, PER_HALF = 8;
+    static constexpr int E = 4;
     using Out = float;
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
@@ -305,7 +313,7 @@ struct MulF32 {
 // (exact) in registers and adds in fp32; SHORT takes the e4m3 instruction, for
 // callers that ask for its rate.
 template <class OutT, bool SHORT> struct MulE4m3 {
-    static constexpr int E = 1, PER_HALF = SHORT ? 1 : 4;
+    static constexpr int E = 1;
     using Out = OutT;
     __device__ static bf16x8 widen(uint32_t lo, uint32_t hi)
     {
@@ -316,6 +324,9 @@ template <class OutT, bool SHORT> struct MulE4m3 {
         const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
         return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
     }
+    using Block = f32x16;
+    static constexpr int T = 32;
+    __device__ static f32x16 block(const u32x4* rows, const u32x4* cols, f32x16 c) { return mfma(rows, cols, c); }
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
         if constexpr (SHORT) {

@@ -4,17 +4,23 @@
 //
 // Eight waves on a tile of BM x BN, one workgroup per CU.  Operands go from
 // memory straight into LDS (buffer loads with an LDS destination, 16 bytes a
-// lane), double-buffered, and from there into the matrix instructions'
-// fragments, which are double-buffered in registers by half steps:
+// lane): A has three buffers there, B two, 160 KB at 256 x 256.  From LDS they
+// pass into the matrix instructions' fragments, double-buffered in registers by
+// half steps:
 //
-//   half 0   read fragments of half 1 of step t       products of half 0
-//   barrier  step t + 1 has landed, nobody reads step t's buffer any more
-//   half 1   start loading step t + 2, read half 0 of step t + 1
-//                                                     products of half 1
+//   half 0   products of half 0, reading half 1 of step t, loading A of t + 2
+//   barrier  A and B of step t + 1 have landed, nobody reads step t's any more
+//   half 1   products of half 1, reading half 0 of step t + 1, loading B of t + 2
 //
-// so the products wait for neither memory nor LDS, and a load has a whole step
-// (2048 cycles at 256 x 256) to arrive.
+// Reads and loads are placed one by one between the matrix instructions: a CU
+// takes a load instruction's kilobyte in about 16 cycles, so loads issued
+// together hold up the products behind them (by half of their own time at
+// 256 x 256), and over both halves they use at most half of that rate.  A load
+// of A has two halves to arrive after its own, one of B one and a half (a half:
+// 1024 cycles at 256 x 256).
 #pragma once
+
+#include <type_traits>
 
 #include "linear_tile.h"
 #include "kernels.h"
@@ -24,6 +30,19 @@ namespace miconv {
 constexpr int FAST_THREADS = 512;
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes a lane from the descriptor's memory at `offset` into LDS at `to` + 16 * lane; past the descriptor's end:
+// zeros.  In assembly because the compiler waits for every load into LDS before each transposing LDS read that follows,
+// whatever the two touch (the gradients' products ran at half speed); the kernel's own waits (landed) order them.
+// Nothing arrives in a register, and the inputs are read when the instruction issues; the no-ops cover the five states
+// that a vector-written scalar would need before it.  m0 is a register the compiler only ever sets itself right before
+// an instruction that takes it, and nothing else here does.
+__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t offset, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(to)
+                 : "memory");
+}
 
 // One operand's loads: R lines of 128 bytes a step, 8 lines per wave
 // instruction, R / 64 instructions per wave (instruction i of wave w: lines
@@ -54,7 +73,7 @@ template <int E, bool ACROSS, int R, bool GATED> struct Stream {
             left = (int64_t)(K - 1 - k) * ld + (int64_t)(rows - r0) * E - panel * 128;
             hop = 64 / LINES * 128;
             advance = ld * LINES;
-            piece = E == 2 ? (lane & 7) ^ ((line & 2) << 1) : lane & 7;
+            piece = (lane & 7) ^ ((line & 2) << 1) ^ ((line & 8) >> 2);
         } else {
             int r = r0 + wave * 8;
             hop = 64 * (uint32_t)ld;
@@ -73,46 +92,46 @@ template <int E, bool ACROSS, int R, bool GATED> struct Stream {
         off = (uint32_t)((lane >> 3) * ld + piece * 16);
     }
 
-    // Loads of the current step into `tile` (nothing is fetched unless `some`), then on to the next step.
-    __device__ __forceinline__ void load(uint8_t* tile, int wave, bool some)
+    // The current step's loads (nothing is fetched unless `some`), then on to the next step.
+    i32x4 rsrc;
+    uint32_t at;
+    __device__ __forceinline__ void next(bool some)
     {
-        // the host keeps pitches below 4 MB: offsets within a tile stay below 2^30
         const int records = (int)(left < 0 || !some ? 0 : left > 0x7fffff00 ? 0x7fffff00 : left);
-        const uint8_t* at = base;
-        uint32_t o = off;
-        if constexpr (!ACROSS) {
-            // a row's end is not the operand's: pieces past K take an offset no descriptor reaches
-            o = k_lane < k_left ? o : 0xfffffff0u;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int here = records - (int)(i * hop);
-            auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), 0, here > 0 ? here : 0, 0x00020000);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(tile + wave * 1024 + i * 8192), 16, o, 0, 0, 0);
-            at += hop;
-        }
+        const uint64_t from = reinterpret_cast<uint64_t>(base);
+        rsrc = i32x4{(int)from, (int)(from >> 32) & 0xffff, records, 0x00020000};
+        at = off;
+        // a row's end is not the operand's: pieces past K take an offset no descriptor reaches (the host keeps pitches
+        // below 4 MB, so offsets within a tile stay below 2^30 and the sum does not wrap)
+        if constexpr (!ACROSS) at = k_lane < k_left ? off : 0x80000000u;
         base += advance;
         left -= advance;
         k_left -= LINES;
     }
+    __device__ __forceinline__ void issue(uint8_t* tile, int wave, int i) const
+    {
+        load_to_lds(rsrc, at + i * hop, (uint32_t)(uintptr_t)(lds_ptr)(tile + wave * 1024 + i * 8192));
+    }
 };
 
-// This wave's loads into LDS have landed, then everyone's.
-__device__ __forceinline__ void landed()
+// All but this wave's last PENDING loads have landed in LDS and its reads are done, then everyone's.
+template <int PENDING> __device__ __forceinline__ void landed()
 {
-    __builtin_amdgcn_s_waitcnt(0x0f70);                        // vmcnt(0)
-    __syncthreads();
+    static_assert(PENDING < 16, "the low four bits of vmcnt");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const ProductArgs p)
 {
     static_assert(WM * WN == 8 && BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "eight waves of 32 x 32 blocks");
-    constexpr int E = Mul::E, BK = 128 / E, FM = BM / WM / 32, FN = BN / WN / 32;
-    constexpr int STEP = (BM + BN) * 128;
+    constexpr int E = Mul::E, BK = 128 / E, T = Mul::T, FM = BM / WM / T, FN = BN / WN / T;
+    constexpr int A_TILE = BM * 128, B_TILE = BN * 128, LDS = 3 * A_TILE + 2 * B_TILE;
     constexpr bool GATED = EPI == EPI_GATED;
-    static_assert(8 * 32 * (32 * FN + 4) * 4 <= 2 * STEP, "the epilogue's stages fit");
-    __shared__ __align__(1024) uint8_t smem[2 * STEP];
+    static_assert(8 * 32 * (T * FN + 4) * 4 <= LDS, "the epilogue's stages fit");
+    __shared__ __align__(1024) uint8_t smem[LDS];
 
     const int raw_n = GATED ? gated_raw_columns(p.N) : p.N;
     const int mt = (p.M + BM - 1) / BM, nt = (raw_n + BN - 1) / BN;
@@ -120,7 +139,7 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Prod
     pick_tile(blockIdx.x, mt, nt, tm, tn);
     const int m0 = tm * BM, j0 = tn * BN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / WN * 32 * FM, wn = wave % WN * 32 * FN;
+    const int wm = wave / WN * T * FM, wn = wave % WN * T * FN;
 
     const int per_segment = (p.K + BK - 1) / BK;
     const int steps = per_segment * p.k_segments;
@@ -140,84 +159,95 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Prod
         sa2.start(p.a + (int64_t)p.k_pitch * E, p.lda, nullptr, 0, m0, p.M, 0, p.a_K, wave, lane);
         sb2.start(p.b2, p.ldb, nullptr, 0, j0, p.b_rows, 0, p.K, wave, lane);
     }
-    int next = first;
-    auto load = [&](int buf) {                                 // the next step not loaded yet
+    uint8_t* const b_tiles = smem + 3 * A_TILE;
+    // the loads of the next step of A or B not loaded yet
+    int next_a = first, next_b = first;
+    auto turn_a = [&] {
         if constexpr (SEGMENTS) {
-            const bool turn = next == per_segment;             // selects, no branch: the pitches are the same
+            const bool turn = next_a == per_segment;           // selects, no branch: the pitches are the same
             sa.base = turn ? sa2.base : sa.base, sa.left = turn ? sa2.left : sa.left;
-            sb.base = turn ? sb2.base : sb.base, sb.left = turn ? sb2.left : sb.left;
             sa.k_left = turn ? sa2.k_left : sa.k_left;
         }
-        sa.load(smem + buf * BM * 128, wave, next < last);
-        sb.load(smem + (2 * BM + buf * BN) * 128, wave, next < last);
-        ++next;
+        sa.next(next_a < last);
+        ++next_a;
+    };
+    auto turn_b = [&] {
+        if constexpr (SEGMENTS) {
+            const bool turn = next_b == per_segment;
+            sb.base = turn ? sb2.base : sb.base, sb.left = turn ? sb2.left : sb.left;
+        }
+        sb.next(next_b < last);
+        ++next_b;
     };
 
-    f32x16 acc[FM][FN];
+    using Block = typename Mul::Block;
+    Block acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+            for (int e = 0; e < (int)(sizeof(Block) / 4); ++e) acc[i][j][e] = 0.0f;
 
-    u32x4 fa[2][FM][2], fb[2][FN][2];
-    auto read = [&](int buf, int s) {
-        // A's two buffers, then B's: either is within an LDS instruction's offset of one address
-        const uint8_t* ta = smem + buf * BM * 128;
-        const uint8_t* tb = smem + (2 * BM + buf * BN) * 128;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) read_fragment<E, BACROSS>(tb, wn + 32 * j, s, lane, fb[s][j]);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) read_fragment<E, AACROSS>(ta, wm + 32 * i, s, lane, fa[s][i]);
+    constexpr int V = T / 16;                                  // vectors of a fragment's half
+    u32x4 fa[2][FM][V], fb[2][FN][V];
+    // read q of the fragments of half s, in the order the products need them
+    constexpr int READS = V * (FM + FN);
+    auto read = [&](const uint8_t* ta, const uint8_t* tb, int s, int q) {
+        const int t = q < V * (FN + 1) ? q / (FN + 1) : q % V;
+        const int i = q < V * (FN + 1) ? q % (FN + 1) - FN : q / V - FN;             // A's block, or < 0: B's i + FN
+        if (i < 0) fb[s][i + FN][t] = read_piece<E, BACROSS, T>(tb, wn + T * (i + FN), s, t, lane);
+        else fa[s][i][t] = read_piece<E, AACROSS, T>(ta, wm + T * i, s, t, lane);
     };
-    auto multiply = [&](int s) {
+    // One half step: its products, with the next half's reads and one operand's loads between them.
+    constexpr int PRODUCTS = FM * FN;
+    auto half = [&](int s, const uint8_t* ta, const uint8_t* tb, auto& stream, uint8_t* into) {
+        constexpr int LOADS = std::remove_reference_t<decltype(stream)>::N;
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int n = 0; n < PRODUCTS; ++n) {
+            const int i = n / FN, j = n % FN;
+            acc[i][j] = Mul::block(fb[s][j], fa[s][i], acc[i][j]);
+            // reads in the first three quarters of the slots, so the barrier does not wait for them
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = Mul::mfma(fb[s][j], fa[s][i], acc[i][j]);
-    };
-
-    // One LDS read (two where rows are read across) before each of the first products: the reads are spread over the
-    // half step in which they have to arrive, and so are the loads.
-    constexpr int PRODUCTS = FM * FN * Mul::PER_HALF, LOADS = (BM + BN) / 64;
-    constexpr int READS = FM * (AACROSS ? 2 * E : 2) + FN * (BACROSS ? 2 * E : 2);
-    auto pace = [&](bool loads) {
+            for (int q = 0; q < READS; ++q)
+                if (q * PRODUCTS * 3 / (READS * 4) == n) read(ta, tb, s ^ 1, q);
+            // loads in the first half of the slots
 #pragma unroll
-        for (int i = 0; i < PRODUCTS; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, (READS + PRODUCTS - 1) / PRODUCTS, 0);
-            if (loads && i < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            for (int l = 0; l < LOADS; ++l)
+                if (l * PRODUCTS / (2 * LOADS) == n) stream.issue(into, wave, l);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     if (first < last) {
-        load(0);
-        landed();
-        load(1);
-        read(0, 0);
-        auto step = [&](int buf) {
-            read(buf, 1);
-            multiply(0);
-            pace(false);
-            __builtin_amdgcn_sched_barrier(0);
-            landed();
-            __builtin_amdgcn_sched_barrier(0);
-            read(buf ^ 1, 0);
-            load(buf);                                         // past the last step: nothing
-            multiply(1);
-            pace(true);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        int t = first;
-        for (; t + 1 < last; t += 2) {
-            step(0);
-            step(1);
+        constexpr int LA = BM / 64, LB = BN / 64;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            turn_a();
+#pragma unroll
+            for (int l = 0; l < LA; ++l) sa.issue(smem + b * A_TILE, wave, l);
+            turn_b();
+#pragma unroll
+            for (int l = 0; l < LB; ++l) sb.issue(b_tiles + b * B_TILE, wave, l);
         }
-        if (t < last) step(0);
-        landed();
+        landed<LA + LB>();
+#pragma unroll
+        for (int q = 0; q < READS; ++q) read(smem, b_tiles, 0, q);
+        int a0 = 0, a1 = A_TILE, a2 = 2 * A_TILE;              // A of steps t, t + 1, t + 2
+        int b0 = 0, b1 = B_TILE;
+        for (int t = first; t < last; ++t) {
+            turn_a();
+            half(0, smem + a0, b_tiles + b0, sa, smem + a2);
+            landed<LA>();
+            turn_b();
+            half(1, smem + a1, b_tiles + b1, sb, b_tiles + b0);
+            const int a = a0;
+            a0 = a1, a1 = a2, a2 = a;
+            b0 ^= B_TILE, b1 ^= B_TILE;
+        }
+        landed<0>();
     }
-    finish_wave<typename Mul::Out, EPI, FM, FN>(p, reinterpret_cast<float*>(smem) + wave * 32 * (32 * FN + 4), acc,
+    finish_wave<typename Mul::Out, EPI>(p, reinterpret_cast<float*>(smem) + wave * 32 * (T * FN + 4), acc,
                                                 m0 + wm, j0 + wn, blockIdx.z, lane);
 }
 

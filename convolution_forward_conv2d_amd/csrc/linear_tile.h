@@ -6,8 +6,10 @@
 //    by (r / 2) % 8, so that sixteen rows read at one k meet all 64 banks;
 //  * operand stored across k: panels of 128 bytes of rows (64 bf16, 32 fp32),
 //    each with one 128-byte line per k.  bf16 is read with the LDS's
-//    transposing loads, four lines at a time: the two 64-byte halves of a line
-//    swap places where k & 2 is set, so four lines' halves meet all 64 banks.
+//    transposing loads, four lines of 64 bytes or eight (four and four, eight
+//    apart) of 32 at a time: the two 64-byte halves of a line swap places where
+//    k & 2 is set and their 32-byte halves where k & 8 is, so either meets all
+//    64 banks.
 // Either way eight lines of 128 bytes are 1 KB, one load instruction's worth.
 #pragma once
 
@@ -20,40 +22,45 @@ namespace miconv {
 template <int E, bool ACROSS> __device__ __forceinline__ int tile_piece(int line, int piece)
 {
     if constexpr (!ACROSS) return line * 128 + 16 * (piece ^ ((line >> 1) & 7));
-    if constexpr (E == 2) return line * 128 + 16 * (piece ^ ((line & 2) << 1));
+    if constexpr (E == 2) return line * 128 + 16 * (piece ^ ((line & 2) << 1) ^ ((line & 8) >> 2));
     return line * 128 + 16 * piece;
 }
 
-// Fragment of rows r0 .. r0 + 31 (r0 a multiple of 32), half `s` of the step.
-template <int E, bool ACROSS>
-__device__ __forceinline__ void read_fragment(const uint8_t* tile, int r0, int s, int lane, u32x4 (&f)[2])
+// Fragment of T rows from r0 (a multiple of T), half `s` of the step: its vector t of T / 16.
+template <int E, bool ACROSS, int T>
+__device__ __forceinline__ u32x4 read_piece(const uint8_t* tile, int r0, int s, int t, int lane)
 {
+    constexpr int G = 64 / T;                                  // lane groups, each at another 16 bytes of k
+    const int group = lane / T;
     if constexpr (!ACROSS) {
-        const int r = r0 + (lane & 31);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-            f[t] = *reinterpret_cast<const u32x4*>(tile + tile_piece<E, false>(r, 4 * s + 2 * t + (lane >> 5)));
+        const int r = r0 + lane % T;
+        return *reinterpret_cast<const u32x4*>(tile + tile_piece<E, false>(r, 4 * s + G * t + group));
     } else if constexpr (E == 2) {
         // sixteen lanes fetch 4 k x 16 rows, 8 bytes each, and get one row's four k
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4* lds4;
         const int j = lane & 15;
-        const int k = 8 * (lane >> 5) + (j >> 2);
-        const int byte = ((r0 & 32) << 1) + ((lane & 16) << 1) + 8 * (j & 3);
-        const uint8_t* at = tile + (r0 >> 6) * 8192 + (32 * s + k) * 128 + (byte ^ ((k & 2) << 5));
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + t * 2048)));
-            const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + t * 2048 + 512)));
-            f[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-        }
+        const int k = 8 * group + (j >> 2);
+        const int byte = ((r0 & 48) << 1) + (T == 32 ? (lane & 16) << 1 : 0) + 8 * (j & 3);
+        const uint8_t* at = tile + (r0 >> 6) * 8192 + (32 * s + 16 * t + k) * 128 + (byte ^ ((k & 2) << 5) ^ ((k & 8) << 2));
+        const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)at));
+        const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 512)));
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
     } else {
-        const uint8_t* at = tile + (r0 >> 5) * 4096 + (16 * s + 4 * (lane >> 5)) * 128 + 4 * (lane & 31);
+        static_assert(T == 32, "fp32 blocks");
+        const uint8_t* at = tile + (r0 >> 5) * 4096 + (16 * s + 8 * t + 4 * group) * 128 + 4 * (lane & 31);
+        u32x4 f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[t][e] = *reinterpret_cast<const uint32_t*>(at + (8 * t + e) * 128);
+        for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const uint32_t*>(at + e * 128);
+        return f;
     }
+}
+
+template <int E, bool ACROSS>
+__device__ __forceinline__ void read_fragment(const uint8_t* tile, int r0, int s, int lane, u32x4 (&f)[2])
+{
+#pragma unroll
+    for (int t = 0; t < 2; ++t) f[t] = read_piece<E, ACROSS, 32>(tile, r0, s, t, lane);
 }
 
 // Lanes exchange data through LDS next: the wave's DS instructions execute in
@@ -64,25 +71,34 @@ __device__ __forceinline__ void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
-// Epilogue of one wave: its FM x FN blocks of 32 rows x 32 raw columns, first
-// row m0, first raw column j0.  acc holds columns along its registers, so a
+// Epilogue of one wave: its FM x FN blocks of T rows x T raw columns (T = 16 or
+// 32), first row m0, first raw column j0.  acc holds columns along its registers, so a
 // lane writes four columns of a row at once into the wave's own LDS stage and
 // then takes eight of a row from it: 16-byte accesses to every tensor, whole
 // 64- or 128-byte lines per row.  The caller has passed a barrier after the
 // last read of the operand tiles.
-template <class Out, int EPI, int FM, int FN>
-__device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, f32x16 (&acc)[FM][FN], int m0, int j0,
+template <class Out, int EPI, class Block, int FM, int FN>
+__device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, Block (&acc)[FM][FN], int m0, int j0,
                                             int split, int lane)
 {
-    constexpr int W = 32 * FN, PITCH = W + 4;
+    constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, W = T * FN, PITCH = W + 4, ROWS = T * FM;
+    static_assert(ROWS % 32 == 0, "32 rows at a time");
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < ROWS / 32; ++i) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (T == 32) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4*>(stage + (lane & 31) * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
-                    f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4*>(stage + (lane & 31) * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
+                        f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<f32x4*>(stage + (16 * h + (lane & 15)) * PITCH + 16 * j + 4 * (lane >> 4)) =
+                        acc[2 * i + h][j];
+            }
+        }
         wave_order();
         if (p.splits > 1) {
             constexpr int PER = W / 8;
