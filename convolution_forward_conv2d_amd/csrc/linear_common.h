@@ -189,6 +189,30 @@ enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2 };
 // whatever its tile.
 __host__ __device__ inline int gated_raw_columns(int n) { return (n + 15) / 16 * 32; }
 
+// Eight values; the branch is outside the loop: eight independent chains inside.
+template <bool EXACT> __device__ __forceinline__ void activate8(int act, float (&v)[8])
+{
+    switch (act) {
+    case ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_RELU, v[i]);
+        break;
+    case ACT_GELU:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_GELU, v[i]);
+        break;
+    case ACT_GELU_TANH:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_GELU_TANH, v[i]);
+        break;
+    case ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_SILU, v[i]);
+        break;
+    default: break;
+    }
+}
+
 // Eight finished columns n..n+7 of row m: v the raw sums (u the second product's).
 template <class Out, int EPI>
 __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, float (&v)[8], float (&u)[8])
@@ -228,25 +252,7 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, floa
     if constexpr (EPI == EPI_GATED) {
         if (p.pre2) store8(static_cast<Out*>(p.pre2) + (int64_t)m * p.ldp2 + n, nv, u);
     }
-    switch (p.act) {           // the branch outside the loop: eight independent chains inside
-    case ACT_RELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_RELU, v[i]);
-        break;
-    case ACT_GELU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_GELU, v[i]);
-        break;
-    case ACT_GELU_TANH:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_GELU_TANH, v[i]);
-        break;
-    case ACT_SILU:
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = act_value<EXACT>(ACT_SILU, v[i]);
-        break;
-    default: break;
-    }
+    activate8<EXACT>(p.act, v);
     if constexpr (EPI == EPI_GATED) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= u[i];

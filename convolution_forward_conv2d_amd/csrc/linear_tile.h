@@ -71,6 +71,105 @@ __device__ __forceinline__ void wave_order()
     __builtin_amdgcn_wave_barrier();
 }
 
+// The epilogue of 32 rows of W raw columns, all of which exist, from the wave's
+// stage.  A lane keeps its eight columns from pass to pass (with 96 columns four
+// lanes stay idle), so bias and column scales are loaded once per tile; a row's
+// scale comes from the lane that loaded it.  A residual is added in a pass of
+// its own, unrolled, so that its loads are in flight together: one load after
+// the other, as in the general form, costs a tile of 256 x 256 about 13 us.
+template <class Out, int EPI, int W> struct WholeRows {
+    static constexpr bool GATED = EPI == EPI_GATED, EXACT = sizeof(Out) == 4;
+    static constexpr int PER = GATED ? W / 16 : W / 8, ROWS = 64 / PER, PASSES = (32 + ROWS - 1) / ROWS, PITCH = W + 4;
+    static constexpr int PIECES = sizeof(Out) / 2;             // of 16 bytes, in eight values
+    struct Columns {
+        float bias[8], scale[8], scale2[8];
+    };
+    int row, n;                  // of the first pass
+    int at;                      // column in the stage
+    __device__ __forceinline__ WholeRows(int lane, int n0)
+    {
+        row = lane < ROWS * PER ? lane / PER : 32;             // past the last row: idle
+        const int g = lane % PER;
+        n = n0 + 8 * g;
+        at = GATED ? (g >> 1) * 32 + (g & 1) * 8 : 8 * g;      // group g: block g / 2, its half g % 2
+    }
+    __device__ __forceinline__ Columns columns(const ProductArgs& p) const
+    {
+        Columns c;
+        if (p.bias) load8(static_cast<const Out*>(p.bias) + n, 8, c.bias);
+        if (p.w_scale) load8(p.w_scale + n, 8, c.scale);
+        if (GATED && p.w2_scale) load8(p.w2_scale + n, 8, c.scale2);
+        return c;
+    }
+    __device__ __forceinline__ void load(const ProductArgs& p, u32x4 (&res)[PASSES][PIECES], int m0) const
+    {
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+            const int m = min(m0 + min(row + k * ROWS, 31), p.M - 1);
+            __builtin_memcpy(res[k], static_cast<const Out*>(p.residual) + (int64_t)m * p.ldr + n, 16 * PIECES);
+        }
+    }
+    __device__ __forceinline__ void finish(const ProductArgs& p, float* stage, const Columns& c,
+                                           const u32x4 (&res)[PASSES][PIECES], int m0, float row_scale) const
+    {
+        const bool adds = p.residual != nullptr;
+        const int rows = min(32, p.M - m0);
+        if (!adds || p.act != ACT_NONE || p.x_scale || p.bias || p.pre) {
+#pragma unroll 1
+            for (int r = row; r - row < PASSES * ROWS; r += ROWS) {
+                const float xs = __shfl(row_scale, r & 31);
+                if (r >= rows) continue;
+                float* s = stage + r * PITCH + at;
+                float v[8], u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = s[e];
+                    if constexpr (GATED) u[e] = s[16 + e];
+                }
+                if (p.x_scale) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] *= xs * c.scale[e];
+                        if constexpr (GATED) u[e] *= xs * c.scale2[e];
+                    }
+                }
+                if (!GATED && p.bias) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
+                }
+                if (p.pre) store8(static_cast<Out*>(p.pre) + (int64_t)(m0 + r) * p.ldp + n, 8, v);
+                if (GATED && p.pre2) store8(static_cast<Out*>(p.pre2) + (int64_t)(m0 + r) * p.ldp2 + n, 8, u);
+                activate8<EXACT>(p.act, v);
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= u[e];
+                }
+                if (adds) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = v[e];
+                } else {
+                    store8(static_cast<Out*>(p.y) + (int64_t)(m0 + r) * p.ldy + n, 8, v);
+                }
+            }
+        }
+        if (adds) {
+            wave_order();
+#pragma unroll
+            for (int k = 0; k < PASSES; ++k) {
+                const int r = row + k * ROWS;
+                if (r >= rows) continue;
+                const float* s = stage + r * PITCH + at;
+                Out x[8];
+                __builtin_memcpy(x, res[k], sizeof(x));
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = s[e] + to_f32(x[e]);
+                store8(static_cast<Out*>(p.y) + (int64_t)(m0 + r) * p.ldy + n, 8, v);
+            }
+        }
+    }
+};
+
 // Epilogue of one wave: its FM x FN blocks of T rows x T raw columns (T = 16 or
 // 32), first row m0, first raw column j0.  acc holds columns along its registers, so a
 // lane writes four columns of a row at once into the wave's own LDS stage and
@@ -83,6 +182,20 @@ __device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, 
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, W = T * FN, PITCH = W + 4, ROWS = T * FM;
     static_assert(ROWS % 32 == 0, "32 rows at a time");
+    // a linear or gated layer's whole tile takes its bias and scales once, and its residual 32 rows ahead
+    using Rows = WholeRows<Out, EPI, W>;
+    const bool whole = EPI != EPI_PLAIN && p.splits == 1 && (EPI == EPI_GATED ? (j0 + W) / 2 : j0 + W) <= p.N;
+    const Rows rows(lane, EPI == EPI_GATED ? j0 / 2 : j0);
+    typename Rows::Columns columns;
+    u32x4 residual[2][Rows::PASSES][sizeof(Out) / 2];
+    float row_scale[ROWS / 32];
+    if (whole) {
+        columns = rows.columns(p);
+        if (p.residual) rows.load(p, residual[0], m0);
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i)
+            row_scale[i] = p.x_scale ? p.x_scale[min(m0 + 32 * i + (lane & 31), p.M - 1)] : 1.0f;
+    }
 #pragma unroll
     for (int i = 0; i < ROWS / 32; ++i) {
 #pragma unroll
@@ -100,7 +213,10 @@ __device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, 
             }
         }
         wave_order();
-        if (p.splits > 1) {
+        if (whole) {
+            if (p.residual && i + 1 < ROWS / 32) rows.load(p, residual[(i + 1) & 1], m0 + 32 * i + 32);
+            rows.finish(p, stage, columns, residual[i & 1], m0 + 32 * i, row_scale[i]);
+        } else if (p.splits > 1) {
             constexpr int PER = W / 8;
 #pragma unroll 2
             for (int it = lane; it < 32 * PER; it += 64) {
