@@ -19,7 +19,7 @@ SOURCES = ["miconv.cpp", "conv_fwd_mfma.hip", "conv_fwd_halo.hip", "conv_fwd_hal
            "conv_bwd_filter_split.hip", "conv_bwd_data_phase.hip", "conv_fwd_rows.hip",
            "conv_bwd_data_subpixel.hip", "conv_bwd_filter_rows.hip", "conv_bwd_filter_cl.hip",
            "conv_bwd_data_taps.hip", "linear.cpp", "linear_any.hip", "linear_grad.hip", "rms_norm.hip",
-           "linear_fast_fwd.hip", "linear_fast_grad.hip", "linear_pack.hip"]
+           "linear_fast_fwd.hip", "linear_fast_grad.hip", "linear_pack.hip", "linear_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -180,6 +180,9 @@ enum class ProductType : int { F32, BF16, E4M3_BF16, E4M3_F32, E4M3_BF16_SHORT, 
 struct ProductArgs;
 // Any sizes, pitches and alignments (linear_any.hip); tile 64 or 128.
 hipError_t launch_product_any(Product kind, ProductType type, const ProductArgs& p, int tile, hipStream_t stream);
+// x W^T on at most FEW_ROWS rows (linear_few.hip).
+constexpr int FEW_ROWS = 32;
+hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, hipStream_t stream);
 // Aligned operands on large tiles (linear_fast_fwd.hip, linear_fast_grad.hip):
 // bf16, and e4m3 by its own instruction.
 enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T128x128, COUNT };

@@ -56,6 +56,7 @@ mic_status launched(hipError_t e) { return e == hipSuccess ? MIC_STATUS_SUCCESS 
 
 // How a product runs.
 struct Plan {
+    bool few;                // linear_few.hip
     bool fast;               // linear_fast.h, else linear_any.hip
     miconv::FastTile fast_tile;
     int tile;                // linear_any.hip's
@@ -84,15 +85,30 @@ Extent extent_of(Product kind, int m, int n, int k)
 }
 
 // The measured cost of a step (128 bytes of k) of each kernel's tile with every
-// CU busy, microseconds, and of a tile's start and epilogue; a launch; memory's
-// rate for the copies and partial sums.  Only their ratios decide.
-constexpr double kLaunchUs = 4.0, kBytesPerUs = 4.0e6;
+// CU busy, microseconds, and of a tile's start and end; a launch; memory's rate
+// for operands, copies and partial sums.  Only their ratios decide.  On
+// 4096 x 4096 outputs 256 x 256 takes 498 us of 9216 terms and 192 x 256, whose
+// 176 tiles leave no CU idle in the last round, 478; on 8192 x 8192 of 8192
+// terms, four rounds of either, 764 and 860.
+constexpr double kLaunchUs = 4.0, kBytesPerUs = 4.0e6, kReadPerUs = 4.5e6;
 struct TileCost {
     int bm, bn;
     double step, tile;
 };
-constexpr TileCost kFast[] = {{256, 256, 2.00, 3.0}, {256, 192, 1.38, 2.3}, {192, 256, 1.30, 2.3},
-                              {256, 128, 1.05, 1.6}, {128, 256, 1.05, 1.6}, {128, 128, 0.55, 1.0}};
+constexpr TileCost kFast[] = {{256, 256, 1.50, 3.0}, {256, 192, 1.12, 3.0}, {192, 256, 1.12, 3.0},
+                              {256, 128, 0.87, 2.5}, {128, 256, 0.93, 2.5}, {128, 128, 0.47, 2.5}};
+
+// linear_few.hip: its start, then memory's time for the weights or a CU's for its workgroups' weights and x, about
+// 37 KB a microsecond (a third of it where rows are not 16-byte aligned).  Measured, with the tiles' time behind it:
+// 16 rows of 1000 x 4096 9.7 us (13.2), of 2048 x 2048 gated 8.4 (12.4), 32 of 4096 x 9216 27.0 (25), of 4001 x 4093
+// 29.2 (20.3).
+double few_us(int num_cu, int m, int raw_n, bool gated, double row_bytes, bool aligned)
+{
+    const int columns = gated ? 32 : 16;
+    const double groups = std::max(1.0, (double)raw_n / columns / num_cu), rate = aligned ? 37.0e3 : 15.0e3;
+    const double x_rows = m <= 2 ? m : (m + 15) / 16 * 16;
+    return 2.5 + std::max(raw_n * row_bytes / kReadPerUs, groups * (columns + x_rows) * row_bytes / rate);
+}
 
 // The cheapest way through a product of m x n outputs and k_segments * k terms.
 // `aligned_a` / `aligned_b`: the operand's rows can be read 16 bytes at a time.
@@ -111,11 +127,19 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         return splits > 1 ? kLaunchUs + (double)m * raw_n * 4 * 2 * splits / kBytesPerUs : 0.0;
     };
     auto rounds = [&](int64_t t, int slots) { return (double)((t + slots - 1) / slots); };
+    const double b_bytes = (double)raw_n * k * k_segments * e, read_us = (b_bytes + (double)m * k * k_segments * e) / kReadPerUs;
     Plan best = {};
     best.us = 1e30;
-    auto consider = [&](Plan pl, int64_t t, int bn, int slots, double step, double tile) {
+    if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED)) {
+        best.few = true;
+        best.splits = 1;
+        best.us = few_us(num_cu, m, raw_n, kind == Product::GATED, (double)k * e, aligned_a && aligned_b);
+    }
+    auto consider = [&](Plan pl, int64_t t, int bm, int bn, int slots, double step, double tile) {
+        // weights that one or two row tiles read come from memory at its latency, two steps in flight
+        if (m <= 2 * bm) step = std::max(step, 0.9);
         for (int s = 1, most = most_splits(t); s <= most; ++s) {
-            const double us = rounds(t * s, slots) * ((steps + s - 1) / s * step + tile) + join_us(s) + pl.us;
+            const double us = std::max(rounds(t * s, slots) * ((steps + s - 1) / s * step + tile), read_us) + join_us(s) + pl.us + 1.5;
             if (us < best.us) {
                 best = pl;
                 best.splits = s;
@@ -129,9 +153,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const double slow = type == ProductType::F32 ? 4.0 : type == ProductType::BF16 ? 1.0 : 1.8;
     Plan any = {};
     any.tile = 128;
-    consider(any, tiles(128, 128), 128, 2 * num_cu, 1.45 * slow, 2.0);
+    consider(any, tiles(128, 128), 128, 128, 2 * num_cu, 1.45 * slow, 2.0);
     any.tile = 64;
-    consider(any, tiles(64, 64), 64, 4 * num_cu, 1.10 * slow, 1.5);
+    consider(any, tiles(64, 64), 64, 64, 4 * num_cu, 1.10 * slow, 1.5);
 
     const Extent x = extent_of(kind, m, n, k);
     const bool short_rows = (int64_t)std::max(x.a_cols, x.b_cols) * e < kMaxPitchBytes / 2 - 64;
@@ -154,7 +178,7 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         for (int i = 0; i < (int)miconv::FastTile::COUNT; ++i) {
             const TileCost& c = kFast[i];
             pl.fast_tile = (miconv::FastTile)i;
-            consider(pl, tiles(c.bm, c.bn), c.bn, num_cu, c.step, c.tile);
+            consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
         }
     }
     const int copies = kind == Product::GATED ? 2 : k_segments;
@@ -217,8 +241,9 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
     p.splits = pl.splits;
     p.part = reinterpret_cast<float*>(ws);
     p.part_ld = pl.part_ld;
-    hipError_t err = pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
-                             : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
+    hipError_t err = pl.few    ? miconv::launch_product_few(kind, type, p, h->stream)
+                     : pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
+                               : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
     if (err == hipSuccess && pl.splits > 1) err = miconv::launch_product_join(kind, type, p, h->stream);
     return launched(err);
 }

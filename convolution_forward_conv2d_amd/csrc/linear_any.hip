@@ -14,26 +14,6 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// The 16-byte piece at p of which the first nv elements exist.
-template <int E> __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int nv)
-{
-    u32x4 v = {0, 0, 0, 0};
-    if (nv >= 16 / E) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (nv > 0) {
-#pragma unroll
-        for (int i = 0; i < 16 / E; ++i)
-            if (i < nv) {
-                uint32_t x;
-                if constexpr (E == 4) x = *reinterpret_cast<const uint32_t*>(p + 4 * i);
-                else if constexpr (E == 2) x = *reinterpret_cast<const uint16_t*>(p + 2 * i);
-                else x = p[i];
-                v[i * E / 4] |= x << (8 * (i * E % 4));
-            }
-    }
-    return v;
-}
-
 // Raw B row j of a gated layer: the gate's or the other weights' row.
 __device__ __forceinline__ int gated_row(int j, bool& up)
 {

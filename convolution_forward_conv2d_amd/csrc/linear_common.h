@@ -62,6 +62,26 @@ template <class T> __device__ __forceinline__ void store8(T* p, int nv, const fl
     }
 }
 
+// The 16-byte piece at p of which the first nv elements exist.
+template <int E> __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int nv)
+{
+    u32x4 v = {0, 0, 0, 0};
+    if (nv >= 16 / E) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (nv > 0) {
+#pragma unroll
+        for (int i = 0; i < 16 / E; ++i)
+            if (i < nv) {
+                uint32_t x;
+                if constexpr (E == 4) x = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+                else if constexpr (E == 2) x = *reinterpret_cast<const uint16_t*>(p + 2 * i);
+                else x = p[i];
+                v[i * E / 4] |= x << (8 * (i * E % 4));
+            }
+    }
+    return v;
+}
+
 // ------------------------------------------------------------------ activations
 //
 // All in fp32.  e^x is 2^(x log2 e) on the hardware's exponential (about
@@ -295,6 +315,8 @@ struct MulBf16 {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, rows[0]),
                                                        __builtin_bit_cast(bf16x8, cols[0]), c, 0, 0, 0);
     }
+    // one vector a lane, of row l % 16, for 16 x 16 (the lane groups and a vector's elements walk k in one order)
+    __device__ static f32x4 mac16(u32x4 rows, u32x4 cols, f32x4 c) { return block(&rows, &cols, c); }
 };
 
 struct MulF32 {
@@ -308,6 +330,13 @@ struct MulF32 {
             for (int e = 0; e < 4; ++e)
                 c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(rows[t][e]), __uint_as_float(cols[t][e]), c,
                                                          0, 0, 0);
+        return c;
+    }
+    __device__ static f32x4 mac16(u32x4 rows, u32x4 cols, f32x4 c)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(rows[e]), __uint_as_float(cols[e]), c, 0, 0, 0);
         return c;
     }
 };
@@ -349,6 +378,14 @@ template <class OutT, bool SHORT> struct MulE4m3 {
             for (int e = 0; e < 4; e += 2)
                 c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(rows[t][e], rows[t][e + 1]),
                                                             widen(cols[t][e], cols[t][e + 1]), c, 0, 0, 0);
+        return c;
+    }
+    __device__ static f32x4 mac16(u32x4 rows, u32x4 cols, f32x4 c)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(rows[e], rows[e + 1]), widen(cols[e], cols[e + 1]), c,
+                                                        0, 0, 0);
         return c;
     }
 };

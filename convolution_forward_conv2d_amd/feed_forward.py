@@ -32,16 +32,26 @@ _bytes_of = {}
 def _handle(device):
     """This thread's library handle on `device`, bound to torch's current stream there."""
     dev = device.index
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("tensors are on %s, the current device is cuda:%d" % (device, torch.cuda.current_device()))
     handles = _local.__dict__
     h = handles.get(dev)
     if h is None:
-        h = handles[dev] = mic.mic_create()
-    status = mic.lib().mic_set_stream(h, torch._C._cuda_getCurrentRawStream(dev))
-    if status:
-        raise mic.MicError(status, "mic_set_stream")
-    return h
+        h = handles[dev] = [mic.mic_create(), None]
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if stream != h[1]:
+        status = mic.lib().mic_set_stream(h[0], stream)
+        if status:
+            raise mic.MicError(status, "mic_set_stream")
+        h[1] = stream
+    return h[0]
+
+
+def _empty(shape, like, dtype):
+    """torch.empty on like's device; the calls below cost a third of its dispatch."""
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _rows(t, cols, what):
@@ -105,8 +115,8 @@ def _weights(w, k, dtype, device, what):
     return _matrix(w, w.shape[0], k, dtype, device, what)
 
 
-def _workspace(fn, h, device, *sizes):
-    key = (fn, device.index, sizes)
+def _workspace(fn, h, like, *sizes):
+    key = (fn, like.device.index, sizes)
     n = _bytes_of.get(key)
     if n is None:
         if len(_bytes_of) > 4096:
@@ -114,7 +124,7 @@ def _workspace(fn, h, device, *sizes):
         n = _bytes_of[key] = getattr(mic, fn)(h, *sizes)
     if n == 0:
         return None, 0, 0
-    t = torch.empty(n, dtype=torch.uint8, device=device)
+    t = like.new_empty(n, dtype=torch.uint8)
     return t, t.data_ptr(), n
 
 
@@ -162,10 +172,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None):
         if residual.shape != x.shape:
             raise ValueError("residual has shape %s, x %s" % (tuple(residual.shape), tuple(x.shape)))
         ldr = _matrix(residual, rows, cols, dtype, device, "residual")
-        total = torch.empty(x.shape, dtype=dtype, device=device)
-    y = torch.empty(x.shape, dtype=out_dtype, device=device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-    scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=device) if out_dtype is E4M3 else None
+        total = _empty(x.shape, x, dtype)
+    y = _empty(x.shape, x, out_dtype)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    scale = torch.empty_like(rstd) if out_dtype is E4M3 else None
     _call("mic_rms_norm", h, _CODE[dtype], _CODE[out_dtype], rows, cols, eps, x.data_ptr(), ldx, _ptr(residual), ldr,
           wp, y.data_ptr(), cols, 0 if residual is None else total.data_ptr(), cols, rstd.data_ptr(), _ptr(scale))
     return RmsNorm(y, total, rstd, scale)
@@ -188,9 +198,9 @@ def rms_norm_backward(dy, sum, weight, rstd, dsum=None):
         raise ValueError("rstd must be %d packed fp32 values on %s" % (rows, device))
     ldd = 0 if dsum is None else _matrix(dsum, rows, cols, dtype, device, "dsum")
     h = _handle(device)
-    dx = torch.empty(dy.shape, dtype=dtype, device=device)
-    dweight = torch.empty(cols, dtype=dtype, device=device)
-    ws, wsp, wsn = _workspace("mic_rms_norm_backward_workspace", h, device, rows, cols)
+    dx = _empty(dy.shape, dy, dtype)
+    dweight = torch.empty_like(weight)
+    ws, wsp, wsn = _workspace("mic_rms_norm_backward_workspace", h, dy, rows, cols)
     _call("mic_rms_norm_backward", h, _CODE[dtype], rows, cols, dy.data_ptr(), lddy, sum.data_ptr(), lds, wp,
           rstd.data_ptr(), _ptr(dsum), ldd, dx.data_ptr(), cols, dweight.data_ptr(), wsp, wsn)
     return dx, dweight
@@ -248,9 +258,9 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
     ldr = 0 if residual is None else _matrix(residual, m, n, out_dtype, device, "residual")
     h = _handle(device)
     shape = x.shape[:-1] + (n,)
-    y = torch.empty(shape, dtype=out_dtype, device=device)
-    z = torch.empty(shape, dtype=out_dtype, device=device) if return_preact else None
-    wk, wkp, wkn = _workspace("mic_linear_forward_workspace", h, device, _CODE[dtype], m, n, k)
+    y = x.new_empty(shape, dtype=out_dtype)
+    z = torch.empty_like(y) if return_preact else None
+    wk, wkp, wkn = _workspace("mic_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
     _call("mic_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, bool(fast_sums), m, n, k, x.data_ptr(), ldx, w.data_ptr(), ldw,
           xs, ws, bp, _ptr(residual), ldr, y.data_ptr(), n, _ptr(z), n, wkp, wkn)
     return (y, z) if return_preact else y
@@ -274,10 +284,10 @@ def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
         raise ValueError("the gradient of activation %r needs preact" % activation)
     ldp = _matrix(preact, m, n, dtype, device, "preact") if act else 0
     h = _handle(device)
-    dx = torch.empty(x.shape, dtype=dtype, device=device)
-    dw = torch.empty((n, k), dtype=dtype, device=device)
-    dbias = torch.empty(n, dtype=dtype, device=device) if bias else None
-    wk, wkp, wkn = _workspace("mic_linear_backward_workspace", h, device, _CODE[dtype], m, n, k)
+    dx = _empty(x.shape, x, dtype)
+    dw = _empty(w.shape, w, dtype)
+    dbias = dy.new_empty(n) if bias else None
+    wk, wkp, wkn = _workspace("mic_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
     _call("mic_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
           ldw, _ptr(preact) if act else 0, ldp, dx.data_ptr(), k, dw.data_ptr(), k, _ptr(dbias), wkp, wkn)
     return dx, dw, dbias
@@ -304,10 +314,10 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
     us = 0 if w_up_scale is None else _vector(w_up_scale, n, torch.float32, device, "w_up_scale")
     h = _handle(device)
     shape = x.shape[:-1] + (n,)
-    y = torch.empty(shape, dtype=out_dtype, device=device)
-    gate = torch.empty(shape, dtype=out_dtype, device=device) if return_products else None
-    up = torch.empty(shape, dtype=out_dtype, device=device) if return_products else None
-    wk, wkp, wkn = _workspace("mic_gated_linear_forward_workspace", h, device, _CODE[dtype], m, n, k)
+    y = x.new_empty(shape, dtype=out_dtype)
+    gate = torch.empty_like(y) if return_products else None
+    up = torch.empty_like(y) if return_products else None
+    wk, wkp, wkn = _workspace("mic_gated_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
     _call("mic_gated_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, bool(fast_sums), m, n, k, x.data_ptr(), ldx,
           w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, xs, gs, us, y.data_ptr(), n, _ptr(gate), n, _ptr(up), n, wkp,
           wkn)
@@ -330,10 +340,10 @@ def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu"):
     ldgate = _matrix(gate, m, n, dtype, device, "gate")
     ldup = _matrix(up, m, n, dtype, device, "up")
     h = _handle(device)
-    dx = torch.empty(x.shape, dtype=dtype, device=device)
-    dwg = torch.empty((n, k), dtype=dtype, device=device)
-    dwu = torch.empty((n, k), dtype=dtype, device=device)
-    wk, wkp, wkn = _workspace("mic_gated_linear_backward_workspace", h, device, _CODE[dtype], m, n, k)
+    dx = _empty(x.shape, x, dtype)
+    dwg = _empty(w_gate.shape, w_gate, dtype)
+    dwu = _empty(w_up.shape, w_up, dtype)
+    wk, wkp, wkn = _workspace("mic_gated_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
     _call("mic_gated_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx,
           w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, gate.data_ptr(), ldgate, up.data_ptr(), ldup, dx.data_ptr(), k,
           dwg.data_ptr(), k, dwu.data_ptr(), k, wkp, wkn)
