@@ -182,12 +182,13 @@ struct ProductArgs;
 hipError_t launch_product_any(Product kind, ProductType type, const ProductArgs& p, int tile, hipStream_t stream);
 // x W^T on at most FEW_ROWS rows (linear_few.hip).
 constexpr int FEW_ROWS = 32;
-hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, hipStream_t stream);
+hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, int num_cu, hipStream_t stream);
 // Aligned operands on large tiles (linear_fast_fwd.hip, linear_fast_grad.hip):
-// bf16, and e4m3 by its own instruction.
+// bf16, fp32 (T128x128 only), and e4m3 by its own instruction.
 enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T128x128, COUNT };
 hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream);
-hipError_t launch_product_fast_grad(Product kind, const ProductArgs& p, FastTile tile, hipStream_t stream);
+hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
+                                    hipStream_t stream);
 // rows x bytes with any pitch into rows of `pitch` bytes (a multiple of 16), zeros behind each (linear_pack.hip).
 hipError_t launch_pack(const void* from, int64_t from_pitch, int rows, int64_t bytes, void* to, int64_t pitch,
                        hipStream_t stream);

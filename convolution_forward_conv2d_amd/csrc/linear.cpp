@@ -97,6 +97,7 @@ struct TileCost {
 };
 constexpr TileCost kFast[] = {{256, 256, 1.50, 3.0}, {256, 192, 1.12, 3.0}, {192, 256, 1.12, 3.0},
                               {256, 128, 0.87, 2.5}, {128, 256, 0.93, 2.5}, {128, 128, 0.47, 2.5}};
+constexpr double kF32Step = 1.9;                       // 128 x 128 in fp32
 
 // linear_few.hip: its start, then memory's time for the weights or a CU's for its workgroups' weights and x, about
 // 37 KB a microsecond (a third of it where rows are not 16-byte aligned).  Measured, with the tiles' time behind it:
@@ -160,7 +161,8 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const Extent x = extent_of(kind, m, n, k);
     const bool short_rows = (int64_t)std::max(x.a_cols, x.b_cols) * e < kMaxPitchBytes / 2 - 64;
     // two k segments are one matrix, laid out by the library and aligned
-    if ((type == ProductType::BF16 || type == ProductType::E4M3_BF16_SHORT || type == ProductType::E4M3_F32_SHORT)
+    const bool f32 = type == ProductType::F32;
+    if ((f32 || type == ProductType::BF16 || type == ProductType::E4M3_BF16_SHORT || type == ProductType::E4M3_F32_SHORT)
         && short_rows && (aligned_a || k_segments == 1)) {
         Plan pl = {};
         pl.fast = true;
@@ -178,7 +180,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         for (int i = 0; i < (int)miconv::FastTile::COUNT; ++i) {
             const TileCost& c = kFast[i];
             pl.fast_tile = (miconv::FastTile)i;
-            consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
+            if (!f32) consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
+            else if (pl.fast_tile == miconv::FastTile::T128x128)
+                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, kF32Step, c.tile);
         }
     }
     const int copies = kind == Product::GATED ? 2 : k_segments;
@@ -241,7 +245,7 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
     p.splits = pl.splits;
     p.part = reinterpret_cast<float*>(ws);
     p.part_ld = pl.part_ld;
-    hipError_t err = pl.few    ? miconv::launch_product_few(kind, type, p, h->stream)
+    hipError_t err = pl.few    ? miconv::launch_product_few(kind, type, p, h->num_cu, h->stream)
                      : pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
                                : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
     if (err == hipSuccess && pl.splits > 1) err = miconv::launch_product_join(kind, type, p, h->stream);

@@ -177,6 +177,7 @@ __global__ __launch_bounds__(256) void join_kernel(const ProductArgs p)
         const int m = (int)(it / per), n = (int)(it % per) * 8;
         const int raw = EPI == EPI_GATED ? (n >> 4) * 32 + (n & 15) : n;
         float v[8] = {}, u[8] = {};
+#pragma unroll 4                                               // loads of four parts in flight together
         for (int z = 0; z < p.splits; ++z) {
             const float* at = p.part + ((int64_t)z * p.M + m) * p.part_ld + raw;
 #pragma unroll

@@ -98,20 +98,23 @@ template <int E> __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, i
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896f); }
 __device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)); }
 
+// erfc(|z| / sqrt 2) / 2 by 7.1.26, and its bell e^(-z^2/2).
+__device__ __forceinline__ float normal_tail(float z, float& bell)
+{
+    bell = __builtin_amdgcn_exp2f(z * (z * -0.721347520444482f));
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.231641888f * fabsf(z));
+    return t * (0.127414796f + t * (-0.142248368f + t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f)))) * bell;
+}
+
 // (Phi(z), e^(-z^2/2)): the normal distribution function and its bell.
 template <bool EXACT> __device__ __forceinline__ void normal_cdf(float z, float& phi, float& bell)
 {
-    bell = fast_exp(-0.5f * z * z);
     if constexpr (EXACT) {
+        bell = fast_exp(-0.5f * z * z);
         phi = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
     } else {
-        const float x = fabsf(z) * 0.70710678118654752f;
-        const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-        const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f
-                           + t * (-1.453152027f + t * 1.061405429f))));
-        const float half = 0.5f * poly * bell;                 // erfc(|x|) / 2
-        phi = z >= 0.0f ? 1.0f - half : half;
-        if (z != z) phi = z;
+        const float half = normal_tail(z, bell);
+        phi = z >= 0.0f ? 1.0f - half : half;                  // a NaN is in half already
     }
 }
 
@@ -121,8 +124,13 @@ template <bool EXACT> __device__ __forceinline__ float act_value(int act, float 
     case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
     case ACT_GELU: {
         float phi, bell;
-        normal_cdf<EXACT>(z, phi, bell);
-        return z * phi;
+        if constexpr (EXACT) {
+            normal_cdf<EXACT>(z, phi, bell);
+            return z * phi;
+        }
+        // z Phi(z) = max(z, 0) - |z| tail(|z|); past 16 the tail is below 2^-180, and infinity times it no number
+        const float tail = normal_tail(z, bell);
+        return fmaxf(z, 0.0f) - fminf(fabsf(z), 16.0f) * tail;
     }
     case ACT_GELU_TANH:       // 0.5 z (1 + tanh(u)) = z * logistic(2 u)
         return z * logistic(1.59576912160573f * (z + 0.044715f * z * z * z));
@@ -149,7 +157,9 @@ template <bool EXACT> __device__ __forceinline__ void act_both(int act, float z,
     case ACT_GELU_TANH: {
         const float p = logistic(1.59576912160573f * (z + 0.044715f * z * z * z));
         value = z * p;
-        slope = p + value * (1.0f - p) * 1.59576912160573f * (1.0f + 0.134145f * z * z);
+        // past 64 p is 0 or 1 to the last bit, and z^2 may overflow
+        const float c = fminf(fmaxf(z, -64.0f), 64.0f);
+        slope = p + c * p * (1.0f - p) * 1.59576912160573f * (1.0f + 0.134145f * c * c);
         break;
     }
     case ACT_SILU: {
@@ -322,6 +332,9 @@ struct MulBf16 {
 struct MulF32 {
     static constexpr int E = 4;
     using Out = float;
+    using Block = f32x16;
+    static constexpr int T = 32;
+    __device__ static f32x16 block(const u32x4* rows, const u32x4* cols, f32x16 c) { return mfma(rows, cols, c); }
     __device__ static f32x16 mfma(const u32x4* rows, const u32x4* cols, f32x16 c)
     {
 #pragma unroll

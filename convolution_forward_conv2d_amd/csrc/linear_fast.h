@@ -73,7 +73,7 @@ template <int E, bool ACROSS, int R, bool GATED> struct Stream {
             left = (int64_t)(K - 1 - k) * ld + (int64_t)(rows - r0) * E - panel * 128;
             hop = 64 / LINES * 128;
             advance = ld * LINES;
-            piece = (lane & 7) ^ ((line & 2) << 1) ^ ((line & 8) >> 2);
+            piece = E == 2 ? (lane & 7) ^ ((line & 2) << 1) ^ ((line & 8) >> 2) : lane & 7;
         } else {
             int r = r0 + wave * 8;
             hop = 64 * (uint32_t)ld;

@@ -3,10 +3,17 @@
 
 namespace miconv {
 
-hipError_t launch_product_fast_grad(Product kind, const ProductArgs& p, FastTile tile, hipStream_t stream)
+template <class Mul> static hipError_t launch_kind(Product kind, const ProductArgs& p, FastTile tile, hipStream_t stream)
 {
-    return kind == Product::INPUT_GRAD ? launch_one<MulBf16, false, true, EPI_PLAIN>(p, tile, stream)
-                                       : launch_one<MulBf16, true, true, EPI_PLAIN>(p, tile, stream);
+    return kind == Product::INPUT_GRAD ? launch_one<Mul, false, true, EPI_PLAIN>(p, tile, stream)
+                                       : launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+}
+
+hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream)
+{
+    if (type == ProductType::BF16) return launch_kind<MulBf16>(kind, p, tile, stream);
+    if (type == ProductType::F32) return launch_kind<MulF32>(kind, p, tile, stream);
+    return hipErrorInvalidValue;                               // no gradients in e4m3
 }
 
 }  // namespace miconv

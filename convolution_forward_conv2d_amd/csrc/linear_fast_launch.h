@@ -21,7 +21,11 @@ hipError_t launch_tile(const ProductArgs& p, hipStream_t stream)
 template <class Mul, bool AACROSS, bool BACROSS, int EPI>
 hipError_t launch_one(const ProductArgs& p, FastTile tile, hipStream_t stream)
 {
-    switch (tile) {
+    if constexpr (Mul::E == 4) {
+        // fp32's matrix instructions take sixteen times bf16's time: the smallest tile already waits for nothing else
+        return tile == FastTile::T128x128 ? launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream)
+                                          : hipErrorInvalidValue;
+    } else switch (tile) {
     case FastTile::T256x256: return launch_tile<Mul, AACROSS, BACROSS, EPI, 256, 256, 2, 4>(p, stream);
     case FastTile::T256x192: return launch_tile<Mul, AACROSS, BACROSS, EPI, 256, 192, 4, 2>(p, stream);
     case FastTile::T192x256: return launch_tile<Mul, AACROSS, BACROSS, EPI, 192, 256, 2, 4>(p, stream);

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const ProductArg
     finish8<Out, EPI>(p, m, n0 + 8 * g, v, u);
 }
 
-template <class Mul, int EPI, int MB>
+template <class Mul, int EPI, int MB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_block_kernel(const ProductArgs p)
 {
     constexpr int E = Mul::E, NB = EPI == EPI_GATED ? 2 : 1;
@@ -256,39 +256,53 @@ __global__ __launch_bounds__(64 * WAVES) void linear_block_kernel(const ProductA
     }
     finish8<typename Mul::Out, EPI>(p, 16 * i + m, n0 + 8 * half, v, u);
 }
-template <class Mul, int EPI> hipError_t launch_rows(const ProductArgs& p, hipStream_t stream)
+// Eight waves a workgroup.  Where they take more than 128 registers (e4m3's widened operands, two row blocks) only one
+// such workgroup runs on a CU, so past one a CU they come in fours: gated 9216 x 4096 on 16 rows in e4m3 22.9 -> 20.9 us,
+// on 32 in bf16 49.9 -> 47.1; with fewer registers eight are faster (bf16 on four rows 33.5, in fours 34.7).
+template <class Mul, int EPI, int MB> void launch_blocks(const ProductArgs& p, int num_cu, hipStream_t stream)
+{
+    const int grid = (p.N + 15) / 16;
+    if constexpr (Mul::E == 1 || MB == 2)
+        if (grid > num_cu) {
+            linear_block_kernel<Mul, EPI, MB, 4><<<grid, 256, 0, stream>>>(p);
+            return;
+        }
+    linear_block_kernel<Mul, EPI, MB, 8><<<grid, 512, 0, stream>>>(p);
+}
+
+template <class Mul, int EPI> hipError_t launch_rows(const ProductArgs& p, int num_cu, hipStream_t stream)
 {
     using Out = typename Mul::Out;
     constexpr int E = Mul::E, COLS = EPI == EPI_GATED ? WAVES : 2 * WAVES;
-    const int rows_grid = (p.N + COLS - 1) / COLS, block_grid = (p.N + 15) / 16;
+    const int rows_grid = (p.N + COLS - 1) / COLS;
     // e4m3 doubles the vector work of a byte: 9216 x 4096 on two rows takes 15.8 us there, 12.2 in blocks
     if (p.M <= 1) linear_few_kernel<E, Out, EPI, 1><<<rows_grid, 64 * WAVES, 0, stream>>>(p);
     else if (E > 1 && p.M <= 2) linear_few_kernel<E, Out, EPI, 2><<<rows_grid, 64 * WAVES, 0, stream>>>(p);
-    else if (p.M <= 16) linear_block_kernel<Mul, EPI, 1><<<block_grid, 64 * WAVES, 0, stream>>>(p);
-    else if (p.M <= FEW_ROWS) linear_block_kernel<Mul, EPI, 2><<<block_grid, 64 * WAVES, 0, stream>>>(p);
+    else if (p.M <= 16) launch_blocks<Mul, EPI, 1>(p, num_cu, stream);
+    else if (p.M <= FEW_ROWS) launch_blocks<Mul, EPI, 2>(p, num_cu, stream);
     else return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
-template <class Mul> hipError_t launch_kind(Product kind, const ProductArgs& p, hipStream_t stream)
+template <class Mul> hipError_t launch_kind(Product kind, const ProductArgs& p, int num_cu, hipStream_t stream)
 {
-    if (kind == Product::FORWARD) return launch_rows<Mul, EPI_LINEAR>(p, stream);
-    if (kind == Product::GATED) return launch_rows<Mul, EPI_GATED>(p, stream);
+    if (kind == Product::FORWARD) return launch_rows<Mul, EPI_LINEAR>(p, num_cu, stream);
+    if (kind == Product::GATED) return launch_rows<Mul, EPI_GATED>(p, num_cu, stream);
     return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, hipStream_t stream)
+hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, int num_cu, hipStream_t stream)
 {
     switch (type) {
-    case ProductType::BF16: return launch_kind<MulBf16>(kind, p, stream);
-    case ProductType::F32: return launch_kind<MulF32>(kind, p, stream);
+    case ProductType::BF16: return launch_kind<MulBf16>(kind, p, num_cu, stream);
+    case ProductType::F32: return launch_kind<MulF32>(kind, p, num_cu, stream);
     // memory is the bound: the e4m3 instruction's short sums would gain nothing
     case ProductType::E4M3_BF16:
-    case ProductType::E4M3_BF16_SHORT: return launch_kind<MulE4m3<Bf16, false>>(kind, p, stream);
+    case ProductType::E4M3_BF16_SHORT: return launch_kind<MulE4m3<Bf16, false>>(kind, p, num_cu, stream);
     case ProductType::E4M3_F32:
-    case ProductType::E4M3_F32_SHORT: return launch_kind<MulE4m3<float, false>>(kind, p, stream);
+    case ProductType::E4M3_F32_SHORT: return launch_kind<MulE4m3<float, false>>(kind, p, num_cu, stream);
     }
     return hipErrorInvalidValue;
 }

@@ -47,12 +47,13 @@ template <int WAVES> __device__ __forceinline__ float block_max(float v, float* 
     return s;
 }
 
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, int nv, const float (&v)[8], float inv)
+// y / scale as y * inv * shift: 1 / scale overflows below 2^-128, and a zero times that is no number.
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int nv, const float (&v)[8], float inv, float shift)
 {
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        t[i] = v[i] * inv;
+        t[i] = v[i] * shift * inv;
         t[i] = t[i] != t[i] ? t[i] : fminf(fmaxf(t[i], -E4M3_MAX), E4M3_MAX);
     }
     uint32_t w[2];
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(64 * WAVES) void rms_norm_kernel(const NormArgs p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * g[i];
     };
-    float inv = 1.0f;
+    float inv = 1.0f, shift = 1.0f;
     if constexpr (E4M3) {
         if constexpr (LOOP)
             for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
@@ -153,12 +154,13 @@ __global__ __launch_bounds__(64 * WAVES) void rms_norm_kernel(const NormArgs p)
         most = block_max<WAVES>(most, part[1]);
         // a row of zeros (or one too small for a scale) keeps the scale 1
         const float scale = most / E4M3_MAX > 0.0f ? most / E4M3_MAX : 1.0f;
-        inv = 1.0f / scale;
+        shift = scale < 0x1p-100f ? 0x1p+64f : 1.0f;
+        inv = 1.0f / (scale * shift);
         if (threadIdx.x == 0) p.scale[row] = scale;
     }
     auto put = [&](int c, const float (&v)[8]) {
         if constexpr (E4M3)
-            store8_e4m3(static_cast<uint8_t*>(p.y) + row * p.ldy + c, p.cols - c, v, inv);
+            store8_e4m3(static_cast<uint8_t*>(p.y) + row * p.ldy + c, p.cols - c, v, inv, shift);
         else
             store8(static_cast<T*>(p.y) + row * p.ldy + c, p.cols - c, v);
     };
