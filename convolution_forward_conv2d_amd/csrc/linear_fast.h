@@ -35,12 +35,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // 16 bytes a lane from the descriptor's memory at `offset` into LDS at `to` + 16 * lane; past the descriptor's end:
 // zeros.  In assembly because the compiler waits for every load into LDS before each transposing LDS read that follows,
 // whatever the two touch (the gradients' products ran at half speed); the kernel's own waits (landed) order them.
-// Nothing arrives in a register, and the inputs are read when the instruction issues; the no-ops cover the five states
-// that a vector-written scalar would need before it.  m0 is a register the compiler only ever sets itself right before
-// an instruction that takes it, and nothing else here does.
+// Nothing arrives in a register, and the inputs are read when the instruction issues.  m0 is a register the compiler only
+// ever sets itself right before an instruction that takes it, and nothing else here does; the no-op is the state it needs.
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t offset, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(to)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(to)
                  : "memory");
 }
 
@@ -100,6 +99,7 @@ template <int E, bool ACROSS, int R, bool GATED> struct Stream {
         const int records = (int)(left < 0 || !some ? 0 : left > 0x7fffff00 ? 0x7fffff00 : left);
         const uint64_t from = reinterpret_cast<uint64_t>(base);
         rsrc = i32x4{(int)from, (int)(from >> 32) & 0xffff, records, 0x00020000};
+        asm volatile("s_nop 4" : "+s"(rsrc));                  // the states a vector-written scalar would need before a load
         at = off;
         // a row's end is not the operand's: pieces past K take an offset no descriptor reaches (the host keeps pitches
         // below 4 MB, so offsets within a tile stay below 2^30 and the sum does not wrap)
@@ -199,9 +199,10 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Prod
         if (i < 0) fb[s][i + FN][t] = read_piece<E, BACROSS, T>(tb, wn + T * (i + FN), s, t, lane);
         else fa[s][i][t] = read_piece<E, AACROSS, T>(ta, wm + T * i, s, t, lane);
     };
-    // One half step: its products, with the next half's reads and one operand's loads between them.
+    // One half step: its products, with the next half's reads and one operand's loads between them, and late in it the
+    // other operand's descriptor for the half after: in front of that half's products it held up both waves of a SIMD.
     constexpr int PRODUCTS = FM * FN;
-    auto half = [&](int s, const uint8_t* ta, const uint8_t* tb, auto& stream, uint8_t* into) {
+    auto half = [&](int s, const uint8_t* ta, const uint8_t* tb, auto& stream, uint8_t* into, auto&& turn) {
         constexpr int LOADS = std::remove_reference_t<decltype(stream)>::N;
 #pragma unroll
         for (int n = 0; n < PRODUCTS; ++n) {
@@ -215,6 +216,7 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Prod
 #pragma unroll
             for (int l = 0; l < LOADS; ++l)
                 if (l * PRODUCTS / (2 * LOADS) == n) stream.issue(into, wave, l);
+            if (n == PRODUCTS * 3 / 4) turn();
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -235,12 +237,11 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Prod
         for (int q = 0; q < READS; ++q) read(smem, b_tiles, 0, q);
         int a0 = 0, a1 = A_TILE, a2 = 2 * A_TILE;              // A of steps t, t + 1, t + 2
         int b0 = 0, b1 = B_TILE;
+        turn_a();
         for (int t = first; t < last; ++t) {
-            turn_a();
-            half(0, smem + a0, b_tiles + b0, sa, smem + a2);
+            half(0, smem + a0, b_tiles + b0, sa, smem + a2, turn_b);
             landed<LA>();
-            turn_b();
-            half(1, smem + a1, b_tiles + b1, sb, b_tiles + b0);
+            half(1, smem + a1, b_tiles + b1, sb, b_tiles + b0, turn_a);
             const int a = a0;
             a0 = a1, a1 = a2, a2 = a;
             b0 ^= B_TILE, b1 ^= B_TILE;

@@ -27,6 +27,7 @@ which rms_norm_backward takes; scale, fp32 per row, where y is e4m3 (else None).
 
 _local = threading.local()
 _bytes_of = {}
+_fns = {}
 
 
 def _handle(device):
@@ -55,8 +56,11 @@ def _empty(shape, like, dtype):
 
 
 def _rows(t, cols, what):
-    """t as (rows, cols, row pitch in elements), or why it cannot be read as one matrix."""
-    shape, strides = t.shape, t.stride()
+    """t as (rows of `cols`, row pitch in elements), or why it cannot be read as one matrix."""
+    shape = t.shape
+    if len(shape) == 2 and shape[1] == cols and t.is_contiguous():
+        return shape[0], cols
+    strides = t.stride()
     if not shape or shape[-1] != cols:
         raise ValueError("%s has shape %s, expected (..., %d)" % (what, tuple(shape), cols))
     if cols > 1 and strides[-1] != 1 and t.numel():
@@ -82,7 +86,7 @@ def _rows(t, cols, what):
 
 def _matrix(t, rows, cols, dtype, device, what):
     """Pitch of t, checked to be rows x cols of dtype on device."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
@@ -93,11 +97,11 @@ def _matrix(t, rows, cols, dtype, device, what):
 
 
 def _vector(t, size, dtype, device, what):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s is on %s, not on %s" % (what, t.device, device))
-    if tuple(t.shape) != (size,) or not (t.is_contiguous() or size < 2):
+    if t.shape != (size,) or not (t.is_contiguous() or size < 2):
         raise ValueError("%s must be a packed vector of %d, got %s" % (what, size, tuple(t.shape)))
     return t.data_ptr()
 
@@ -129,7 +133,10 @@ def _workspace(fn, h, like, *sizes):
 
 
 def _call(name, *args):
-    status = getattr(mic.lib(), name)(*args)
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(mic.lib(), name)
+    status = fn(*args)
     if status:
         raise mic.MicError(status, name)
 
