@@ -182,6 +182,9 @@ struct ProductArgs;
 hipError_t launch_product_any(Product kind, ProductType type, const ProductArgs& p, int tile, hipStream_t stream);
 // x W^T on at most FEW_ROWS rows (linear_few.hip).
 constexpr int FEW_ROWS = 32;
+// Of these, on the vector units.  e4m3 doubles the vector work of a byte: 9216 x 4096 on two rows takes 15.8 us there,
+// 12.2 on the matrix instructions.
+constexpr int vector_rows(int element_bytes) { return element_bytes == 1 ? 1 : 2; }
 hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, int num_cu, hipStream_t stream);
 // Aligned operands on large tiles (linear_fast_fwd.hip, linear_fast_grad.hip):
 // bf16, fp32 (T128x128 only), and e4m3 by its own instruction.

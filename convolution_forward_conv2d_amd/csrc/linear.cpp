@@ -99,7 +99,7 @@ constexpr TileCost kFast[] = {{256, 256, 1.50, 3.0}, {256, 192, 1.12, 3.0}, {192
                               {256, 128, 0.87, 2.5}, {128, 256, 0.93, 2.5}, {128, 128, 0.47, 2.5}};
 constexpr double kF32Step = 1.9;                       // 128 x 128 in fp32
 
-// linear_few.hip: its start, then memory's time for the weights or a CU's for its workgroups' weights and x, about
+// linear_few.hip's blocks: their start, then memory's time for the weights or a CU's for its workgroups' weights and x, about
 // 37 KB a microsecond (a third of it where rows are not 16-byte aligned).  Measured, with the tiles' time behind it:
 // 16 rows of 1000 x 4096 9.7 us (13.2), of 2048 x 2048 gated 8.4 (12.4), 32 of 4096 x 9216 27.0 (25), of 4001 x 4093
 // 29.2 (20.3).
@@ -107,7 +107,7 @@ double few_us(int num_cu, int m, int raw_n, bool gated, double row_bytes, bool a
 {
     const int columns = gated ? 32 : 16;
     const double groups = std::max(1.0, (double)raw_n / columns / num_cu), rate = aligned ? 37.0e3 : 15.0e3;
-    const double x_rows = m <= 2 ? m : (m + 15) / 16 * 16;
+    const double x_rows = (m + 15) / 16 * 16;
     return 2.5 + std::max(raw_n * row_bytes / kReadPerUs, groups * (columns + x_rows) * row_bytes / rate);
 }
 
@@ -134,6 +134,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED)) {
         best.few = true;
         best.splits = 1;
+        // one or two rows on the vector units: faster at every size and alignment measured (4001 x 4093, rows of odd
+        // lengths, 11.4 us against 22.0)
+        if (m <= miconv::vector_rows(e)) return best;
         best.us = few_us(num_cu, m, raw_n, kind == Product::GATED, (double)k * e, aligned_a && aligned_b);
     }
     auto consider = [&](Plan pl, int64_t t, int bm, int bn, int slots, double step, double tile) {

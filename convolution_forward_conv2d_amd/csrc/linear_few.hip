@@ -275,9 +275,8 @@ template <class Mul, int EPI> hipError_t launch_rows(const ProductArgs& p, int n
     using Out = typename Mul::Out;
     constexpr int E = Mul::E, COLS = EPI == EPI_GATED ? WAVES : 2 * WAVES;
     const int rows_grid = (p.N + COLS - 1) / COLS;
-    // e4m3 doubles the vector work of a byte: 9216 x 4096 on two rows takes 15.8 us there, 12.2 in blocks
     if (p.M <= 1) linear_few_kernel<E, Out, EPI, 1><<<rows_grid, 64 * WAVES, 0, stream>>>(p);
-    else if (E > 1 && p.M <= 2) linear_few_kernel<E, Out, EPI, 2><<<rows_grid, 64 * WAVES, 0, stream>>>(p);
+    else if (p.M <= vector_rows(E)) linear_few_kernel<E, Out, EPI, vector_rows(E)><<<rows_grid, 64 * WAVES, 0, stream>>>(p);
     else if (p.M <= 16) launch_blocks<Mul, EPI, 1>(p, num_cu, stream);
     else if (p.M <= FEW_ROWS) launch_blocks<Mul, EPI, 2>(p, num_cu, stream);
     else return hipErrorInvalidValue;
