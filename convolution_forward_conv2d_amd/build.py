@@ -1,16 +1,19 @@
-"""Build libmiconv.so in-tree with hipcc for gfx950 (no GPU needed to build).
+"""Build libmiconv.so in-tree with hipcc for gfx950 (no GPU needed to build),
+and _native.so, the torch binding of the feed-forward operators, with g++.
 
     python -m convolution_forward_conv2d_amd.build [--verbose]
 """
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmiconv.so")
+NATIVE = os.path.join(PKG, "_native.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["miconv.cpp", "conv_fwd_mfma.hip", "conv_fwd_halo.hip", "conv_fwd_halo_bf16.hip",
@@ -51,16 +54,47 @@ def _compile(src, verbose):
     return obj
 
 
+def _compile_binding(verbose):
+    """binding.cpp, host code against torch's headers."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "binding.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp:\n%s" % proc.stderr)
+    if proc.stderr.strip() and verbose:
+        print(proc.stderr, flush=True)
+    return obj, os.path.join(root, "lib")
+
+
 def build(verbose=False):
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(_compile_binding, verbose)
         objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
+        obj, torch_lib = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True, capture_output=not verbose)
     os.replace(tmp, LIB)
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-lmiconv", "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True, capture_output=not verbose)
+    os.replace(tmp, NATIVE)
     return LIB
 
 

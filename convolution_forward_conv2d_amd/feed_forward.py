@@ -4,7 +4,9 @@
 Argument marshalling only, as for the convolutions: every step runs in the
 HIP kernels of ``libmiconv.so``, on torch's current stream of the tensors'
 device.  Outputs and workspaces are torch allocations on that stream, so the
-calls may be captured into graphs.
+calls may be captured into graphs.  Contiguous arguments that fit each other
+pass through ``_native.so`` (csrc/binding.cpp), which takes half of Python's
+time over a small call; all others, and wrong ones, through the checks here.
 
 Activations ``x`` have any leading dimensions before their features; weights
 are ``(out_features, in_features)``.  Features must be consecutive in memory
@@ -25,9 +27,18 @@ RmsNorm = collections.namedtuple("RmsNorm", ["y", "sum", "rstd", "scale"])
 RmsNorm.__doc__ = """rms_norm's results: y; sum = x + residual (x itself without a residual) and rstd, fp32 per row,
 which rms_norm_backward takes; scale, fp32 per row, where y is e4m3 (else None)."""
 
+_native = None
 _local = threading.local()
 _bytes_of = {}
 _fns = {}
+
+
+def _load():
+    global _native
+    mic.lib()                                  # says what to do where nothing is built
+    from . import _native as module
+    _native = module
+    return module
 
 
 def _handle(device):
@@ -161,6 +172,11 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None):
     torch.float8_e4m3fn with a scale per row (y * scale is the value).
     Returns RmsNorm(y, sum, rstd, scale).
     """
+    e4m3 = out_dtype is E4M3
+    if e4m3 or out_dtype is None or out_dtype is x.dtype:
+        r = (_native or _load()).rms_norm(x, weight, residual, eps, e4m3)
+        if r is not None:
+            return RmsNorm(*r)
     _gpu(x, "x", (torch.float32, torch.bfloat16))
     dtype, device = x.dtype, x.device
     out_dtype = dtype if out_dtype is None else out_dtype
@@ -193,6 +209,9 @@ def rms_norm_backward(dy, sum, weight, rstd, dsum=None):
 
     dsum: the gradient that reaches sum past the norm (added to dx).
     """
+    r = (_native or _load()).rms_norm_backward(dy, sum, weight, rstd, dsum)
+    if r is not None:
+        return r
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     dtype, device = dy.dtype, dy.device
     cols = dy.shape[-1] if dy.dim() else 0
@@ -214,6 +233,15 @@ def rms_norm_backward(dy, sum, weight, rstd, dsum=None):
 
 
 # ---------------------------------------------------------------- layers
+
+def _wide(x, out_dtype):
+    """Whether an e4m3 layer's outputs are fp32; None where out_dtype does not go with x."""
+    if out_dtype is None or out_dtype is x.dtype:
+        return None if out_dtype is E4M3 else False
+    if x.dtype is E4M3 and out_dtype in (torch.bfloat16, torch.float32):
+        return out_dtype is torch.float32
+    return None
+
 
 def _layer_types(x, out_dtype, scales):
     """The output type of a layer on x, with its scales checked to be there or not."""
@@ -253,6 +281,11 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
     twice the rate but in sums shorter than fp32 (off by up to 2^-11 of the
     largest of 64 products); only e4m3 operands have that choice.
     """
+    act, wide = mic.ACTIVATIONS.get(activation), _wide(x, out_dtype)
+    if act is not None and wide is not None:
+        r = (_native or _load()).linear(x, w, bias, residual, act, x_scale, w_scale, wide, return_preact, fast_sums)
+        if r is not None:
+            return r if return_preact else r[0]
     out_dtype = _layer_types(x, out_dtype, (x_scale, w_scale))
     act, dtype, device = _act(activation), x.dtype, x.device
     k = x.shape[-1] if x.dim() else 0
@@ -278,6 +311,11 @@ def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
 
     dbias is None unless bias is true.  The residual's gradient is dy.
     """
+    act = mic.ACTIVATIONS.get(activation)
+    if act is not None:
+        r = (_native or _load()).linear_backward(dy, x, w, preact, act, bias)
+        if r is not None:
+            return r
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     act, dtype, device = _act(activation), dy.dtype, dy.device
     n = dy.shape[-1] if dy.dim() else 0
@@ -307,6 +345,12 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
     return_products: (y, gate, up) with the two products, for
     gated_linear_backward.
     """
+    act, wide = mic.ACTIVATIONS.get(activation), _wide(x, out_dtype)
+    if act is not None and wide is not None:
+        r = (_native or _load()).gated_linear(x, w_gate, w_up, act, x_scale, w_gate_scale, w_up_scale, wide,
+                                              return_products, fast_sums)
+        if r is not None:
+            return r if return_products else r[0]
     out_dtype = _layer_types(x, out_dtype, (x_scale, w_gate_scale, w_up_scale))
     act, dtype, device = _act(activation), x.dtype, x.device
     k = x.shape[-1] if x.dim() else 0
@@ -333,6 +377,11 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
 
 def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu"):
     """(dx, dw_gate, dw_up) of gated_linear, from its inputs and two products."""
+    act = mic.ACTIVATIONS.get(activation)
+    if act is not None:
+        r = (_native or _load()).gated_linear_backward(dy, x, w_gate, w_up, gate, up, act)
+        if r is not None:
+            return r
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     act, dtype, device = _act(activation), dy.dtype, dy.device
     n = dy.shape[-1] if dy.dim() else 0
