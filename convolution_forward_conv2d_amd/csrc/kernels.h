@@ -192,9 +192,15 @@ enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T1
 hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream);
 hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
-// rows x bytes with any pitch into rows of `pitch` bytes (a multiple of 16), zeros behind each (linear_pack.hip).
-hipError_t launch_pack(const void* from, int64_t from_pitch, int rows, int64_t bytes, void* to, int64_t pitch,
-                       hipStream_t stream);
+// Rows of `bytes` bytes at any pitch into rows of `to_pitch` (a multiple of 16), zeros behind each (linear_pack.hip).
+constexpr int PACK_JOBS = 3;
+struct PackJob {
+    const uint8_t* from;
+    int64_t from_pitch, rows, bytes;
+    uint8_t* to;
+    int64_t to_pitch;
+};
+hipError_t launch_pack(const PackJob* jobs, int count, hipStream_t stream);
 // Joins p.splits partial products and finishes them.
 hipError_t launch_product_join(Product kind, ProductType type, const ProductArgs& p, hipStream_t stream);
 

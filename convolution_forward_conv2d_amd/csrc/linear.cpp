@@ -172,14 +172,15 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         if (!aligned_a) {
             pl.pack_a = align_up((int64_t)x.a_cols * e, 16);
             pl.a_bytes = (size_t)align_up(pl.pack_a * x.a_rows, 256);
-            pl.us += kLaunchUs + 2.0 * pl.a_bytes / kBytesPerUs;
+            pl.us += 2.0 * pl.a_bytes / kBytesPerUs;
         }
         if (!aligned_b) {
             const int copies = kind == Product::GATED ? 2 : k_segments;
             pl.pack_b = align_up((int64_t)x.b_cols * e, 16);
             pl.b_bytes = (size_t)align_up(pl.pack_b * x.b_rows, 256);
-            pl.us += copies * (kLaunchUs + 2.0 * pl.b_bytes / kBytesPerUs);
+            pl.us += copies * 2.0 * pl.b_bytes / kBytesPerUs;
         }
+        if (pl.pack_a || pl.pack_b) pl.us += kLaunchUs;
         for (int i = 0; i < (int)miconv::FastTile::COUNT; ++i) {
             const TileCost& c = kFast[i];
             pl.fast_tile = (miconv::FastTile)i;
@@ -227,24 +228,23 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
     if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Extent x = extent_of(kind, p.M, p.N, p.K);
+    miconv::PackJob jobs[miconv::PACK_JOBS];
+    int packs = 0;
+    auto pack = [&](const uint8_t*& from, int64_t& ld, int64_t rows, int64_t bytes, int64_t pitch, size_t size) {
+        jobs[packs++] = {from, ld, rows, bytes, ws, pitch};
+        from = ws, ld = pitch;
+        ws += size;
+    };
     if (pl.pack_a) {
-        MIC_TRY(launched(miconv::launch_pack(p.a, p.lda, x.a_rows, (int64_t)x.a_cols * e, ws, pl.pack_a, h->stream)));
-        p.a = ws, p.lda = pl.pack_a;
+        pack(p.a, p.lda, x.a_rows, (int64_t)x.a_cols * e, pl.pack_a, pl.a_bytes);
         if (a_across) p.a_rows = (int)(pl.pack_a / e);
-        ws += pl.a_bytes;
     }
     if (pl.pack_b) {
-        const int64_t row = (int64_t)x.b_cols * e;
-        MIC_TRY(launched(miconv::launch_pack(p.b, p.ldb, x.b_rows, row, ws, pl.pack_b, h->stream)));
-        p.b = ws, p.ldb = pl.pack_b;
-        ws += pl.b_bytes;
-        if (two_b) {
-            MIC_TRY(launched(miconv::launch_pack(p.b2, p.ldb2, x.b_rows, row, ws, pl.pack_b, h->stream)));
-            p.b2 = ws, p.ldb2 = pl.pack_b;
-            ws += pl.b_bytes;
-        }
+        pack(p.b, p.ldb, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
+        if (two_b) pack(p.b2, p.ldb2, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
         if (b_across) p.b_rows = (int)(pl.pack_b / e);
     }
+    if (packs) MIC_TRY(launched(miconv::launch_pack(jobs, packs, h->stream)));
     p.splits = pl.splits;
     p.part = reinterpret_cast<float*>(ws);
     p.part_ld = pl.part_ld;

@@ -99,10 +99,10 @@ __global__ __launch_bounds__(1024) void column_join_kernel(const float* partial,
 
 int slope_row_groups(int rows, int cols)
 {
-    // enough blocks for eight to a CU; a group has at least four rows a lane
+    // enough blocks for eight to a CU, down to one row a lane: rows one after another wait for memory each
     const int wide = cols > 0 ? (cols + COLS * 8 - 1) / (COLS * 8) : 1;
     const int want = (2048 + wide - 1) / wide;
-    const int most = (rows + 4 * LANES - 1) / (4 * LANES);
+    const int most = (rows + LANES - 1) / LANES;
     return want < most ? want : (most > 1 ? most : 1);
 }
 
