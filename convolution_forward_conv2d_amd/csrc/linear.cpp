@@ -86,10 +86,10 @@ Extent extent_of(Product kind, int m, int n, int k)
 
 // The measured cost of a step (128 bytes of k) of each kernel's tile with every
 // CU busy, microseconds, and of a tile's start and end; a launch; memory's rate
-// for operands, copies and partial sums.  Only their ratios decide.  On
-// 4096 x 4096 outputs 256 x 256 takes 498 us of 9216 terms and 192 x 256, whose
-// 176 tiles leave no CU idle in the last round, 478; on 8192 x 8192 of 8192
-// terms, four rounds of either, 764 and 860.
+// for operands, copies and partial sums.  Only their ratios decide: 8192 x 8192
+// outputs of 8192 terms take 754 us in four rounds of 256 x 256 and 859 in 5.4
+// of 256 x 192; 4096 x 9216 of 4096 terms, 2.25 rounds of the one and exactly
+// three of the other, 311 and 258.
 constexpr double kLaunchUs = 4.0, kBytesPerUs = 4.0e6, kReadPerUs = 4.5e6;
 struct TileCost {
     int bm, bn;

@@ -18,6 +18,13 @@
 // 256 x 256), and over both halves they use at most half of that rate.  A load
 // of A has two halves to arrive after its own, one of B one and a half (a half:
 // 1024 cycles at 256 x 256).
+//
+// What bounds it is power: bf16 8192^3 takes 754 us (1458 TFLOP/s) with the
+// matrix units busy 70% of the cycles at 1.8 GHz of 2.4, and 605 us on zeros.
+// So what moves fewer bits wins: the 16 x 16 x 32 instruction, whose blocks'
+// sums pass through the registers half as often for the same work as 32 x 32 x
+// 16's, took 846 us to 778.  fp32 (128 x 128 only, two workgroups a CU) is bound
+// by its matrix instructions: 119 TFLOP/s of 157 at 4096^3.
 #pragma once
 
 #include <type_traits>

@@ -76,7 +76,8 @@ __device__ __forceinline__ void wave_order()
 // lanes stay idle), so bias and column scales are loaded once per tile; a row's
 // scale comes from the lane that loaded it.  A residual is added in a pass of
 // its own, unrolled, so that its loads are in flight together: one load after
-// the other, as in the general form, costs a tile of 256 x 256 about 13 us.
+// the other, as in the general form, costs a tile of 256 x 256 about 13 us (526
+// us instead of 500 on 8192 x 4096 x 9216 with a residual).
 template <class Out, int EPI, int W> struct WholeRows {
     static constexpr bool GATED = EPI == EPI_GATED, EXACT = sizeof(Out) == 4;
     static constexpr int PER = GATED ? W / 16 : W / 8, ROWS = 64 / PER, PASSES = (32 + ROWS - 1) / ROWS, PITCH = W + 4;

@@ -9,6 +9,12 @@
 // y / scale rounded to the nearest e4m3.  Both passes are bound by memory:
 // each tensor is read and written once, a row stays in registers between its
 // sum and its output, and all sums are fp32.
+//
+// The gradient of 8192 x 4096 bf16 takes 50 us, a copy's rate, and joining the
+// weight's partial sums 6 more.  2047 x 4096 with e4m3 outputs takes 16.8 us,
+// 3.5 TB/s: a row's loads, its two sums over the workgroup and its stores follow
+// one another, and all rows are on the chip at once.  Four waves a row are best
+// there (one 18.7, two 18.3, eight 18.5).
 #include "linear_common.h"
 #include "kernels.h"
 
