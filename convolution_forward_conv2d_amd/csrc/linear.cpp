@@ -95,9 +95,9 @@ struct TileCost {
     int bm, bn;
     double step, tile;
 };
-constexpr TileCost kFast[] = {{256, 256, 1.50, 3.0}, {256, 192, 1.12, 3.0}, {192, 256, 1.12, 3.0},
-                              {256, 128, 0.87, 2.5}, {128, 256, 0.93, 2.5}, {128, 128, 0.47, 2.5}};
-constexpr double kF32Step = 1.9;                       // 128 x 128 in fp32
+constexpr TileCost kFast[] = {{256, 256, 1.50, 3.0}, {256, 192, 1.12, 3.0}, {192, 256, 1.12, 3.0}, {256, 128, 0.87, 2.5},
+                              {128, 256, 0.93, 2.5}, {128, 128, 0.47, 2.5}, {128, 64, 0.0, 2.0},  {64, 128, 0.0, 2.0}};
+constexpr double kF32Step = 1.9;                       // 128 x 128 in fp32; of the smaller tiles, its share
 
 // linear_few.hip's blocks: their start, then memory's time for the weights or a CU's for its workgroups' weights and x, about
 // 37 KB a microsecond (a third of it where rows are not 16-byte aligned).  Measured, with the tiles' time behind it:
@@ -184,9 +184,11 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         for (int i = 0; i < (int)miconv::FastTile::COUNT; ++i) {
             const TileCost& c = kFast[i];
             pl.fast_tile = (miconv::FastTile)i;
-            if (!f32) consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
-            else if (pl.fast_tile == miconv::FastTile::T128x128)
-                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, kF32Step, c.tile);
+            const bool small = c.bm * c.bn <= 128 * 128;
+            if (f32 && small)
+                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, kF32Step * c.bm * c.bn / (128 * 128), c.tile);
+            else if (!f32 && c.step > 0)
+                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
         }
     }
     const int copies = kind == Product::GATED ? 2 : k_segments;

@@ -23,8 +23,8 @@
 // matrix units busy 70% of the cycles at 1.8 GHz of 2.4, and 605 us on zeros.
 // So what moves fewer bits wins: the 16 x 16 x 32 instruction, whose blocks'
 // sums pass through the registers half as often for the same work as 32 x 32 x
-// 16's, took 846 us to 778.  fp32 (128 x 128 only, two workgroups a CU) is bound
-// by its matrix instructions: 119 TFLOP/s of 157 at 4096^3.
+// 16's, took 846 us to 778.  fp32 (tiles up to 128 x 128, two workgroups a CU)
+// is bound by its matrix instructions: 119 TFLOP/s of 157 at 4096^3.
 #pragma once
 
 #include <type_traits>

@@ -21,10 +21,12 @@ hipError_t launch_tile(const ProductArgs& p, hipStream_t stream)
 template <class Mul, bool AACROSS, bool BACROSS, int EPI>
 hipError_t launch_one(const ProductArgs& p, FastTile tile, hipStream_t stream)
 {
-    if constexpr (Mul::E == 4) {
-        // fp32's matrix instructions take sixteen times bf16's time: the smallest tile already waits for nothing else
-        return tile == FastTile::T128x128 ? launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream)
-                                          : hipErrorInvalidValue;
+    // fp32's matrix instructions take sixteen times bf16's time: already small tiles wait for nothing else
+    if constexpr (Mul::E == 4) switch (tile) {
+    case FastTile::T128x128: return launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream);
+    case FastTile::T128x64: return launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 64, 4, 2>(p, stream);
+    case FastTile::T64x128: return launch_tile<Mul, AACROSS, BACROSS, EPI, 64, 128, 2, 4>(p, stream);
+    default: return hipErrorInvalidValue;
     } else switch (tile) {
     case FastTile::T256x256: return launch_tile<Mul, AACROSS, BACROSS, EPI, 256, 256, 2, 4>(p, stream);
     case FastTile::T256x192: return launch_tile<Mul, AACROSS, BACROSS, EPI, 256, 192, 4, 2>(p, stream);
@@ -32,7 +34,7 @@ hipError_t launch_one(const ProductArgs& p, FastTile tile, hipStream_t stream)
     case FastTile::T256x128: return launch_tile<Mul, AACROSS, BACROSS, EPI, 256, 128, 4, 2>(p, stream);
     case FastTile::T128x256: return launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 256, 2, 4>(p, stream);
     case FastTile::T128x128: return launch_tile<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream);
-    case FastTile::COUNT: break;
+    default: break;
     }
     return hipErrorInvalidValue;
 }
