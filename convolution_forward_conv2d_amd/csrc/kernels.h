@@ -187,7 +187,7 @@ constexpr int FEW_ROWS = 32;
 constexpr int vector_rows(int element_bytes) { return element_bytes == 1 ? 1 : 2; }
 hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs& p, int num_cu, hipStream_t stream);
 // Aligned operands on large tiles (linear_fast_fwd.hip, linear_fast_grad.hip):
-// bf16 and e4m3 by its own instruction from T128x128 up, fp32 from there down.
+// bf16 and e4m3 from T128x128 up, fp32 from there down.
 enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T128x128, T128x64, T64x128, COUNT };
 hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream);
 hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile,

@@ -154,7 +154,7 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     };
     // linear_any.hip: two workgroups per CU on 128 x 128 tiles, four on 64 x 64; fp32's matrix instructions take
     // sixteen times bf16's time for the same bytes
-    const double slow = type == ProductType::F32 ? 4.0 : type == ProductType::BF16 ? 1.0 : 1.8;
+    const double slow = type == ProductType::F32 ? 4.0 : type == ProductType::BF16 ? 1.0 : 1.2;
     Plan any = {};
     any.tile = 128;
     consider(any, tiles(128, 128), 128, 128, 2 * num_cu, 1.45 * slow, 2.0);
@@ -165,8 +165,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const bool short_rows = (int64_t)std::max(x.a_cols, x.b_cols) * e < kMaxPitchBytes / 2 - 64;
     // two k segments are one matrix, laid out by the library and aligned
     const bool f32 = type == ProductType::F32;
-    if ((f32 || type == ProductType::BF16 || type == ProductType::E4M3_BF16_SHORT || type == ProductType::E4M3_F32_SHORT)
-        && short_rows && (aligned_a || k_segments == 1)) {
+    // a step's 128 bytes are twice the products in e4m3, which only its own instruction takes in bf16's time
+    const double widened = type == ProductType::E4M3_BF16 || type == ProductType::E4M3_F32 ? 2.0 : 1.0;
+    if (short_rows && (aligned_a || k_segments == 1)) {
         Plan pl = {};
         pl.fast = true;
         if (!aligned_a) {
@@ -188,7 +189,7 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
             if (f32 && small)
                 consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, kF32Step * c.bm * c.bn / (128 * 128), c.tile);
             else if (!f32 && c.step > 0)
-                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step, c.tile);
+                consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, c.step * widened, c.tile);
         }
     }
     const int copies = kind == Product::GATED ? 2 : k_segments;

@@ -5,7 +5,7 @@
 // Four waves, 2 x 2, on a tile of BM x BN; two LDS buffers, one barrier a
 // step: the next step's pieces load into registers while the current step's
 // products run.  It is for what the large tiles cannot take without a copy that
-// costs more: small or unaligned products, e4m3 in fp32 sums.  131 x 1001 x 4093
+// costs more: small or unaligned products.  131 x 1001 x 4093
 // in bf16 takes 12 us in ten parts and 4.5 to join them: the latency of its
 // steps, one load to the next.
 #include "linear_tile.h"

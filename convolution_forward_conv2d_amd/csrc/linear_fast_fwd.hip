@@ -15,14 +15,20 @@ hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs
     case ProductType::F32:
         return gated ? launch_one<MulF32, false, false, EPI_GATED>(p, tile, stream)
                      : launch_one<MulF32, false, false, EPI_LINEAR>(p, tile, stream);
+    case ProductType::E4M3_BF16:
+        return gated ? launch_one<MulE4m3<Bf16, false>, false, false, EPI_GATED>(p, tile, stream)
+                     : launch_one<MulE4m3<Bf16, false>, false, false, EPI_LINEAR>(p, tile, stream);
+    case ProductType::E4M3_F32:
+        return gated ? launch_one<MulE4m3<float, false>, false, false, EPI_GATED>(p, tile, stream)
+                     : launch_one<MulE4m3<float, false>, false, false, EPI_LINEAR>(p, tile, stream);
     case ProductType::E4M3_BF16_SHORT:
         return gated ? launch_one<MulE4m3<Bf16, true>, false, false, EPI_GATED>(p, tile, stream)
                      : launch_one<MulE4m3<Bf16, true>, false, false, EPI_LINEAR>(p, tile, stream);
     case ProductType::E4M3_F32_SHORT:
         return gated ? launch_one<MulE4m3<float, true>, false, false, EPI_GATED>(p, tile, stream)
                      : launch_one<MulE4m3<float, true>, false, false, EPI_LINEAR>(p, tile, stream);
-    default: return hipErrorInvalidValue;
     }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace miconv
