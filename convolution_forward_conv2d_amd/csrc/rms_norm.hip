@@ -15,6 +15,8 @@
 // 3.5 TB/s: a row's loads, its two sums over the workgroup and its stores follow
 // one another, and all rows are on the chip at once.  Four waves a row are best
 // there (one 18.7, two 18.3, eight 18.5).
+#include <type_traits>
+
 #include "linear_common.h"
 #include "kernels.h"
 
@@ -290,7 +292,10 @@ template <class T> __global__ __launch_bounds__(64) void norm_weight_kernel(cons
     store8(p.partial + (int64_t)blockIdx.x * p.cols + c, nv, dw);
 }
 
-template <class T, bool E4M3> hipError_t launch_type(const NormArgs& p, hipStream_t stream)
+// HIP takes grids of fewer than 2^32 threads; a workgroup per row of at most 512 threads reaches that at 2^23 rows.
+constexpr int GRID_ROWS = 1 << 22;
+
+template <class T, bool E4M3> hipError_t launch_rows(const NormArgs& p, hipStream_t stream)
 {
     const int v = (p.cols + 7) / 8;                            // vectors in a row
     if (v <= 64) rms_norm_kernel<T, E4M3, 1, 1, false><<<p.rows, 64, 0, stream>>>(p);
@@ -299,6 +304,24 @@ template <class T, bool E4M3> hipError_t launch_type(const NormArgs& p, hipStrea
     else if (v <= 1024) rms_norm_kernel<T, E4M3, 4, 4, false><<<p.rows, 256, 0, stream>>>(p);
     else rms_norm_kernel<T, E4M3, 8, 4, true><<<p.rows, 512, 0, stream>>>(p);
     return hipGetLastError();
+}
+
+template <class T, bool E4M3> hipError_t launch_type(const NormArgs& all, hipStream_t stream)
+{
+    using Out = typename std::conditional<E4M3, uint8_t, T>::type;
+    for (int64_t first = 0; first < all.rows; first += GRID_ROWS) {
+        NormArgs p = all;
+        p.rows = (int)(all.rows - first < GRID_ROWS ? all.rows - first : GRID_ROWS);
+        p.x = static_cast<const T*>(all.x) + first * all.ldx;
+        if (p.residual) p.residual = static_cast<const T*>(all.residual) + first * all.ldr;
+        p.y = static_cast<Out*>(all.y) + first * all.ldy;
+        if (p.sum) p.sum = static_cast<T*>(all.sum) + first * all.lds;
+        if (p.rstd) p.rstd = all.rstd + first;
+        if (p.scale) p.scale = all.scale + first;
+        const hipError_t err = launch_rows<T, E4M3>(p, stream);
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 constexpr int GRAD_MOST = 8192;    // columns whose dweight share a workgroup keeps in registers
