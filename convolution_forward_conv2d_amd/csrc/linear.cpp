@@ -26,8 +26,17 @@ bool plain_type(mic_dtype d) { return d == MIC_DTYPE_F32 || d == MIC_DTYPE_BF16;
 DType device_type(mic_dtype d) { return d == MIC_DTYPE_F32 ? DType::F32 : DType::BF16; }
 bool valid_act(mic_activation a) { return (int)a >= 0 && (int)a <= (int)MIC_ACT_SILU; }
 
-// Host-only calls need no device: without a handle they plan for the MI355X.
-int num_cus(mic_handle h) { return h ? h->num_cu : 256; }
+// The compute units a handle may have: an MI355X whole and in its two, four and eight partitions.  Host-only calls
+// need no device: without a handle they answer for every one of these.
+constexpr int kCuCounts[] = {256, 128, 64, 32};
+
+template <class Bytes> size_t most_bytes(mic_handle h, Bytes bytes)
+{
+    if (h) return bytes(h->num_cu);
+    size_t most = 0;
+    for (int cus : kCuCounts) most = std::max(most, bytes(cus));
+    return most;
+}
 
 int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -275,7 +284,9 @@ mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m,
     ProductType type, fast;
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &type));
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &fast, true));
-    *bytes = std::max(product_bytes(num_cus(h), kind, type, m, n, k, 1), product_bytes(num_cus(h), kind, fast, m, n, k, 1));
+    *bytes = most_bytes(h, [&](int cus) {
+        return std::max(product_bytes(cus, kind, type, m, n, k, 1), product_bytes(cus, kind, fast, m, n, k, 1));
+    });
     return MIC_STATUS_SUCCESS;
 }
 
@@ -285,15 +296,15 @@ struct GradLayout {
     size_t dz, sums, product, total;
 };
 
-GradLayout grad_layout(mic_handle h, ProductType type, int m, int n, int k, bool gated, bool bias)
+GradLayout grad_layout(int num_cu, ProductType type, int m, int n, int k, bool gated, bool bias)
 {
     GradLayout g = {};
     const int two = gated ? 2 : 1;
     g.pitch = align_up(n, 64);
     g.dz = (size_t)align_up((int64_t)m * g.pitch * two * (type == ProductType::F32 ? 4 : 2), 256);
     g.sums = bias ? (size_t)align_up((int64_t)miconv::slope_row_groups(m, n) * n * 4, 256) : 0;
-    const size_t a = product_bytes(num_cus(h), Product::INPUT_GRAD, type, m, k, n, two);
-    const size_t b = product_bytes(num_cus(h), Product::WEIGHT_GRAD, type, (int)(gated ? 2 * g.pitch : n), k, m, 1);
+    const size_t a = product_bytes(num_cu, Product::INPUT_GRAD, type, m, k, n, two);
+    const size_t b = product_bytes(num_cu, Product::WEIGHT_GRAD, type, (int)(gated ? 2 * g.pitch : n), k, m, 1);
     g.product = std::max(a, b);
     g.total = g.dz + g.sums + g.product;
     return g;
@@ -307,7 +318,7 @@ mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k
     if (n >= kMaxSize / 2) return MIC_STATUS_NOT_SUPPORTED;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    *bytes = grad_layout(h, type, m, n, k, gated, !gated).total;
+    *bytes = most_bytes(h, [&](int cus) { return grad_layout(cus, type, m, n, k, gated, !gated).total; });
     return MIC_STATUS_SUCCESS;
 }
 
@@ -375,7 +386,7 @@ mic_status mic_rms_norm_backward_workspace(mic_handle handle, int rows, int cols
 {
     if (!bytes) return MIC_STATUS_BAD_PARAM;
     MIC_TRY(check_sizes(rows, cols, 0));
-    *bytes = (size_t)miconv::rms_norm_grad_groups(rows, cols, num_cus(handle)) * cols * 4;
+    *bytes = most_bytes(handle, [&](int cus) { return (size_t)miconv::rms_norm_grad_groups(rows, cols, cus) * cols * 4; });
     return MIC_STATUS_SUCCESS;
 }
 
@@ -400,7 +411,7 @@ mic_status mic_rms_norm_backward(mic_handle handle, mic_dtype dtype, int rows, i
     if (dweight && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return MIC_STATUS_BAD_PARAM;
     miconv::NormGradArgs p = {rows, cols, dy, lddy, sum, lds, weight, rstd, dsum, ldd, dx, lddx, dweight,
                               static_cast<float*>(workspace),
-                              miconv::rms_norm_grad_groups(rows, cols, num_cus(handle))};
+                              miconv::rms_norm_grad_groups(rows, cols, handle->num_cu)};
     return launched(miconv::launch_rms_norm_grad(device_type(dtype), p, handle->stream));
 }
 
@@ -469,7 +480,7 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
     if (n == 0 && (!dx || k == 0)) return MIC_STATUS_SUCCESS;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    const GradLayout g = grad_layout(handle, type, m, n, k, false, true);
+    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, false, true);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     // without an activation dz is dy, read where it is
     const bool own = slope && (dx || dw);
@@ -569,7 +580,7 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
     if ((!dx && !dw_gate) || k == 0) return MIC_STATUS_SUCCESS;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    const GradLayout g = grad_layout(handle, type, m, n, k, true, false);
+    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, true, false);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (m && n) {
         miconv::SlopeArgs s = {};

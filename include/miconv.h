@@ -403,9 +403,10 @@ mic_status mic_brgemm_kernel_name(mic_handle handle, mic_dtype dtype, int m, int
  * zero.  Outputs must not overlap inputs or each other (not checked).
  *
  * Workspaces are the caller's device memory, 16-byte aligned, of at least the
- * bytes the matching ..._workspace call (host only; the handle may be null)
- * returns for the same sizes; their contents need no preparation and nothing in them survives a
- * call.  Calls are asynchronous on the handle's stream and may be captured
+ * bytes the matching ..._workspace call (host only) returns for the same sizes
+ * and handle, or without a handle, which answers for an MI355X whole or in any
+ * of its partitions; their contents need no preparation and nothing in them
+ * survives a call.  Calls are asynchronous on the handle's stream and may be captured
  * into graphs.  Results do not depend on workgroup order: no atomics.
  *
  * Errors: MIC_STATUS_BAD_PARAM (null handle or needed pointer, negative size,
