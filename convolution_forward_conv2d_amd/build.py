@@ -81,13 +81,13 @@ def build(verbose=False):
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
         binding = pool.submit(_compile_binding, verbose)
         objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
-        obj, torch_lib = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True, capture_output=not verbose)
     os.replace(tmp, LIB)
+    obj, torch_lib = binding.result()          # the library is there without what needs torch's headers
     tmp = NATIVE + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-lmiconv", "-Wl,-rpath,$ORIGIN", "-L" + torch_lib,
            "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
