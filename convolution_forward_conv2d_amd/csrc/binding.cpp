@@ -133,6 +133,19 @@ template <class Ask> bool workspace(int call, mic_dtype d, int64_t m, int64_t n,
     return true;
 }
 
+// A truth value; false, with the exception set: it has none, as a tensor has not unless it is one bool.
+bool flag(PyObject* o, const char* name, bool& v)
+{
+    const Tensor* t = tensor(o);
+    if (t && (t->scalar_type() != at::kBool || t->numel() != 1)) {
+        PyErr_Format(PyExc_TypeError, "%s must be True or False, not a tensor", name);
+        return false;
+    }
+    const int is = PyObject_IsTrue(o);
+    v = is > 0;
+    return is >= 0;
+}
+
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 
 PyObject* none()
@@ -160,7 +173,8 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         return none();
     const double eps = PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) return nullptr;
-    const bool e4m3 = PyObject_IsTrue(a[4]);
+    bool e4m3;
+    if (!flag(a[4], "e4m3", e4m3)) return nullptr;
     const auto type = x->scalar_type();
     if (!dtype_of(*x, d) || d == MIC_DTYPE_F8_E4M3 || !plain(*w, type, *x, {cols})) return none();
     if (residual && (residual->sizes() != x->sizes() || !plain_matrix(*residual, type, *x, rows, cols))) return none();
@@ -215,12 +229,11 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 }
 
 // The scales of a forward call, there where the operands are e4m3 and only there, and the output's type.
-bool layer_types(mic_dtype d, PyObject* f32, std::initializer_list<const Tensor*> scales, at::ScalarType type,
+bool layer_types(mic_dtype d, bool wide, std::initializer_list<const Tensor*> scales, at::ScalarType type,
                  at::ScalarType& out, mic_dtype& out_d)
 {
     for (const Tensor* s : scales)
         if ((d == MIC_DTYPE_F8_E4M3) != (s != nullptr)) return false;
-    const bool wide = PyObject_IsTrue(f32);
     if (d != MIC_DTYPE_F8_E4M3) out = type, out_d = d;
     else out = wide ? at::kFloat : at::kBFloat16, out_d = wide ? MIC_DTYPE_F32 : MIC_DTYPE_BF16;
     return true;
@@ -237,8 +250,10 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (n_args != 10 || !plain_rows(x = tensor(a[0]), m, k) || !(w = tensor(a[1])) || !maybe(a[2], bias)
         || !maybe(a[3], residual) || !maybe(a[5], xs) || !maybe(a[6], ws) || !dtype_of(*x, d) || w->dim() != 2)
         return none();
+    bool wide, keep, fast;
+    if (!flag(a[7], "out in fp32", wide) || !flag(a[8], "return_preact", keep) || !flag(a[9], "fast_sums", fast)) return nullptr;
     const int64_t n = w->size(0);
-    if (!n || n >= INT32_MAX || !layer_types(d, a[7], {xs, ws}, x->scalar_type(), out, out_d)
+    if (!n || n >= INT32_MAX || !layer_types(d, wide, {xs, ws}, x->scalar_type(), out, out_d)
         || !plain(*w, x->scalar_type(), *x, {n, k}) || (bias && !plain(*bias, out, *x, {n}))
         || (residual && !plain_matrix(*residual, out, *x, m, n)) || (xs && !plain_scale(*xs, *x, m))
         || (ws && (!plain_scale(*ws, *x, n) || ws->dim() != 1)))
@@ -252,10 +267,9 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
             return mic_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
-    const bool keep = PyObject_IsTrue(a[8]);
     Tensor y = rows_of(*x, n, out), z;
     if (keep) z = like(y, out);
-    if (mic_linear_forward(h, d, out_d, (mic_activation)act, PyObject_IsTrue(a[9]), (int)m, (int)n, (int)k, x->data_ptr(), k,
+    if (mic_linear_forward(h, d, out_d, (mic_activation)act, fast, (int)m, (int)n, (int)k, x->data_ptr(), k,
                            w->data_ptr(), k, floats(xs), floats(ws), data(bias), data(residual), n, y.data_ptr(), n,
                            keep ? z.data_ptr() : nullptr, n, bytes ? space.data_ptr() : nullptr, bytes)
         != MIC_STATUS_SUCCESS)
@@ -274,6 +288,8 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (n_args != 6 || !plain_rows(dy = tensor(a[0]), m, n) || !(x = tensor(a[1])) || !(w = tensor(a[2]))
         || !maybe(a[3], pre) || !dtype_of(*dy, d) || d == MIC_DTYPE_F8_E4M3 || x->dim() < 1)
         return none();
+    bool bias;
+    if (!flag(a[5], "bias", bias)) return nullptr;
     const long act = PyLong_AsLong(a[4]);
     if (act == -1 && PyErr_Occurred()) return nullptr;
     const auto type = dy->scalar_type();
@@ -288,7 +304,6 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
             return mic_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
-    const bool bias = PyObject_IsTrue(a[5]);
     Tensor dx = like(*x, type), dw = like(*w, type), db;
     if (bias) db = at::empty({n}, dy->options());
     if (mic_linear_backward(h, d, (mic_activation)act, (int)m, (int)n, (int)k, dy->data_ptr(), n, x->data_ptr(), k,
@@ -311,9 +326,11 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (n_args != 10 || !plain_rows(x = tensor(a[0]), m, k) || !(wg = tensor(a[1])) || !(wu = tensor(a[2]))
         || !maybe(a[4], xs) || !maybe(a[5], gs) || !maybe(a[6], us) || !dtype_of(*x, d) || wg->dim() != 2)
         return none();
+    bool wide, keep, fast;
+    if (!flag(a[7], "out in fp32", wide) || !flag(a[8], "return_products", keep) || !flag(a[9], "fast_sums", fast)) return nullptr;
     const int64_t n = wg->size(0);
     const auto type = x->scalar_type();
-    if (!n || n >= INT32_MAX || !layer_types(d, a[7], {xs, gs, us}, type, out, out_d) || !plain(*wg, type, *x, {n, k})
+    if (!n || n >= INT32_MAX || !layer_types(d, wide, {xs, gs, us}, type, out, out_d) || !plain(*wg, type, *x, {n, k})
         || !plain(*wu, type, *x, {n, k}) || (xs && !plain_scale(*xs, *x, m))
         || (gs && (!plain_scale(*gs, *x, n) || gs->dim() != 1)) || (us && (!plain_scale(*us, *x, n) || us->dim() != 1)))
         return none();
@@ -326,10 +343,9 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
             return mic_gated_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
-    const bool keep = PyObject_IsTrue(a[8]);
     Tensor y = rows_of(*x, n, out), gate, up;
     if (keep) gate = like(y, out), up = like(y, out);
-    if (mic_gated_linear_forward(h, d, out_d, (mic_activation)act, PyObject_IsTrue(a[9]), (int)m, (int)n, (int)k, x->data_ptr(),
+    if (mic_gated_linear_forward(h, d, out_d, (mic_activation)act, fast, (int)m, (int)n, (int)k, x->data_ptr(),
                                  k, wg->data_ptr(), k, wu->data_ptr(), k, floats(xs), floats(gs), floats(us), y.data_ptr(),
                                  n, keep ? gate.data_ptr() : nullptr, n, keep ? up.data_ptr() : nullptr, n,
                                  bytes ? space.data_ptr() : nullptr, bytes)

@@ -159,6 +159,12 @@ def _act(activation):
         raise ValueError("unknown activation %r (one of %s)" % (activation, ", ".join(mic.ACTIVATIONS))) from None
 
 
+def _flag(v, name):
+    if isinstance(v, torch.Tensor) and (v.dtype is not torch.bool or v.numel() != 1):
+        raise TypeError("%s must be True or False, not a tensor" % name)
+    return bool(v)
+
+
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -286,6 +292,7 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
         r = (_native or _load()).linear(x, w, bias, residual, act, x_scale, w_scale, wide, return_preact, fast_sums)
         if r is not None:
             return r if return_preact else r[0]
+    return_preact, fast_sums = _flag(return_preact, "return_preact"), _flag(fast_sums, "fast_sums")
     out_dtype = _layer_types(x, out_dtype, (x_scale, w_scale))
     act, dtype, device = _act(activation), x.dtype, x.device
     k = x.shape[-1] if x.dim() else 0
@@ -301,7 +308,7 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
     y = x.new_empty(shape, dtype=out_dtype)
     z = torch.empty_like(y) if return_preact else None
     wk, wkp, wkn = _workspace("mic_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
-    _call("mic_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, bool(fast_sums), m, n, k, x.data_ptr(), ldx, w.data_ptr(), ldw,
+    _call("mic_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, fast_sums, m, n, k, x.data_ptr(), ldx, w.data_ptr(), ldw,
           xs, ws, bp, _ptr(residual), ldr, y.data_ptr(), n, _ptr(z), n, wkp, wkn)
     return (y, z) if return_preact else y
 
@@ -316,6 +323,7 @@ def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
         r = (_native or _load()).linear_backward(dy, x, w, preact, act, bias)
         if r is not None:
             return r
+    bias = _flag(bias, "bias")
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     act, dtype, device = _act(activation), dy.dtype, dy.device
     n = dy.shape[-1] if dy.dim() else 0
@@ -351,6 +359,7 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
                                               return_products, fast_sums)
         if r is not None:
             return r if return_products else r[0]
+    return_products, fast_sums = _flag(return_products, "return_products"), _flag(fast_sums, "fast_sums")
     out_dtype = _layer_types(x, out_dtype, (x_scale, w_gate_scale, w_up_scale))
     act, dtype, device = _act(activation), x.dtype, x.device
     k = x.shape[-1] if x.dim() else 0
@@ -369,7 +378,7 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
     gate = torch.empty_like(y) if return_products else None
     up = torch.empty_like(y) if return_products else None
     wk, wkp, wkn = _workspace("mic_gated_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
-    _call("mic_gated_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, bool(fast_sums), m, n, k, x.data_ptr(), ldx,
+    _call("mic_gated_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, fast_sums, m, n, k, x.data_ptr(), ldx,
           w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, xs, gs, us, y.data_ptr(), n, _ptr(gate), n, _ptr(up), n, wkp,
           wkn)
     return (y, gate, up) if return_products else y
