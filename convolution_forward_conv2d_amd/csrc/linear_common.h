@@ -242,6 +242,22 @@ template <bool EXACT> __device__ __forceinline__ void activate8(int act, float (
     }
 }
 
+// A scale s = part * 2^power.  The product of a row's and a column's scale can leave fp32's normal range where the sum
+// times both does not, so the parts (in [1/2, 1)) are multiplied first and the powers applied last, with one rounding
+// more only where the result is subnormal; anywhere else the bits are those of sum * (x_scale * w_scale).
+struct Scale {
+    float part;
+    int power;
+};
+__device__ __forceinline__ Scale split_scale(float s)
+{
+    return Scale{__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+}
+__device__ __forceinline__ float scaled(float v, Scale a, Scale b)
+{
+    return __builtin_ldexpf(v * (a.part * b.part), a.power + b.power);
+}
+
 // Eight finished columns n..n+7 of row m: v the raw sums (u the second product's).
 template <class Out, int EPI>
 __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, float (&v)[8], float (&u)[8])
@@ -258,15 +274,15 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, floa
     if (m >= p.M || n >= p.N) return;
     const int nv = p.N - n;
     if (p.x_scale) {
-        const float xs = p.x_scale[m];
+        const Scale xs = split_scale(p.x_scale[m]);
         float ws[8];
         load8(p.w_scale + n, nv, ws);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= xs * ws[i];
+        for (int i = 0; i < 8; ++i) v[i] = scaled(v[i], xs, split_scale(ws[i]));
         if constexpr (EPI == EPI_GATED) {
             load8(p.w2_scale + n, nv, ws);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] *= xs * ws[i];
+            for (int i = 0; i < 8; ++i) u[i] = scaled(u[i], xs, split_scale(ws[i]));
         }
     }
     if constexpr (EPI == EPI_LINEAR) {
