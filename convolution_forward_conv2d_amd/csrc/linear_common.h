@@ -83,33 +83,50 @@ template <int E> __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, i
 
 // ------------------------------------------------------------------ activations
 //
-// All in fp32.  e^x is 2^(x log2 e) on the hardware's exponential (about
-// 1 ulp) and 1/x its reciprocal (1 ulp): relative errors near 2^-22, far
-// below a bf16 rounding and inside the fp32 outputs' tolerance.
+// All in fp32.  e^x is 2^(x log2 e) on the hardware's exponential and 1/x its
+// reciprocal, each within 1 ulp.  Rounding x log2 e to fp32 puts e^x off by up
+// to |x| 2^-24 of itself more: that is below 2^-17 where bf16 outputs round to
+// 2^-8, but not for fp32 ones (EXACT), which put what the rounding took back.
+// e^x is then within 2^-22 of itself, SiLU within 2^-21, and the tanh GELU
+// within 2^-21 (1 + |a|), a the logistic function's argument, which fp32 itself
+// holds no better.  What is below 2^-126 becomes zero.
 //
-// The normal distribution function of the exact GELU: fp32 tensors use erff;
-// bf16 ones Abramowitz & Stegun's formula 7.1.26 for erfc, whose error of at
-// most 1.5e-7 is 2^-22.7 of the function's range, about that of erff's own
-// complement 1 + erf(x) in fp32, at a third of its instructions (the
-// epilogue of an e4m3 product of depth 4096 would otherwise spend half as
-// long in erff as in its matrix instructions).
+// The normal distribution function of the exact GELU: fp32 tensors use erff,
+// whose complement 1 + erf(x) is within 2^-24 (of 1, not of itself).  bf16 ones
+// take its tail as the bell times a polynomial of 1 / (1 + 0.292 |z|), fitted
+// for this: the polynomial is within 6.2e-8 of the tail in all and within 6.1e-5
+// (2^-14) relative to it up to |z| = 14, where the bell ends, so outputs far
+// below zero keep bf16's precision too, at a third of erff's instructions (the epilogue of an e4m3
+// product of depth 4096 would otherwise spend half as long in erff as in its
+// matrix instructions).
 
-__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896f); }
-__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)); }
+template <bool EXACT> __device__ __forceinline__ float exponential(float x)
+{
+    const float e = __builtin_amdgcn_exp2f(x * 1.44269504f);
+    if constexpr (!EXACT) return e;
+    // past 128 e is 0 or infinite already, and the rest of the argument no small number
+    const float c = fminf(fmaxf(x, -128.0f), 128.0f), p = c * 1.44269504f;
+    const float rest = fmaf(c, 1.92596303e-8f, fmaf(c, 1.44269504f, -p));      // of x log2 e, past p
+    return e * fmaf(rest, 0.693147181f, 1.0f);
+}
+template <bool EXACT> __device__ __forceinline__ float logistic(float x)
+{
+    return __builtin_amdgcn_rcpf(1.0f + exponential<EXACT>(-x));
+}
 
-// erfc(|z| / sqrt 2) / 2 by 7.1.26, and its bell e^(-z^2/2).
+// Phi(-|z|), the normal distribution's tail, and its bell e^(-z^2/2).
 __device__ __forceinline__ float normal_tail(float z, float& bell)
 {
     bell = __builtin_amdgcn_exp2f(z * (z * -0.721347520444482f));
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.231641888f * fabsf(z));
-    return t * (0.127414796f + t * (-0.142248368f + t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f)))) * bell;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.292f * fabsf(z));
+    return t * (0.11744149f + t * (0.10390588f + t * (0.1709076f + t * (-0.076288655f + t * (0.27079475f + t * -0.086761124f))))) * bell;
 }
 
 // (Phi(z), e^(-z^2/2)): the normal distribution function and its bell.
 template <bool EXACT> __device__ __forceinline__ void normal_cdf(float z, float& phi, float& bell)
 {
     if constexpr (EXACT) {
-        bell = fast_exp(-0.5f * z * z);
+        bell = exponential<EXACT>(-0.5f * z * z);
         phi = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
     } else {
         const float half = normal_tail(z, bell);
@@ -132,8 +149,8 @@ template <bool EXACT> __device__ __forceinline__ float act_value(int act, float 
         return fmaxf(z, 0.0f) - fminf(fabsf(z), 16.0f) * tail;
     }
     case ACT_GELU_TANH:       // 0.5 z (1 + tanh(u)) = z * logistic(2 u)
-        return z * logistic(1.59576912160573f * (z + 0.044715f * z * z * z));
-    case ACT_SILU: return z * logistic(z);
+        return z * logistic<EXACT>(1.59576912160573f * (z + 0.044715f * z * z * z));
+    case ACT_SILU: return z * logistic<EXACT>(z);
     default: return z;
     }
 }
@@ -154,7 +171,7 @@ template <bool EXACT> __device__ __forceinline__ void act_both(int act, float z,
         break;
     }
     case ACT_GELU_TANH: {
-        const float p = logistic(1.59576912160573f * (z + 0.044715f * z * z * z));
+        const float p = logistic<EXACT>(1.59576912160573f * (z + 0.044715f * z * z * z));
         value = z * p;
         // past 64 p is 0 or 1 to the last bit, and z^2 may overflow
         const float c = fminf(fmaxf(z, -64.0f), 64.0f);
@@ -162,7 +179,7 @@ template <bool EXACT> __device__ __forceinline__ void act_both(int act, float z,
         break;
     }
     case ACT_SILU: {
-        const float p = logistic(z);
+        const float p = logistic<EXACT>(z);
         value = z * p;
         slope = p + value * (1.0f - p);
         break;
