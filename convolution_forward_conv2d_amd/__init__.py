@@ -129,6 +129,10 @@ _SIGS = {
     "mic_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
                             _vp, _i64, _vp, ctypes.c_size_t], _i),
+    "mic_linear_forward_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
+    "mic_gated_linear_forward_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
+    "mic_linear_backward_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
+    "mic_gated_linear_backward_kernel_name": ([_vp, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
     "mic_linear_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_backward": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                              _i64, _vp, _vp, ctypes.c_size_t], _i),
@@ -433,6 +437,28 @@ def mic_gated_linear_backward_workspace(handle, dtype, m, n, k):
 
 def mic_gated_linear_backward(*args):
     _check(lib().mic_gated_linear_backward(*args), "mic_gated_linear_backward")
+
+
+def _name(name, *args):
+    buf = ctypes.create_string_buffer(128)
+    _check(getattr(lib(), name)(*args, buf, len(buf)), name)
+    return buf.value.decode()
+
+
+def mic_linear_forward_kernel_name(handle, dtype, out_dtype, fast_sums, m, n, k, aligned=True):
+    return _name("mic_linear_forward_kernel_name", handle, dtype, out_dtype, fast_sums, m, n, k, aligned)
+
+
+def mic_gated_linear_forward_kernel_name(handle, dtype, out_dtype, fast_sums, m, n, k, aligned=True):
+    return _name("mic_gated_linear_forward_kernel_name", handle, dtype, out_dtype, fast_sums, m, n, k, aligned)
+
+
+def mic_linear_backward_kernel_name(handle, dtype, act, m, n, k, aligned=True):
+    return _name("mic_linear_backward_kernel_name", handle, dtype, act, m, n, k, aligned)
+
+
+def mic_gated_linear_backward_kernel_name(handle, dtype, m, n, k, aligned=True):
+    return _name("mic_gated_linear_backward_kernel_name", handle, dtype, m, n, k, aligned)
 
 
 # ---------------------------------------------------------------- torch-facing helpers

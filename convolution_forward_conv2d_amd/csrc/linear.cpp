@@ -1,6 +1,8 @@
 // linear.cpp -- host side of the feed-forward operators: validation, the
 // choice of kernel and tile, workspaces and launches.
 #include <stdint.h>
+#include <stdio.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -223,6 +225,44 @@ bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes)
     return aligned(p, 16) && ld % 16 == 0 && bytes % 16 == 0 && ld < kMaxPitchBytes / 2;
 }
 
+// Which of a product's operands can be read 16 bytes at a time, where the caller says that every operand's pointer and
+// pitch is a multiple of 16 bytes (`aligned`).  A gradient's dz is the library's own (`own_dz`) unless it is dy.
+struct Aligned {
+    bool a, b;
+};
+
+Aligned aligned_operands(Product kind, ProductType type, int n, int k, bool aligned, bool own_dz, int64_t dz_pitch)
+{
+    const int e = element_bytes(type);
+    auto even = [&](int64_t cols) { return cols * e % 16 == 0 && cols * e < kMaxPitchBytes / 2; };
+    const bool x = aligned && even(k);                         // x's rows and w's are k long
+    if (kind == Product::FORWARD || kind == Product::GATED) return {x, x};
+    return {own_dz ? even(dz_pitch) : aligned && even(n), x};
+}
+
+void describe(const Plan& pl, char* text, size_t size)
+{
+    constexpr const char* kFastNames[] = {"256x256", "256x192", "192x256", "256x128", "128x256", "128x128", "128x64", "64x128"};
+    static_assert(sizeof(kFastNames) / sizeof(*kFastNames) == (size_t)miconv::FastTile::COUNT, "one name a tile");
+    int at;
+    if (pl.few) at = snprintf(text, size, "few");
+    else if (pl.fast) at = snprintf(text, size, "fast %s", kFastNames[(int)pl.fast_tile]);
+    else at = snprintf(text, size, "any %dx%d", pl.tile, pl.tile);
+    if (pl.splits > 1) at += snprintf(text + at, size - at, " split %d", pl.splits);
+    if (pl.pack_a) at += snprintf(text + at, size - at, " pack a");
+    if (pl.pack_b) snprintf(text + at, size - at, " pack b");
+}
+
+mic_status give_name(const char* text, char* buf, size_t buflen)
+{
+    const size_t len = strlen(text);
+    if (!buf || len + 1 > buflen) return MIC_STATUS_BAD_PARAM;
+    memcpy(buf, text, len + 1);
+    return MIC_STATUS_SUCCESS;
+}
+
+int cus_of(mic_handle h) { return h ? h->num_cu : kCuCounts[0]; }
+
 mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes)
 {
     if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
@@ -290,6 +330,19 @@ mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m,
     return MIC_STATUS_SUCCESS;
 }
 
+mic_status forward_name(mic_handle h, Product kind, mic_dtype dtype, mic_dtype out_dtype, int fast_sums, int m, int n, int k,
+                        int aligned, char* buf, size_t buflen)
+{
+    MIC_TRY(check_sizes(m, n, k));
+    ProductType type;
+    MIC_TRY(product_type(dtype, out_dtype, &type, fast_sums != 0));
+    if (!m || !n) return give_name("nothing", buf, buflen);
+    const Aligned al = aligned_operands(kind, type, n, k, aligned != 0, false, 0);
+    char text[64];
+    describe(plan_product(cus_of(h), kind, type, m, n, k, 1, al.a, al.b), text, sizeof(text));
+    return give_name(text, buf, buflen);
+}
+
 // The backward workspace: dz, dbias's partial sums, the products' own.
 struct GradLayout {
     int64_t pitch;           // of one layer's dz columns
@@ -320,6 +373,25 @@ mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k
     MIC_TRY(product_type(dtype, dtype, &type));
     *bytes = most_bytes(h, [&](int cus) { return grad_layout(cus, type, m, n, k, gated, !gated).total; });
     return MIC_STATUS_SUCCESS;
+}
+
+mic_status backward_name(mic_handle h, mic_dtype dtype, bool own_dz, int m, int n, int k, bool gated, int aligned, char* buf,
+                         size_t buflen)
+{
+    MIC_TRY(check_sizes(m, n, k));
+    if (!plain_type(dtype)) return MIC_STATUS_NOT_SUPPORTED;
+    ProductType type;
+    MIC_TRY(product_type(dtype, dtype, &type));
+    if (!k) return give_name("nothing", buf, buflen);
+    const int two = gated ? 2 : 1;
+    const int64_t pitch = align_up(n, 64);
+    char dx[64] = "nothing", dw[64] = "nothing", text[160];
+    const Aligned in = aligned_operands(Product::INPUT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
+    if (m) describe(plan_product(cus_of(h), Product::INPUT_GRAD, type, m, k, n, two, in.a, in.b), dx, sizeof(dx));
+    const Aligned w = aligned_operands(Product::WEIGHT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
+    if (n) describe(plan_product(cus_of(h), Product::WEIGHT_GRAD, type, gated ? (int)(2 * pitch) : n, k, m, 1, w.a, w.b), dw, sizeof(dw));
+    snprintf(text, sizeof(text), "dx: %s, dw: %s", dx, dw);
+    return give_name(text, buf, buflen);
 }
 
 // dx = dz w (+ dz2 w2) and dw = dz^T x (dw2 = dz2^T x).  dz has dz_cols >= n columns, zeros from n on (and the
@@ -451,6 +523,31 @@ mic_status mic_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_
     p.x_scale = x_scale, p.w_scale = w_scale;
     p.pre = preact, p.ldp = ldp;
     return run_product(handle, Product::FORWARD, type, p, workspace, workspace_bytes);
+}
+
+mic_status mic_linear_forward_kernel_name(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int fast_sums, int m,
+                                          int n, int k, int aligned, char* buf, size_t buflen)
+{
+    return forward_name(handle, Product::FORWARD, dtype, out_dtype, fast_sums, m, n, k, aligned, buf, buflen);
+}
+
+mic_status mic_gated_linear_forward_kernel_name(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int fast_sums,
+                                                int m, int n, int k, int aligned, char* buf, size_t buflen)
+{
+    return forward_name(handle, Product::GATED, dtype, out_dtype, fast_sums, m, n, k, aligned, buf, buflen);
+}
+
+mic_status mic_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
+                                           int aligned, char* buf, size_t buflen)
+{
+    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
+    return backward_name(handle, dtype, act != MIC_ACT_NONE, m, n, k, false, aligned, buf, buflen);
+}
+
+mic_status mic_gated_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, int m, int n, int k, int aligned,
+                                                 char* buf, size_t buflen)
+{
+    return backward_name(handle, dtype, true, m, n, k, true, aligned, buf, buflen);
 }
 
 mic_status mic_linear_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)

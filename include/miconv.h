@@ -495,6 +495,23 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
                                      int64_t lddg, void* dw_up, int64_t lddu, void* workspace,
                                      size_t workspace_bytes);
 
+/* How a call runs its products, host only, NUL-terminated into buf of buflen
+ * bytes (MIC_STATUS_BAD_PARAM if it does not fit; 128 do): "few" rows, large
+ * tiles ("fast 256x192") or small ones through registers ("any 64x64"), in how
+ * many parts the reduction is split and which operands are packed first; a
+ * gradient's as "dx: ..., dw: ...".  aligned: whether all operands' pointers and
+ * pitches are multiples of 16 bytes, pitches below 4 MB and w_gate's that of
+ * w_up.  Without a handle the answer is that of a whole MI355X.  Errors as the
+ * call's own checks of sizes and types. */
+mic_status mic_linear_forward_kernel_name(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int fast_sums, int m,
+                                          int n, int k, int aligned, char* buf, size_t buflen);
+mic_status mic_gated_linear_forward_kernel_name(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int fast_sums,
+                                                int m, int n, int k, int aligned, char* buf, size_t buflen);
+mic_status mic_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
+                                           int aligned, char* buf, size_t buflen);
+mic_status mic_gated_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, int m, int n, int k, int aligned,
+                                                 char* buf, size_t buflen);
+
 #ifdef __cplusplus
 }
 #endif
