@@ -147,10 +147,15 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         best.splits = 1;
         // one or two rows on the vector units: faster at every size and alignment measured (4001 x 4093, rows of odd
         // lengths, 11.4 us against 22.0)
-        if (m <= miconv::vector_rows(e)) return best;
+        if (m <= miconv::vector_rows(e)) {
+            best.us = 0.0;
+            return best;
+        }
         best.us = few_us(num_cu, m, raw_n, kind == Product::GATED, (double)k * e, aligned_a && aligned_b);
     }
     auto consider = [&](Plan pl, int64_t t, int bm, int bn, int slots, double step, double tile) {
+        // HIP takes grids of fewer than 2^32 threads: 2^30 rows of 64 x 64 are past that
+        if (t * (pl.fast ? 512 : 256) >= int64_t(1) << 32) return;
         // weights that one or two row tiles read come from memory at its latency, two steps in flight
         if (m <= 2 * bm) step = std::max(step, 0.9);
         for (int s = 1, most = most_splits(t); s <= most; ++s) {
@@ -208,6 +213,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
                  + (best.splits > 1 ? (size_t)best.splits * m * best.part_ld * 4 : 0);
     return best;
 }
+
+// Whether any kernel's grid holds the product.
+bool planned(const Plan& pl) { return pl.us < 1e30; }
 
 // Workspace for any alignment of the operands.
 size_t product_bytes(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments)
@@ -277,6 +285,7 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
     if (two_b) aligned_b = aligned_b && fast_rows(p.b2, p.ldb2, (int64_t)(b_across ? p.N : p.K) * e);
     if (p.k_segments > 1) aligned_b = aligned_b && p.ldb == p.ldb2;
     const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b);
+    if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
     if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const Extent x = extent_of(kind, p.M, p.N, p.K);
@@ -338,8 +347,10 @@ mic_status forward_name(mic_handle h, Product kind, mic_dtype dtype, mic_dtype o
     MIC_TRY(product_type(dtype, out_dtype, &type, fast_sums != 0));
     if (!m || !n) return give_name("nothing", buf, buflen);
     const Aligned al = aligned_operands(kind, type, n, k, aligned != 0, false, 0);
+    const Plan pl = plan_product(cus_of(h), kind, type, m, n, k, 1, al.a, al.b);
+    if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
     char text[64];
-    describe(plan_product(cus_of(h), kind, type, m, n, k, 1, al.a, al.b), text, sizeof(text));
+    describe(pl, text, sizeof(text));
     return give_name(text, buf, buflen);
 }
 
@@ -386,10 +397,18 @@ mic_status backward_name(mic_handle h, mic_dtype dtype, bool own_dz, int m, int 
     const int two = gated ? 2 : 1;
     const int64_t pitch = align_up(n, 64);
     char dx[64] = "nothing", dw[64] = "nothing", text[160];
-    const Aligned in = aligned_operands(Product::INPUT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
-    if (m) describe(plan_product(cus_of(h), Product::INPUT_GRAD, type, m, k, n, two, in.a, in.b), dx, sizeof(dx));
-    const Aligned w = aligned_operands(Product::WEIGHT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
-    if (n) describe(plan_product(cus_of(h), Product::WEIGHT_GRAD, type, gated ? (int)(2 * pitch) : n, k, m, 1, w.a, w.b), dw, sizeof(dw));
+    if (m) {
+        const Aligned al = aligned_operands(Product::INPUT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
+        const Plan pl = plan_product(cus_of(h), Product::INPUT_GRAD, type, m, k, n, two, al.a, al.b);
+        if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
+        describe(pl, dx, sizeof(dx));
+    }
+    if (n) {
+        const Aligned al = aligned_operands(Product::WEIGHT_GRAD, type, n, k, aligned != 0, own_dz, two * pitch);
+        const Plan pl = plan_product(cus_of(h), Product::WEIGHT_GRAD, type, gated ? (int)(2 * pitch) : n, k, m, 1, al.a, al.b);
+        if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
+        describe(pl, dw, sizeof(dw));
+    }
     snprintf(text, sizeof(text), "dx: %s, dw: %s", dx, dw);
     return give_name(text, buf, buflen);
 }

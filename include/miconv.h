@@ -412,7 +412,8 @@ mic_status mic_brgemm_kernel_name(mic_handle handle, mic_dtype dtype, int m, int
  * Errors: MIC_STATUS_BAD_PARAM (null handle or needed pointer, negative size,
  * pitch below the row's length, misaligned pointer, workspace too small),
  * MIC_STATUS_NOT_SUPPORTED (element type or activation, a size reaching 2^30,
- * a row pitch of 2^23 bytes or more), MIC_STATUS_LAUNCH_FAILED. */
+ * a row pitch of 2^23 bytes or more, more outputs than a launch of 128 x 128
+ * tiles reaches, about 2^38), MIC_STATUS_LAUNCH_FAILED. */
 typedef enum {
     MIC_ACT_NONE = 0,
     MIC_ACT_RELU = 1,

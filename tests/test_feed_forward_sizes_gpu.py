@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import convolution_forward_conv2d_amd as mic
-from test_feed_forward_gpu import BF16, E4M3, dev
+from test_feed_forward_gpu import BF16, E4M3, F32, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,15 @@ def test_norm_of_more_rows_than_a_grid_takes(m, c):
             if out is E4M3:
                 assert torch.equal(r.scale[rows], want.scale), a
         del r
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_as_many_rows_as_there_may_be(dtype):
+    """2^30 - 1 rows of one feature: 2^24 tiles of 64 rows would be 2^32 threads.  An output is one product, rounded once."""
+    m = (1 << 30) - 1
+    x = torch.empty((m, 1), dtype=dtype, device=dev()).normal_(generator=torch.Generator(device=dev()).manual_seed(2))
+    w = torch.tensor([[1.25]], dtype=dtype, device=dev())
+    y = mic.linear(x, w)
+    for a in range(0, m, 1 << 27):
+        rows = slice(a, min(a + (1 << 27), m))
+        assert torch.equal(y[rows], (x[rows].float() * 1.25).to(dtype)), a
