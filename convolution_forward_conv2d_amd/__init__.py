@@ -127,6 +127,7 @@ _SIGS = {
     "mic_rms_norm_backward": ([_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
                                ctypes.c_size_t], _i),
     "mic_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_forward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
                             _vp, _i64, _vp, ctypes.c_size_t], _i),
     "mic_linear_forward_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
@@ -134,12 +135,15 @@ _SIGS = {
     "mic_linear_backward_kernel_name": ([_vp, _i, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
     "mic_gated_linear_backward_kernel_name": ([_vp, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
     "mic_linear_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_backward_workspace_aligned": ([_vp, _i, _i, _i, _i, _i, _szp], _i),
     "mic_linear_backward": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                              _i64, _vp, _vp, ctypes.c_size_t], _i),
     "mic_gated_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_gated_linear_forward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_gated_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
                                   _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t], _i),
     "mic_gated_linear_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_gated_linear_backward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_gated_linear_backward": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                                    _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_size_t], _i),
 }
@@ -409,12 +413,22 @@ def mic_linear_forward_workspace(handle, dtype, m, n, k):
     return _bytes(lib().mic_linear_forward_workspace, "mic_linear_forward_workspace", handle, dtype, m, n, k)
 
 
+def mic_linear_forward_workspace_aligned(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_forward_workspace_aligned, "mic_linear_forward_workspace_aligned", handle,
+                  dtype, m, n, k)
+
+
 def mic_linear_forward(*args):
     _check(lib().mic_linear_forward(*args), "mic_linear_forward")
 
 
 def mic_linear_backward_workspace(handle, dtype, m, n, k):
     return _bytes(lib().mic_linear_backward_workspace, "mic_linear_backward_workspace", handle, dtype, m, n, k)
+
+
+def mic_linear_backward_workspace_aligned(handle, dtype, act, m, n, k):
+    return _bytes(lib().mic_linear_backward_workspace_aligned, "mic_linear_backward_workspace_aligned", handle,
+                  dtype, act, m, n, k)
 
 
 def mic_linear_backward(*args):
@@ -426,6 +440,11 @@ def mic_gated_linear_forward_workspace(handle, dtype, m, n, k):
                   n, k)
 
 
+def mic_gated_linear_forward_workspace_aligned(handle, dtype, m, n, k):
+    return _bytes(lib().mic_gated_linear_forward_workspace_aligned, "mic_gated_linear_forward_workspace_aligned", handle,
+                  dtype, m, n, k)
+
+
 def mic_gated_linear_forward(*args):
     _check(lib().mic_gated_linear_forward(*args), "mic_gated_linear_forward")
 
@@ -433,6 +452,11 @@ def mic_gated_linear_forward(*args):
 def mic_gated_linear_backward_workspace(handle, dtype, m, n, k):
     return _bytes(lib().mic_gated_linear_backward_workspace, "mic_gated_linear_backward_workspace", handle, dtype, m,
                   n, k)
+
+
+def mic_gated_linear_backward_workspace_aligned(handle, dtype, m, n, k):
+    return _bytes(lib().mic_gated_linear_backward_workspace_aligned, "mic_gated_linear_backward_workspace_aligned", handle,
+                  dtype, m, n, k)
 
 
 def mic_gated_linear_backward(*args):

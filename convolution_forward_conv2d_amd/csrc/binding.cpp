@@ -105,6 +105,13 @@ Tensor rows_of(const Tensor& x, int64_t cols, at::ScalarType type)
 
 Tensor like(const Tensor& t, at::ScalarType type) { return at::empty(t.sizes(), t.options().dtype(type)); }
 
+// Whether the rows of a contiguous matrix count as aligned: a call on such operands copies none.
+bool even(const Tensor& t)
+{
+    const int64_t pitch = t.size(-1) * (int64_t)t.element_size();
+    return (reinterpret_cast<uintptr_t>(t.data_ptr()) | (uintptr_t)pitch) % 16 == 0 && pitch < int64_t(1) << 22;
+}
+
 // A workspace of the size the library asks for; sizes are kept by call and shape.
 template <class Ask> bool workspace(int call, mic_dtype d, int64_t m, int64_t n, int64_t k, const Tensor& x, Tensor& space,
                                     size_t& bytes, Ask ask)
@@ -261,10 +268,12 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const long act = PyLong_AsLong(a[4]);
     if (act == -1 && PyErr_Occurred()) return nullptr;
     const mic_handle h = handle_on(x->get_device());
+    const bool aligned = even(*x) && even(*w);
     Tensor space;
     size_t bytes;
-    if (!h || !workspace(1, d, m, n, k, *x, space, bytes, [&](size_t* b) {
-            return mic_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
+    if (!h || !workspace(aligned ? 5 : 1, d, m, n, k, *x, space, bytes, [&](size_t* b) {
+            return aligned ? mic_linear_forward_workspace_aligned(h, d, (int)m, (int)n, (int)k, b)
+                           : mic_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
     Tensor y = rows_of(*x, n, out), z;
@@ -298,10 +307,12 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         || (act && (!pre || !plain_matrix(*pre, type, *dy, m, n))))
         return none();
     const mic_handle h = handle_on(dy->get_device());
+    const bool aligned = even(*x) && even(*w) && (act || even(*dy));
     Tensor space;
     size_t bytes;
-    if (!h || !workspace(2, d, m, n, k, *dy, space, bytes, [&](size_t* b) {
-            return mic_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
+    if (!h || !workspace(aligned ? act ? 6 : 7 : 2, d, m, n, k, *dy, space, bytes, [&](size_t* b) {
+            return aligned ? mic_linear_backward_workspace_aligned(h, d, (mic_activation)act, (int)m, (int)n, (int)k, b)
+                           : mic_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
     Tensor dx = like(*x, type), dw = like(*w, type), db;
@@ -337,10 +348,12 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const long act = PyLong_AsLong(a[3]);
     if (act == -1 && PyErr_Occurred()) return nullptr;
     const mic_handle h = handle_on(x->get_device());
+    const bool aligned = even(*x) && even(*wg) && even(*wu);
     Tensor space;
     size_t bytes;
-    if (!h || !workspace(3, d, m, n, k, *x, space, bytes, [&](size_t* b) {
-            return mic_gated_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
+    if (!h || !workspace(aligned ? 8 : 3, d, m, n, k, *x, space, bytes, [&](size_t* b) {
+            return aligned ? mic_gated_linear_forward_workspace_aligned(h, d, (int)m, (int)n, (int)k, b)
+                           : mic_gated_linear_forward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
     Tensor y = rows_of(*x, n, out), gate, up;
@@ -374,10 +387,12 @@ PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args
         || !plain(*wu, type, *dy, {n, k}) || !plain_matrix(*gate, type, *dy, m, n) || !plain_matrix(*up, type, *dy, m, n))
         return none();
     const mic_handle h = handle_on(dy->get_device());
+    const bool aligned = even(*x) && even(*wg) && even(*wu);
     Tensor space;
     size_t bytes;
-    if (!h || !workspace(4, d, m, n, k, *dy, space, bytes, [&](size_t* b) {
-            return mic_gated_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
+    if (!h || !workspace(aligned ? 9 : 4, d, m, n, k, *dy, space, bytes, [&](size_t* b) {
+            return aligned ? mic_gated_linear_backward_workspace_aligned(h, d, (int)m, (int)n, (int)k, b)
+                           : mic_gated_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
     Tensor dx = like(*x, type), dg = like(*wg, type), du = like(*wu, type);

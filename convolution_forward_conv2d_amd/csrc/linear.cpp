@@ -228,11 +228,6 @@ size_t product_bytes(int num_cu, Product kind, ProductType type, int m, int n, i
     return most;
 }
 
-bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes)
-{
-    return aligned(p, 16) && ld % 16 == 0 && bytes % 16 == 0 && ld < kMaxPitchBytes / 2;
-}
-
 // Which of a product's operands can be read 16 bytes at a time, where the caller says that every operand's pointer and
 // pitch is a multiple of 16 bytes (`aligned`).  A gradient's dz is the library's own (`own_dz`) unless it is dy.
 struct Aligned {
@@ -247,6 +242,16 @@ Aligned aligned_operands(Product kind, ProductType type, int n, int k, bool alig
     if (kind == Product::FORWARD || kind == Product::GATED) return {x, x};
     return {own_dz ? even(dz_pitch) : aligned && even(n), x};
 }
+
+// The same for operands of known alignment.
+size_t aligned_bytes(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, Aligned al)
+{
+    return m && n ? plan_product(num_cu, kind, type, m, n, k, k_segments, al.a, al.b).bytes : 0;
+}
+
+// A matrix that counts as aligned (its rows' length is looked at where it matters).
+bool aligned_matrix(const void* p, int64_t ld_bytes) { return aligned(p, 16) && ld_bytes % 16 == 0 && ld_bytes < kMaxPitchBytes / 2; }
+bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes) { return aligned_matrix(p, ld) && bytes % 16 == 0; }
 
 void describe(const Plan& pl, char* text, size_t size)
 {
@@ -326,7 +331,7 @@ mic_status product_type(mic_dtype in, mic_dtype out, ProductType* type, bool fas
     return MIC_STATUS_SUCCESS;
 }
 
-mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m, int n, int k, size_t* bytes)
+mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m, int n, int k, bool aligned, size_t* bytes)
 {
     if (!bytes) return MIC_STATUS_BAD_PARAM;
     MIC_TRY(check_sizes(m, n, k));
@@ -334,7 +339,11 @@ mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m,
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &type));
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &fast, true));
     *bytes = most_bytes(h, [&](int cus) {
-        return std::max(product_bytes(cus, kind, type, m, n, k, 1), product_bytes(cus, kind, fast, m, n, k, 1));
+        auto need = [&](ProductType t) {
+            if (!aligned) return product_bytes(cus, kind, t, m, n, k, 1);
+            return aligned_bytes(cus, kind, t, m, n, k, 1, aligned_operands(kind, t, n, k, true, false, 0));
+        };
+        return std::max(need(type), need(fast));
     });
     return MIC_STATUS_SUCCESS;
 }
@@ -360,21 +369,31 @@ struct GradLayout {
     size_t dz, sums, product, total;
 };
 
-GradLayout grad_layout(int num_cu, ProductType type, int m, int n, int k, bool gated, bool bias)
+// `aligned`: every operand is; without an activation (own_dz false) dz is then dy, read where it is and never copied.
+GradLayout grad_layout(int num_cu, ProductType type, int m, int n, int k, bool gated, bool bias, bool aligned, bool own_dz)
 {
     GradLayout g = {};
     const int two = gated ? 2 : 1;
     g.pitch = align_up(n, 64);
-    g.dz = (size_t)align_up((int64_t)m * g.pitch * two * (type == ProductType::F32 ? 4 : 2), 256);
+    if (own_dz) g.dz = (size_t)align_up((int64_t)m * g.pitch * two * (type == ProductType::F32 ? 4 : 2), 256);
     g.sums = bias ? (size_t)align_up((int64_t)miconv::slope_row_groups(m, n) * n * 4, 256) : 0;
-    const size_t a = product_bytes(num_cu, Product::INPUT_GRAD, type, m, k, n, two);
-    const size_t b = product_bytes(num_cu, Product::WEIGHT_GRAD, type, (int)(gated ? 2 * g.pitch : n), k, m, 1);
-    g.product = std::max(a, b);
+    const int wide = (int)(gated ? 2 * g.pitch : n);
+    if (aligned) {
+        auto bytes = [&](Product kind, int rows, int columns, int terms, int segments) {
+            return aligned_bytes(num_cu, kind, type, rows, columns, terms, segments,
+                                 aligned_operands(kind, type, n, k, true, own_dz, two * g.pitch));
+        };
+        g.product = std::max(bytes(Product::INPUT_GRAD, m, k, n, two), bytes(Product::WEIGHT_GRAD, wide, k, m, 1));
+    } else {
+        g.product = std::max(product_bytes(num_cu, Product::INPUT_GRAD, type, m, k, n, two),
+                             product_bytes(num_cu, Product::WEIGHT_GRAD, type, wide, k, m, 1));
+    }
     g.total = g.dz + g.sums + g.product;
     return g;
 }
 
-mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k, bool gated, size_t* bytes)
+mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k, bool gated, bool aligned, bool own_dz,
+                              size_t* bytes)
 {
     if (!bytes) return MIC_STATUS_BAD_PARAM;
     MIC_TRY(check_sizes(m, n, k));
@@ -382,7 +401,7 @@ mic_status backward_workspace(mic_handle h, mic_dtype dtype, int m, int n, int k
     if (n >= kMaxSize / 2) return MIC_STATUS_NOT_SUPPORTED;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    *bytes = most_bytes(h, [&](int cus) { return grad_layout(cus, type, m, n, k, gated, !gated).total; });
+    *bytes = most_bytes(h, [&](int cus) { return grad_layout(cus, type, m, n, k, gated, !gated, aligned, own_dz).total; });
     return MIC_STATUS_SUCCESS;
 }
 
@@ -508,7 +527,12 @@ mic_status mic_rms_norm_backward(mic_handle handle, mic_dtype dtype, int rows, i
 
 mic_status mic_linear_forward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
 {
-    return forward_workspace(handle, Product::FORWARD, dtype, m, n, k, bytes);
+    return forward_workspace(handle, Product::FORWARD, dtype, m, n, k, false, bytes);
+}
+
+mic_status mic_linear_forward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
+{
+    return forward_workspace(handle, Product::FORWARD, dtype, m, n, k, true, bytes);
 }
 
 mic_status mic_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, mic_activation act,
@@ -571,7 +595,14 @@ mic_status mic_gated_linear_backward_kernel_name(mic_handle handle, mic_dtype dt
 
 mic_status mic_linear_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
 {
-    return backward_workspace(handle, dtype, m, n, k, false, bytes);
+    return backward_workspace(handle, dtype, m, n, k, false, false, true, bytes);
+}
+
+mic_status mic_linear_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
+                                                 size_t* bytes)
+{
+    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
+    return backward_workspace(handle, dtype, m, n, k, false, true, act != MIC_ACT_NONE, bytes);
 }
 
 mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
@@ -580,11 +611,13 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
                                void* dbias, void* workspace, size_t workspace_bytes)
 {
     if (!handle) return MIC_STATUS_BAD_PARAM;
-    size_t need;
-    MIC_TRY(backward_workspace(handle, dtype, m, n, k, false, &need));
-    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
     const size_t e = size_of(dtype);
     const bool slope = act != MIC_ACT_NONE;
+    const bool even = (!dw || aligned_matrix(x, ldx * (int64_t)e)) && (!dx || aligned_matrix(w, ldw * (int64_t)e))
+                      && (slope || aligned_matrix(dy, lddy * (int64_t)e));
+    size_t need;
+    MIC_TRY(backward_workspace(handle, dtype, m, n, k, false, even, slope || !even, &need));
+    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
     MIC_TRY(check_matrix(dy, lddy, m, n, e));
     if (slope) MIC_TRY(check_matrix(preact, ldp, m, n, e));
     if (dw) MIC_TRY(check_matrix(x, ldx, m, k, e));
@@ -596,7 +629,7 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
     if (n == 0 && (!dx || k == 0)) return MIC_STATUS_SUCCESS;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, false, true);
+    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, false, true, even, slope || !even);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     // without an activation dz is dy, read where it is
     const bool own = slope && (dx || dw);
@@ -616,7 +649,12 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
 
 mic_status mic_gated_linear_forward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
 {
-    return forward_workspace(handle, Product::GATED, dtype, m, n, k, bytes);
+    return forward_workspace(handle, Product::GATED, dtype, m, n, k, false, bytes);
+}
+
+mic_status mic_gated_linear_forward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
+{
+    return forward_workspace(handle, Product::GATED, dtype, m, n, k, true, bytes);
 }
 
 mic_status mic_gated_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, mic_activation act,
@@ -663,7 +701,12 @@ mic_status mic_gated_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtyp
 mic_status mic_gated_linear_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k,
                                                size_t* bytes)
 {
-    return backward_workspace(handle, dtype, m, n, k, true, bytes);
+    return backward_workspace(handle, dtype, m, n, k, true, false, true, bytes);
+}
+
+mic_status mic_gated_linear_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes)
+{
+    return backward_workspace(handle, dtype, m, n, k, true, true, true, bytes);
 }
 
 mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
@@ -674,10 +717,12 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
                                      size_t workspace_bytes)
 {
     if (!handle) return MIC_STATUS_BAD_PARAM;
-    size_t need;
-    MIC_TRY(backward_workspace(handle, dtype, m, n, k, true, &need));
-    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
     const size_t e = size_of(dtype);
+    const bool even = (!dw_gate || aligned_matrix(x, ldx * (int64_t)e))
+                      && (!dx || (aligned_matrix(w_gate, ldg * (int64_t)e) && aligned_matrix(w_up, ldu * (int64_t)e) && ldg == ldu));
+    size_t need;
+    MIC_TRY(backward_workspace(handle, dtype, m, n, k, true, even, true, &need));
+    if (!valid_act(act)) return MIC_STATUS_NOT_SUPPORTED;
     MIC_TRY(check_matrix(dy, lddy, m, n, e));
     MIC_TRY(check_matrix(gate, ldgate, m, n, e));
     MIC_TRY(check_matrix(up, ldup, m, n, e));
@@ -696,7 +741,7 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
     if ((!dx && !dw_gate) || k == 0) return MIC_STATUS_SUCCESS;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
-    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, true, false);
+    const GradLayout g = grad_layout(handle->num_cu, type, m, n, k, true, false, even, true);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (m && n) {
         miconv::SlopeArgs s = {};

@@ -130,6 +130,12 @@ def _weights(w, k, dtype, device, what):
     return _matrix(w, w.shape[0], k, dtype, device, what)
 
 
+def _even(*matrices):
+    """Whether every (tensor, pitch) has rows that count as aligned, so a call on them copies none."""
+    return all((t.data_ptr() | pitch * t.element_size()) % 16 == 0 and pitch * t.element_size() < 1 << 22
+               for t, pitch in matrices)
+
+
 def _workspace(fn, h, like, *sizes):
     key = (fn, like.device.index, sizes)
     n = _bytes_of.get(key)
@@ -307,7 +313,8 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
     shape = x.shape[:-1] + (n,)
     y = x.new_empty(shape, dtype=out_dtype)
     z = torch.empty_like(y) if return_preact else None
-    wk, wkp, wkn = _workspace("mic_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
+    fn = "mic_linear_forward_workspace" + ("_aligned" if _even((x, ldx), (w, ldw)) else "")
+    wk, wkp, wkn = _workspace(fn, h, x, _CODE[dtype], m, n, k)
     _call("mic_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, fast_sums, m, n, k, x.data_ptr(), ldx, w.data_ptr(), ldw,
           xs, ws, bp, _ptr(residual), ldr, y.data_ptr(), n, _ptr(z), n, wkp, wkn)
     return (y, z) if return_preact else y
@@ -340,7 +347,10 @@ def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
     dx = _empty(x.shape, x, dtype)
     dw = _empty(w.shape, w, dtype)
     dbias = dy.new_empty(n) if bias else None
-    wk, wkp, wkn = _workspace("mic_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
+    if _even((x, ldx), (w, ldw)) and (act or _even((dy, lddy))):
+        wk, wkp, wkn = _workspace("mic_linear_backward_workspace_aligned", h, dy, _CODE[dtype], act, m, n, k)
+    else:
+        wk, wkp, wkn = _workspace("mic_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
     _call("mic_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
           ldw, _ptr(preact) if act else 0, ldp, dx.data_ptr(), k, dw.data_ptr(), k, _ptr(dbias), wkp, wkn)
     return dx, dw, dbias
@@ -377,7 +387,8 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
     y = x.new_empty(shape, dtype=out_dtype)
     gate = torch.empty_like(y) if return_products else None
     up = torch.empty_like(y) if return_products else None
-    wk, wkp, wkn = _workspace("mic_gated_linear_forward_workspace", h, x, _CODE[dtype], m, n, k)
+    fn = "mic_gated_linear_forward_workspace" + ("_aligned" if _even((x, ldx), (w_gate, ldg), (w_up, ldu)) and ldg == ldu else "")
+    wk, wkp, wkn = _workspace(fn, h, x, _CODE[dtype], m, n, k)
     _call("mic_gated_linear_forward", h, _CODE[dtype], _CODE[out_dtype], act, fast_sums, m, n, k, x.data_ptr(), ldx,
           w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, xs, gs, us, y.data_ptr(), n, _ptr(gate), n, _ptr(up), n, wkp,
           wkn)
@@ -408,7 +419,8 @@ def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu"):
     dx = _empty(x.shape, x, dtype)
     dwg = _empty(w_gate.shape, w_gate, dtype)
     dwu = _empty(w_up.shape, w_up, dtype)
-    wk, wkp, wkn = _workspace("mic_gated_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
+    fn = "mic_gated_linear_backward_workspace" + ("_aligned" if _even((x, ldx), (w_gate, ldg), (w_up, ldu)) and ldg == ldu else "")
+    wk, wkp, wkn = _workspace(fn, h, dy, _CODE[dtype], m, n, k)
     _call("mic_gated_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx,
           w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, gate.data_ptr(), ldgate, up.data_ptr(), ldup, dx.data_ptr(), k,
           dwg.data_ptr(), k, dwu.data_ptr(), k, wkp, wkn)

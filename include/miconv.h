@@ -406,7 +406,10 @@ mic_status mic_brgemm_kernel_name(mic_handle handle, mic_dtype dtype, int m, int
  * bytes the matching ..._workspace call (host only) returns for the same sizes
  * and handle, or without a handle, which answers for an MI355X whole or in any
  * of its partitions; their contents need no preparation and nothing in them
- * survives a call.  Calls are asynchronous on the handle's stream and may be captured
+ * survives a call.  Those bytes are enough for rows at any alignment, which may
+ * have to be copied; ..._workspace_aligned returns what a call needs, often
+ * nothing, whose operands' pointers and pitches are all multiples of 16 bytes
+ * with pitches below 4 MB (and w_gate's that of w_up).  Calls are asynchronous on the handle's stream and may be captured
  * into graphs.  Results do not depend on workgroup order: no atomics.
  *
  * Errors: MIC_STATUS_BAD_PARAM (null handle or needed pointer, negative size,
@@ -456,6 +459,7 @@ mic_status mic_rms_norm_backward(mic_handle handle, mic_dtype dtype, int rows, i
  * to 2^-11 of that one): far below a bf16 output's rounding unless the sum
  * nearly cancels. */
 mic_status mic_linear_forward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_linear_forward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
 mic_status mic_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, mic_activation act,
                               int fast_sums, int m, int n, int k, const void* x, int64_t ldx, const void* w, int64_t ldw,
                               const float* x_scale, const float* w_scale, const void* bias, const void* residual,
@@ -468,6 +472,8 @@ mic_status mic_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_
  * computed (w is needed for dx only, x for dw only).  The residual's gradient
  * is dy itself.  dz enters the products in the tensors' type. */
 mic_status mic_linear_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_linear_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
+                                                 size_t* bytes);
 mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
                                const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
                                const void* preact, int64_t ldp, void* dx, int64_t lddx, void* dw, int64_t lddw,
@@ -477,6 +483,8 @@ mic_status mic_linear_backward(mic_handle handle, mic_dtype dtype, mic_activatio
  * y[m,n] = act(gate[m,n]) * up[m,n].  gate and up (both or neither null)
  * receive the two products, which the gradient needs. */
 mic_status mic_gated_linear_forward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_gated_linear_forward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k,
+                                                      size_t* bytes);
 mic_status mic_gated_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, mic_activation act,
                                     int fast_sums, int m, int n, int k, const void* x, int64_t ldx, const void* w_gate,
                                     int64_t ldg, const void* w_up, int64_t ldu, const float* x_scale,
@@ -489,6 +497,8 @@ mic_status mic_gated_linear_forward(mic_handle handle, mic_dtype dtype, mic_dtyp
  * F32 or BF16.  dx may be null, and dw_gate and dw_up together. */
 mic_status mic_gated_linear_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k,
                                                size_t* bytes);
+mic_status mic_gated_linear_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k,
+                                                       size_t* bytes);
 mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_activation act, int m, int n, int k,
                                      const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w_gate,
                                      int64_t ldg, const void* w_up, int64_t ldu, const void* gate, int64_t ldgate,
@@ -500,9 +510,8 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
  * bytes (MIC_STATUS_BAD_PARAM if it does not fit; 128 do): "few" rows, large
  * tiles ("fast 256x192") or small ones through registers ("any 64x64"), in how
  * many parts the reduction is split and which operands are packed first; a
- * gradient's as "dx: ..., dw: ...".  aligned: whether all operands' pointers and
- * pitches are multiples of 16 bytes, pitches below 4 MB and w_gate's that of
- * w_up.  Without a handle the answer is that of a whole MI355X.  Errors as the
+ * gradient's as "dx: ..., dw: ...".  aligned: as ..._workspace_aligned's operands.
+ * Without a handle the answer is that of a whole MI355X.  Errors as the
  * call's own checks of sizes and types. */
 mic_status mic_linear_forward_kernel_name(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int fast_sums, int m,
                                           int n, int k, int aligned, char* buf, size_t buflen);
