@@ -203,16 +203,18 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
-// (dy, sum, weight, rstd, dsum) -> (dx, dweight)
+// (dy, sum, weight, rstd, dsum, need_dweight) -> (dx, dweight or None)
 PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     const Tensor *dy, *sum, *w, *rstd, *dsum;
     int64_t rows, cols;
     mic_dtype d;
-    if (n_args != 5 || !plain_rows(dy = tensor(a[0]), rows, cols) || !(sum = tensor(a[1])) || !(w = tensor(a[2]))
+    if (n_args != 6 || !plain_rows(dy = tensor(a[0]), rows, cols) || !(sum = tensor(a[1])) || !(w = tensor(a[2]))
         || !(rstd = tensor(a[3])) || !maybe(a[4], dsum))
         return none();
+    bool need_dw;
+    if (!flag(a[5], "need_dweight", need_dw)) return nullptr;
     const auto type = dy->scalar_type();
     if (!dtype_of(*dy, d) || d == MIC_DTYPE_F8_E4M3 || !plain_matrix(*sum, type, *dy, rows, cols)
         || !plain(*w, type, *dy, {cols}) || !plain_scale(*rstd, *dy, rows)
@@ -220,18 +222,19 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         return none();
     const mic_handle h = handle_on(dy->get_device());
     Tensor space;
-    size_t bytes;
-    if (!h || !workspace(0, d, rows, cols, 0, *dy, space, bytes, [&](size_t* b) {
+    size_t bytes = 0;
+    if (!h || (need_dw && !workspace(0, d, rows, cols, 0, *dy, space, bytes, [&](size_t* b) {
             return mic_rms_norm_backward_workspace(h, (int)rows, (int)cols, b);
-        }))
+        })))
         return none();
-    Tensor dx = like(*dy, type), dw = like(*w, type);
+    Tensor dx = like(*dy, type), dw;
+    if (need_dw) dw = like(*w, type);
     if (mic_rms_norm_backward(h, d, (int)rows, (int)cols, dy->data_ptr(), cols, sum->data_ptr(), cols, w->data_ptr(),
-                              floats(rstd), data(dsum), cols, dx.data_ptr(), cols, dw.data_ptr(),
+                              floats(rstd), data(dsum), cols, dx.data_ptr(), cols, need_dw ? dw.data_ptr() : nullptr,
                               bytes ? space.data_ptr() : nullptr, bytes)
         != MIC_STATUS_SUCCESS)
         return none();
-    return pack({wrap(dx), wrap(dw)});
+    return pack({wrap(dx), need_dw ? wrap(dw) : none()});
     END_HANDLE_TH_ERRORS
 }
 
@@ -287,18 +290,18 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
-// (dy, x, w, preact, act, bias) -> (dx, dw, dbias or None)
+// (dy, x, w, preact, act, bias, need_dx, need_dw) -> (dx, dw, dbias), each None where not asked for
 PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     const Tensor *dy, *x, *w, *pre;
     int64_t m, n;
     mic_dtype d;
-    if (n_args != 6 || !plain_rows(dy = tensor(a[0]), m, n) || !(x = tensor(a[1])) || !(w = tensor(a[2]))
+    if (n_args != 8 || !plain_rows(dy = tensor(a[0]), m, n) || !(x = tensor(a[1])) || !(w = tensor(a[2]))
         || !maybe(a[3], pre) || !dtype_of(*dy, d) || d == MIC_DTYPE_F8_E4M3 || x->dim() < 1)
         return none();
-    bool bias;
-    if (!flag(a[5], "bias", bias)) return nullptr;
+    bool bias, need_dx, need_dw;
+    if (!flag(a[5], "bias", bias) || !flag(a[6], "need_dx", need_dx) || !flag(a[7], "need_dw", need_dw)) return nullptr;
     const long act = PyLong_AsLong(a[4]);
     if (act == -1 && PyErr_Occurred()) return nullptr;
     const auto type = dy->scalar_type();
@@ -315,14 +318,17 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
                            : mic_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
-    Tensor dx = like(*x, type), dw = like(*w, type), db;
+    Tensor dx, dw, db;
+    if (need_dx) dx = like(*x, type);
+    if (need_dw) dw = like(*w, type);
     if (bias) db = at::empty({n}, dy->options());
     if (mic_linear_backward(h, d, (mic_activation)act, (int)m, (int)n, (int)k, dy->data_ptr(), n, x->data_ptr(), k,
-                            w->data_ptr(), k, act ? data(pre) : nullptr, n, dx.data_ptr(), k, dw.data_ptr(), k,
+                            w->data_ptr(), k, act ? data(pre) : nullptr, n, need_dx ? dx.data_ptr() : nullptr, k,
+                            need_dw ? dw.data_ptr() : nullptr, k,
                             bias ? db.data_ptr() : nullptr, bytes ? space.data_ptr() : nullptr, bytes)
         != MIC_STATUS_SUCCESS)
         return none();
-    return pack({wrap(dx), wrap(dw), bias ? wrap(db) : none()});
+    return pack({need_dx ? wrap(dx) : none(), need_dw ? wrap(dw) : none(), bias ? wrap(db) : none()});
     END_HANDLE_TH_ERRORS
 }
 
@@ -368,17 +374,19 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
-// (dy, x, w_gate, w_up, gate, up, act) -> (dx, dw_gate, dw_up)
+// (dy, x, w_gate, w_up, gate, up, act, need_dx, need_dw) -> (dx, dw_gate, dw_up), each None where not asked for
 PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
     const Tensor *dy, *x, *wg, *wu, *gate, *up;
     int64_t m, n;
     mic_dtype d;
-    if (n_args != 7 || !plain_rows(dy = tensor(a[0]), m, n) || !(x = tensor(a[1])) || !(wg = tensor(a[2]))
+    if (n_args != 9 || !plain_rows(dy = tensor(a[0]), m, n) || !(x = tensor(a[1])) || !(wg = tensor(a[2]))
         || !(wu = tensor(a[3])) || !(gate = tensor(a[4])) || !(up = tensor(a[5])) || !dtype_of(*dy, d)
         || d == MIC_DTYPE_F8_E4M3 || x->dim() < 1)
         return none();
+    bool need_dx, need_dw;
+    if (!flag(a[7], "need_dx", need_dx) || !flag(a[8], "need_dw", need_dw)) return nullptr;
     const long act = PyLong_AsLong(a[6]);
     if (act == -1 && PyErr_Occurred()) return nullptr;
     const auto type = dy->scalar_type();
@@ -395,14 +403,17 @@ PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args
                            : mic_gated_linear_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
         }))
         return none();
-    Tensor dx = like(*x, type), dg = like(*wg, type), du = like(*wu, type);
+    Tensor dx, dg, du;
+    if (need_dx) dx = like(*x, type);
+    if (need_dw) dg = like(*wg, type), du = like(*wu, type);
     if (mic_gated_linear_backward(h, d, (mic_activation)act, (int)m, (int)n, (int)k, dy->data_ptr(), n, x->data_ptr(), k,
                                   wg->data_ptr(), k, wu->data_ptr(), k, gate->data_ptr(), n, up->data_ptr(), n,
-                                  dx.data_ptr(), k, dg.data_ptr(), k, du.data_ptr(), k,
+                                  need_dx ? dx.data_ptr() : nullptr, k, need_dw ? dg.data_ptr() : nullptr, k,
+                                  need_dw ? du.data_ptr() : nullptr, k,
                                   bytes ? space.data_ptr() : nullptr, bytes)
         != MIC_STATUS_SUCCESS)
         return none();
-    return pack({wrap(dx), wrap(dg), wrap(du)});
+    return pack({need_dx ? wrap(dx) : none(), need_dw ? wrap(dg) : none(), need_dw ? wrap(du) : none()});
     END_HANDLE_TH_ERRORS
 }
 

@@ -216,14 +216,16 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out_dtype=None):
     return RmsNorm(y, total, rstd, scale)
 
 
-def rms_norm_backward(dy, sum, weight, rstd, dsum=None):
+def rms_norm_backward(dy, sum, weight, rstd, dsum=None, need_dweight=True):
     """(dx, dweight) of rms_norm, from its sum and rstd; dx is residual's gradient too.
 
     dsum: the gradient that reaches sum past the norm (added to dx).
+    dweight is None, and not computed, where need_dweight is false.
     """
-    r = (_native or _load()).rms_norm_backward(dy, sum, weight, rstd, dsum)
+    r = (_native or _load()).rms_norm_backward(dy, sum, weight, rstd, dsum, need_dweight)
     if r is not None:
         return r
+    need_dweight = _flag(need_dweight, "need_dweight")
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     dtype, device = dy.dtype, dy.device
     cols = dy.shape[-1] if dy.dim() else 0
@@ -237,10 +239,10 @@ def rms_norm_backward(dy, sum, weight, rstd, dsum=None):
     ldd = 0 if dsum is None else _matrix(dsum, rows, cols, dtype, device, "dsum")
     h = _handle(device)
     dx = _empty(dy.shape, dy, dtype)
-    dweight = torch.empty_like(weight)
-    ws, wsp, wsn = _workspace("mic_rms_norm_backward_workspace", h, dy, rows, cols)
+    dweight = torch.empty_like(weight) if need_dweight else None
+    ws, wsp, wsn = _workspace("mic_rms_norm_backward_workspace", h, dy, rows, cols) if need_dweight else (None, 0, 0)
     _call("mic_rms_norm_backward", h, _CODE[dtype], rows, cols, dy.data_ptr(), lddy, sum.data_ptr(), lds, wp,
-          rstd.data_ptr(), _ptr(dsum), ldd, dx.data_ptr(), cols, dweight.data_ptr(), wsp, wsn)
+          rstd.data_ptr(), _ptr(dsum), ldd, dx.data_ptr(), cols, _ptr(dweight), wsp, wsn)
     return dx, dweight
 
 
@@ -320,17 +322,19 @@ def linear(x, w, bias=None, residual=None, activation="none", x_scale=None, w_sc
     return (y, z) if return_preact else y
 
 
-def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
+def linear_backward(dy, x, w, preact=None, activation="none", bias=False, need_dx=True, need_dw=True):
     """(dx, dw, dbias) of linear, from its inputs and preact (None without an activation).
 
-    dbias is None unless bias is true.  The residual's gradient is dy.
+    dbias is None unless bias is true, and dx and dw are where need_dx and
+    need_dw are false (a first layer, frozen weights): what is None is not
+    computed.  The residual's gradient is dy.
     """
     act = mic.ACTIVATIONS.get(activation)
     if act is not None:
-        r = (_native or _load()).linear_backward(dy, x, w, preact, act, bias)
+        r = (_native or _load()).linear_backward(dy, x, w, preact, act, bias, need_dx, need_dw)
         if r is not None:
             return r
-    bias = _flag(bias, "bias")
+    bias, need_dx, need_dw = _flag(bias, "bias"), _flag(need_dx, "need_dx"), _flag(need_dw, "need_dw")
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     act, dtype, device = _act(activation), dy.dtype, dy.device
     n = dy.shape[-1] if dy.dim() else 0
@@ -344,15 +348,15 @@ def linear_backward(dy, x, w, preact=None, activation="none", bias=False):
         raise ValueError("the gradient of activation %r needs preact" % activation)
     ldp = _matrix(preact, m, n, dtype, device, "preact") if act else 0
     h = _handle(device)
-    dx = _empty(x.shape, x, dtype)
-    dw = _empty(w.shape, w, dtype)
+    dx = _empty(x.shape, x, dtype) if need_dx else None
+    dw = _empty(w.shape, w, dtype) if need_dw else None
     dbias = dy.new_empty(n) if bias else None
     if _even((x, ldx), (w, ldw)) and (act or _even((dy, lddy))):
         wk, wkp, wkn = _workspace("mic_linear_backward_workspace_aligned", h, dy, _CODE[dtype], act, m, n, k)
     else:
         wk, wkp, wkn = _workspace("mic_linear_backward_workspace", h, dy, _CODE[dtype], m, n, k)
     _call("mic_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
-          ldw, _ptr(preact) if act else 0, ldp, dx.data_ptr(), k, dw.data_ptr(), k, _ptr(dbias), wkp, wkn)
+          ldw, _ptr(preact) if act else 0, ldp, _ptr(dx), k, _ptr(dw), k, _ptr(dbias), wkp, wkn)
     return dx, dw, dbias
 
 
@@ -395,13 +399,18 @@ def gated_linear(x, w_gate, w_up, activation="silu", x_scale=None, w_gate_scale=
     return (y, gate, up) if return_products else y
 
 
-def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu"):
-    """(dx, dw_gate, dw_up) of gated_linear, from its inputs and two products."""
+def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu", need_dx=True, need_dw=True):
+    """(dx, dw_gate, dw_up) of gated_linear, from its inputs and two products.
+
+    dx is None where need_dx is false, both weights' gradients where need_dw is:
+    what is None is not computed.
+    """
     act = mic.ACTIVATIONS.get(activation)
     if act is not None:
-        r = (_native or _load()).gated_linear_backward(dy, x, w_gate, w_up, gate, up, act)
+        r = (_native or _load()).gated_linear_backward(dy, x, w_gate, w_up, gate, up, act, need_dx, need_dw)
         if r is not None:
             return r
+    need_dx, need_dw = _flag(need_dx, "need_dx"), _flag(need_dw, "need_dw")
     _gpu(dy, "dy", (torch.float32, torch.bfloat16))
     act, dtype, device = _act(activation), dy.dtype, dy.device
     n = dy.shape[-1] if dy.dim() else 0
@@ -416,12 +425,12 @@ def gated_linear_backward(dy, x, w_gate, w_up, gate, up, activation="silu"):
     ldgate = _matrix(gate, m, n, dtype, device, "gate")
     ldup = _matrix(up, m, n, dtype, device, "up")
     h = _handle(device)
-    dx = _empty(x.shape, x, dtype)
-    dwg = _empty(w_gate.shape, w_gate, dtype)
-    dwu = _empty(w_up.shape, w_up, dtype)
+    dx = _empty(x.shape, x, dtype) if need_dx else None
+    dwg = _empty(w_gate.shape, w_gate, dtype) if need_dw else None
+    dwu = _empty(w_up.shape, w_up, dtype) if need_dw else None
     fn = "mic_gated_linear_backward_workspace" + ("_aligned" if _even((x, ldx), (w_gate, ldg), (w_up, ldu)) and ldg == ldu else "")
     wk, wkp, wkn = _workspace(fn, h, dy, _CODE[dtype], m, n, k)
     _call("mic_gated_linear_backward", h, _CODE[dtype], act, m, n, k, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-          w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, gate.data_ptr(), ldgate, up.data_ptr(), ldup, dx.data_ptr(), k,
-          dwg.data_ptr(), k, dwu.data_ptr(), k, wkp, wkn)
+          w_gate.data_ptr(), ldg, w_up.data_ptr(), ldu, gate.data_ptr(), ldgate, up.data_ptr(), ldup, _ptr(dx), k, _ptr(dwg),
+          k, _ptr(dwu), k, wkp, wkn)
     return dx, dwg, dwu
