@@ -96,9 +96,9 @@ template <int E> __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, i
 // take its tail as the bell times a polynomial of 1 / (1 + 0.292 |z|), fitted
 // for this: the polynomial is within 6.2e-8 of the tail in all and within 6.1e-5
 // (2^-14) relative to it up to |z| = 14, where the bell ends, so outputs far
-// below zero keep bf16's precision too, at a third of erff's instructions (the epilogue of an e4m3
-// product of depth 4096 would otherwise spend half as long in erff as in its
-// matrix instructions).
+// below zero keep bf16's precision too, at a third of erff's instructions (the
+// epilogue of an e4m3 product of depth 4096 would otherwise spend half as long
+// in erff as in its matrix instructions).
 
 template <bool EXACT> __device__ __forceinline__ float exponential(float x)
 {
