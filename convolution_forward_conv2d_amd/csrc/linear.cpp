@@ -335,6 +335,7 @@ mic_status forward_workspace(mic_handle h, Product kind, mic_dtype dtype, int m,
 {
     if (!bytes) return MIC_STATUS_BAD_PARAM;
     MIC_TRY(check_sizes(m, n, k));
+    if (kind == Product::GATED && n >= kMaxSize / 2) return MIC_STATUS_NOT_SUPPORTED;      // twice as many raw columns
     ProductType type, fast;
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &type));
     MIC_TRY(product_type(dtype, plain_type(dtype) ? dtype : MIC_DTYPE_BF16, &fast, true));
@@ -352,6 +353,7 @@ mic_status forward_name(mic_handle h, Product kind, mic_dtype dtype, mic_dtype o
                         int aligned, char* buf, size_t buflen)
 {
     MIC_TRY(check_sizes(m, n, k));
+    if (kind == Product::GATED && n >= kMaxSize / 2) return MIC_STATUS_NOT_SUPPORTED;
     ProductType type;
     MIC_TRY(product_type(dtype, out_dtype, &type, fast_sums != 0));
     if (!m || !n) return give_name("nothing", buf, buflen);
@@ -410,6 +412,7 @@ mic_status backward_name(mic_handle h, mic_dtype dtype, bool own_dz, int m, int 
 {
     MIC_TRY(check_sizes(m, n, k));
     if (!plain_type(dtype)) return MIC_STATUS_NOT_SUPPORTED;
+    if (n >= kMaxSize / 2) return MIC_STATUS_NOT_SUPPORTED;
     ProductType type;
     MIC_TRY(product_type(dtype, dtype, &type));
     if (!k) return give_name("nothing", buf, buflen);

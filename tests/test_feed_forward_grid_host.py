@@ -38,3 +38,17 @@ def test_more_outputs_than_any_grid_holds_are_refused():
         mic.mic_linear_forward_kernel_name(None, BF16, BF16, 0, MOST, 1 << 21, 8)
     assert e.value.status == mic.MIC_STATUS_NOT_SUPPORTED
     assert mic.mic_linear_forward_workspace(None, BF16, MOST, 1 << 21, 8) == 0
+
+
+def test_gated_sizes_are_refused_by_every_call_alike():
+    """A gated layer's raw columns, twice its features, have to stay a 32-bit count: from 2^29 on no call takes them."""
+    n = 1 << 29
+    for call in (lambda: mic.mic_gated_linear_forward_workspace(None, BF16, 4, n, 4),
+                 lambda: mic.mic_gated_linear_forward_workspace(None, BF16, 4, MOST, 4),
+                 lambda: mic.mic_gated_linear_forward_workspace_aligned(None, BF16, 4, MOST, 8),
+                 lambda: mic.mic_gated_linear_forward_kernel_name(None, BF16, BF16, 0, 4, MOST, 8),
+                 lambda: mic.mic_gated_linear_backward_kernel_name(None, BF16, 4, MOST, 8),
+                 lambda: mic.mic_linear_backward_kernel_name(None, BF16, 0, 4, n, 8)):
+        with pytest.raises(mic.MicError) as e:
+            call()
+        assert e.value.status == mic.MIC_STATUS_NOT_SUPPORTED
