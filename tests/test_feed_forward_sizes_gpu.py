@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import convolution_forward_conv2d_amd as mic
+import feed_forward_ref as R
 from test_feed_forward_gpu import BF16, E4M3, F32, dev
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +42,29 @@ def test_as_many_rows_as_there_may_be(dtype):
     for a in range(0, m, 1 << 27):
         rows = slice(a, min(a + (1 << 27), m))
         assert torch.equal(y[rows], (x[rows].float() * 1.25).to(dtype)), a
+
+
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_offsets_past_32_bits(m, monkeypatch):
+    """Weights of 2.4e9 elements: every way through a layer (few rows on the vector units and in blocks, large tiles) and
+    its gradients, on sampled outputs, the first and last among them."""
+    monkeypatch.setattr(R, "d", lambda t: None if t is None else t.detach().double())     # sums on the GPU
+    n, k = (1 << 18) + 5, 9216
+    g = torch.Generator(device=dev()).manual_seed(m)
+
+    def normal(*shape, std=1.0):
+        return torch.empty(shape, dtype=BF16, device=dev()).normal_(std=std, generator=g)
+    x, w = normal(m, k), normal(n, k, std=k ** -0.5)
+    pick = torch.Generator().manual_seed(m)                    # 233016: 2^31 / k
+    at = torch.cat([torch.tensor([0, 1, 233016, 233017, n - 2, n - 1]), torch.randint(0, n, (26,), generator=pick)]).to(dev())
+    kat = torch.cat([torch.tensor([0, k - 1]), torch.randint(0, k, (30,), generator=pick)]).to(dev())
+    y = mic.linear(x, w)
+    R.check(y[:, at], R.linear(x, w[at], None, None, "none", BF16)[0], "y")
+    h = mic.gated_linear(x, w, w)
+    R.check(h[:, at], R.gated(x, w[at], w[at], "silu", BF16)[0], "h")
+    del h
+    dx, dw, db = mic.linear_backward(y, x, w, bias=True)
+    ref = R.linear_backward(y[:, at], x[:, kat], w[at][:, kat], None, "none")
+    R.check(dw[at][:, kat], ref[1], "dw")
+    R.check(db[at], ref[2], "dbias")
+    R.check(dx[:, kat], R.linear_backward(y, x[:, kat], w[:, kat], None, "none")[0], "dx")
