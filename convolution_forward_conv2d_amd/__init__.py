@@ -126,6 +126,13 @@ _SIGS = {
     "mic_rms_norm_backward_workspace": ([_vp, _i, _i, _szp], _i),
     "mic_rms_norm_backward": ([_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
                                ctypes.c_size_t], _i),
+    "mic_layer_norm": ([_vp, _i, _i, _i, _i, ctypes.c_double, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                        _vp], _i),
+    "mic_layer_norm_backward_workspace": ([_vp, _i, _i, _szp], _i),
+    "mic_layer_norm_backward": ([_vp, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                 ctypes.c_size_t], _i),
+    "mic_dropout": ([_vp, _i, _i64, _i64, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _i64, _vp, _i64, _vp,
+                     _i64], _i),
     "mic_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
@@ -407,6 +414,22 @@ def mic_rms_norm_backward_workspace(handle, rows, cols):
 
 def mic_rms_norm_backward(*args):
     _check(lib().mic_rms_norm_backward(*args), "mic_rms_norm_backward")
+
+
+def mic_layer_norm(*args):
+    _check(lib().mic_layer_norm(*args), "mic_layer_norm")
+
+
+def mic_layer_norm_backward_workspace(handle, rows, cols):
+    return _bytes(lib().mic_layer_norm_backward_workspace, "mic_layer_norm_backward_workspace", handle, rows, cols)
+
+
+def mic_layer_norm_backward(*args):
+    _check(lib().mic_layer_norm_backward(*args), "mic_layer_norm_backward")
+
+
+def mic_dropout(*args):
+    _check(lib().mic_dropout(*args), "mic_dropout")
 
 
 def mic_linear_forward_workspace(handle, dtype, m, n, k):
@@ -933,3 +956,4 @@ class BlockedConvPlan(ConvPlan):
 
 from .feed_forward import (RmsNorm, gated_linear, gated_linear_backward, linear, linear_backward,  # noqa: E402,F401
                            rms_norm, rms_norm_backward)
+from .training import (LayerNorm, dropout, dropout_backward, layer_norm, layer_norm_backward)  # noqa: E402,F401

@@ -417,9 +417,129 @@ PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args
     END_HANDLE_TH_ERRORS
 }
 
+// (x, weight, bias, residual, eps, e4m3) -> (y, sum, mean, rstd, scale)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *x, *w, *bias, *residual;
+    int64_t rows, cols;
+    mic_dtype d;
+    if (n_args != 6 || !plain_rows(x = tensor(a[0]), rows, cols) || !(w = tensor(a[1])) || !maybe(a[2], bias)
+        || !maybe(a[3], residual))
+        return none();
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (PyErr_Occurred()) return nullptr;
+    bool e4m3;
+    if (!flag(a[5], "e4m3", e4m3)) return nullptr;
+    const auto type = x->scalar_type();
+    if (!dtype_of(*x, d) || d == MIC_DTYPE_F8_E4M3 || !plain(*w, type, *x, {cols}) || (bias && !plain(*bias, type, *x, {cols})))
+        return none();
+    if (residual && (residual->sizes() != x->sizes() || !plain_matrix(*residual, type, *x, rows, cols))) return none();
+    const mic_handle h = handle_on(x->get_device());
+    if (!h) return none();
+    Tensor y = like(*x, e4m3 ? at::kFloat8_e4m3fn : type), sum, scale;
+    if (residual) sum = like(*x, type);
+    Tensor mean = at::empty(x->sizes().slice(0, x->dim() - 1), x->options().dtype(at::kFloat));
+    Tensor rstd = like(mean, at::kFloat);
+    if (e4m3) scale = like(mean, at::kFloat);
+    if (mic_layer_norm(h, d, e4m3 ? MIC_DTYPE_F8_E4M3 : d, (int)rows, (int)cols, eps, x->data_ptr(), cols, data(residual), cols,
+                       w->data_ptr(), data(bias), y.data_ptr(), cols, residual ? sum.data_ptr() : nullptr, cols,
+                       floats(&mean), floats(&rstd), e4m3 ? floats(&scale) : nullptr)
+        != MIC_STATUS_SUCCESS)
+        return none();
+    PyObject* s = a[0];
+    if (residual) s = wrap(sum);
+    else Py_INCREF(s);
+    return pack({wrap(y), s, wrap(mean), wrap(rstd), e4m3 ? wrap(scale) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dy, sum, weight, mean, rstd, dsum, bias, need_dweight) -> (dx, dweight, dbias), the last two None where not asked for
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *dy, *sum, *w, *mean, *rstd, *dsum;
+    int64_t rows, cols;
+    mic_dtype d;
+    if (n_args != 8 || !plain_rows(dy = tensor(a[0]), rows, cols) || !(sum = tensor(a[1])) || !(w = tensor(a[2]))
+        || !(mean = tensor(a[3])) || !(rstd = tensor(a[4])) || !maybe(a[5], dsum))
+        return none();
+    bool bias, need_dw;
+    if (!flag(a[6], "bias", bias) || !flag(a[7], "need_dweight", need_dw)) return nullptr;
+    const auto type = dy->scalar_type();
+    if (!dtype_of(*dy, d) || d == MIC_DTYPE_F8_E4M3 || !plain_matrix(*sum, type, *dy, rows, cols)
+        || !plain(*w, type, *dy, {cols}) || !plain_scale(*mean, *dy, rows) || !plain_scale(*rstd, *dy, rows)
+        || (dsum && !plain_matrix(*dsum, type, *dy, rows, cols)))
+        return none();
+    const mic_handle h = handle_on(dy->get_device());
+    Tensor space;
+    size_t bytes = 0;
+    if (!h || ((need_dw || bias) && !workspace(10, d, rows, cols, 0, *dy, space, bytes, [&](size_t* b) {
+            return mic_layer_norm_backward_workspace(h, (int)rows, (int)cols, b);
+        })))
+        return none();
+    Tensor dx = like(*dy, type), dw, db;
+    if (need_dw) dw = like(*w, type);
+    if (bias) db = like(*w, type);
+    if (mic_layer_norm_backward(h, d, (int)rows, (int)cols, dy->data_ptr(), cols, sum->data_ptr(), cols, w->data_ptr(),
+                                floats(mean), floats(rstd), data(dsum), cols, dx.data_ptr(), cols,
+                                need_dw ? dw.data_ptr() : nullptr, bias ? db.data_ptr() : nullptr,
+                                bytes ? space.data_ptr() : nullptr, bytes)
+        != MIC_STATUS_SUCCESS)
+        return none();
+    return pack({wrap(dx), need_dw ? wrap(dw) : none(), bias ? wrap(db) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, p, seed, offset, residual) -> y; any shape, everything contiguous
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *x, *residual;
+    mic_dtype d;
+    if (n_args != 5 || !(x = tensor(a[0])) || !maybe(a[4], residual)) return none();
+    if (!x->is_cuda() || !x->is_contiguous() || x->numel() == 0 || x->get_device() != c10::hip::current_device()
+        || !dtype_of(*x, d) || d == MIC_DTYPE_F8_E4M3)
+        return none();
+    const auto type = x->scalar_type();
+    if (residual
+        && (residual->scalar_type() != type || residual->device() != x->device() || !residual->is_contiguous()
+            || residual->sizes() != x->sizes()))
+        return none();
+    if (!(PyFloat_Check(a[1]) || (PyLong_Check(a[1]) && !PyBool_Check(a[1])))) return none();
+    const double p = PyFloat_AsDouble(a[1]);
+    uint64_t number[2] = {0, 0};
+    const uint64_t* state = nullptr;
+    for (int i = 0; i < 2; ++i) {
+        if (const Tensor* t = i ? nullptr : tensor(a[2])) {
+            if (t->scalar_type() != at::kLong || t->device() != x->device() || t->dim() != 1 || t->size(0) != 2
+                || !t->is_contiguous())
+                return none();
+            state = static_cast<const uint64_t*>(t->data_ptr());
+            continue;
+        }
+        if (!PyLong_Check(a[2 + i]) || PyBool_Check(a[2 + i])) return none();
+        number[i] = PyLong_AsUnsignedLongLong(a[2 + i]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();                                     // out of range: the Python checks say so
+            return none();
+        }
+    }
+    const mic_handle h = handle_on(x->get_device());
+    if (!h) return none();
+    Tensor y = like(*x, type);
+    const int64_t n = x->numel();
+    if (mic_dropout(h, d, 1, n, p, number[0], number[1], state, x->data_ptr(), n, data(residual), n, y.data_ptr(), n)
+        != MIC_STATUS_SUCCESS)
+        return none();
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(rms_norm), FAST(rms_norm_backward), FAST(linear), FAST(linear_backward),
-                         FAST(gated_linear), FAST(gated_linear_backward), {nullptr, nullptr, 0, nullptr}};
+                         FAST(gated_linear), FAST(gated_linear_backward), FAST(layer_norm),
+                         FAST(layer_norm_backward), FAST(dropout), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The feed-forward operators on plainly laid out tensors.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -259,6 +259,61 @@ struct NormGradArgs {
 hipError_t launch_rms_norm(DType dt, bool e4m3, const NormArgs& p, hipStream_t stream);
 int rms_norm_grad_groups(int rows, int cols, int num_cu);
 hipError_t launch_rms_norm_grad(DType dt, const NormGradArgs& p, hipStream_t stream);
+// Layer norm of s = x + residual (layer_norm.hip).
+struct LayerNormArgs {
+    int rows, cols;
+    float eps;
+    const void* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    const void* weight;
+    const void* bias;         // or null
+    void* y;
+    int64_t ldy;
+    void* sum;
+    int64_t lds;
+    float* mean;
+    float* rstd;
+    float* scale;             // e4m3 output only
+};
+struct LayerNormGradArgs {
+    int rows, cols;
+    const void* dy;
+    int64_t lddy;
+    const void* sum;
+    int64_t lds;
+    const void* weight;
+    const float* mean;
+    const float* rstd;
+    const void* dsum;
+    int64_t ldd;
+    void* dx;
+    int64_t lddx;
+    void* dweight;
+    void* dbias;
+    float* partial;           // [groups][2][cols]: shares of dweight, of dbias
+    int groups;
+};
+hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStream_t stream);
+int layer_norm_grad_groups(int rows, int cols, int num_cu);
+hipError_t launch_layer_norm_grad(DType dt, const LayerNormGradArgs& p, hipStream_t stream);
+
+// Dropout (dropout.hip); one row: everything packed.
+struct DropoutArgs {
+    int64_t rows, cols;
+    uint64_t seed, offset;
+    const uint64_t* state;    // device memory: the seed, and what is added to the offset; or null
+    uint32_t least;           // of the 16-bit lots that keep an element; 65536: none does
+    float scale;
+    const void* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+};
+hipError_t launch_dropout(DType dt, const DropoutArgs& p, hipStream_t stream);
 // out[c] = sum over `groups` of partial[g][c], in out's type.
 hipError_t launch_column_join(DType dt, const float* partial, int groups, int cols, void* out, hipStream_t stream);
 

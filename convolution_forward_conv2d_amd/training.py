@@ -1,0 +1,170 @@
+"""What a network is trained with, on torch tensors: ``layer_norm``,
+``dropout``, ``linear_cross_entropy`` and their gradients.
+
+Marshalling only, by the rules of ``feed_forward.py``: the HIP kernels of
+``libmiconv.so`` on torch's current stream of the tensors' device, outputs and
+workspaces as torch allocations on that stream, rows at any pitch and
+alignment, contiguous arguments that fit each other through ``_native.so``.
+"""
+import collections
+
+import torch
+
+from . import feed_forward as ff
+from .feed_forward import E4M3, _CODE, _call, _empty, _flag, _gpu, _handle, _matrix, _ptr, _rows, _vector, _workspace
+
+LayerNorm = collections.namedtuple("LayerNorm", ["y", "sum", "mean", "rstd", "scale"])
+LayerNorm.__doc__ = """layer_norm's results: y; sum = x + residual (x itself without a residual), mean and rstd, fp32 per
+row, which layer_norm_backward takes; scale, fp32 per row, where y is e4m3 (else None)."""
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _native():
+    return ff._native or ff._load()
+
+
+def _per_row(t, rows, device, what):
+    if t.dtype != torch.float32 or t.device != device or t.numel() != rows or not t.is_contiguous():
+        raise ValueError("%s must be %d packed fp32 values on %s" % (what, rows, device))
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------------- norm
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5, out_dtype=None):
+    """s = x + residual, y = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps) * weight + bias over the last dimension.
+
+    x, residual, weight, bias: fp32 or bf16, one type.  y has x's type, or is
+    torch.float8_e4m3fn with a scale per row (y * scale is the value).
+    Returns LayerNorm(y, sum, mean, rstd, scale).
+    """
+    e4m3 = out_dtype is E4M3
+    if e4m3 or out_dtype is None or out_dtype is x.dtype:
+        r = _native().layer_norm(x, weight, bias, residual, eps, e4m3)
+        if r is not None:
+            return LayerNorm(*r)
+    _gpu(x, "x", _FLOATS)
+    dtype, device = x.dtype, x.device
+    out_dtype = dtype if out_dtype is None else out_dtype
+    if out_dtype not in (dtype, E4M3):
+        raise TypeError("out_dtype must be %s or %s, got %s" % (dtype, E4M3, out_dtype))
+    cols = x.shape[-1] if x.dim() else 0
+    if cols < 1:
+        raise ValueError("x must have at least one feature")
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
+    rows, ldx = _rows(x, cols, "x")
+    wp = _vector(weight, cols, dtype, device, "weight")
+    bp = 0 if bias is None else _vector(bias, cols, dtype, device, "bias")
+    ldr, total = 0, x
+    h = _handle(device)
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual has shape %s, x %s" % (tuple(residual.shape), tuple(x.shape)))
+        ldr = _matrix(residual, rows, cols, dtype, device, "residual")
+        total = _empty(x.shape, x, dtype)
+    y = _empty(x.shape, x, out_dtype)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
+    scale = torch.empty_like(mean) if out_dtype is E4M3 else None
+    _call("mic_layer_norm", h, _CODE[dtype], _CODE[out_dtype], rows, cols, eps, x.data_ptr(), ldx, _ptr(residual), ldr,
+          wp, bp, y.data_ptr(), cols, 0 if residual is None else total.data_ptr(), cols, mean.data_ptr(), rstd.data_ptr(),
+          _ptr(scale))
+    return LayerNorm(y, total, mean, rstd, scale)
+
+
+def layer_norm_backward(dy, sum, weight, mean, rstd, dsum=None, bias=False, need_dweight=True):
+    """(dx, dweight, dbias) of layer_norm, from its sum, mean and rstd; dx is residual's gradient too.
+
+    dsum: the gradient that reaches sum past the norm (added to dx).
+    dbias is None unless bias is true, and dweight is where need_dweight is
+    false: what is None is not computed.
+    """
+    r = _native().layer_norm_backward(dy, sum, weight, mean, rstd, dsum, bias, need_dweight)
+    if r is not None:
+        return r
+    bias, need_dweight = _flag(bias, "bias"), _flag(need_dweight, "need_dweight")
+    _gpu(dy, "dy", _FLOATS)
+    dtype, device = dy.dtype, dy.device
+    cols = dy.shape[-1] if dy.dim() else 0
+    if cols < 1:
+        raise ValueError("dy must have at least one feature")
+    rows, lddy = _rows(dy, cols, "dy")
+    lds = _matrix(sum, rows, cols, dtype, device, "sum")
+    wp = _vector(weight, cols, dtype, device, "weight")
+    mp, rp = _per_row(mean, rows, device, "mean"), _per_row(rstd, rows, device, "rstd")
+    ldd = 0 if dsum is None else _matrix(dsum, rows, cols, dtype, device, "dsum")
+    h = _handle(device)
+    dx = _empty(dy.shape, dy, dtype)
+    dweight = torch.empty_like(weight) if need_dweight else None
+    dbias = torch.empty_like(weight) if bias else None
+    ws, wsp, wsn = None, 0, 0
+    if need_dweight or bias:
+        ws, wsp, wsn = _workspace("mic_layer_norm_backward_workspace", h, dy, rows, cols)
+    _call("mic_layer_norm_backward", h, _CODE[dtype], rows, cols, dy.data_ptr(), lddy, sum.data_ptr(), lds, wp, mp, rp,
+          _ptr(dsum), ldd, dx.data_ptr(), cols, _ptr(dweight), _ptr(dbias), wsp, wsn)
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------- dropout
+
+def _drop(x, p, seed, offset, residual, what):
+    r = _native().dropout(x, p, seed, offset, residual)
+    if r is not None:
+        return r
+    _gpu(x, what, _FLOATS)
+    if isinstance(p, torch.Tensor) or not 0 <= p <= 1:
+        raise ValueError("p must be a number from 0 to 1, got %s" % (p,))
+    dtype, device = x.dtype, x.device
+    state = 0
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.device != device or seed.shape != (2,) or not seed.is_contiguous():
+            raise ValueError("seed must be a number, or two packed int64 values on %s" % device)
+        state, seed = seed.data_ptr(), 0
+    for name, v in (("seed", seed), ("offset", offset)):
+        if isinstance(v, bool) or not isinstance(v, int):
+            raise TypeError("%s must be a whole number, got %s" % (name, type(v).__name__))
+        if not 0 <= v < 1 << 64:
+            raise ValueError("%s must be from 0 to 2^64 - 1, got %d" % (name, v))
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual has shape %s, %s %s" % (tuple(residual.shape), what, tuple(x.shape)))
+    if x.is_contiguous() and (residual is None or residual.is_contiguous()):
+        rows, cols = 1, x.numel()
+        ldx = ldr = cols
+        if residual is not None:
+            if residual.dtype is not dtype:
+                raise TypeError("residual must be %s, got %s" % (dtype, residual.dtype))
+            if residual.device != device:
+                raise ValueError("residual is on %s, not on %s" % (residual.device, device))
+    else:
+        cols = x.shape[-1]
+        rows, ldx = _rows(x, cols, what)
+        ldr = 0 if residual is None else _matrix(residual, rows, cols, dtype, device, "residual")
+    h = _handle(device)
+    y = _empty(x.shape, x, dtype)
+    _call("mic_dropout", h, _CODE[dtype], rows, cols, float(p), seed, offset, state, x.data_ptr(), ldx, _ptr(residual), ldr,
+          y.data_ptr(), cols)
+    return y
+
+
+def dropout(x, p, seed, offset=0, residual=None):
+    """x / (1 - p) where an element is kept, 0 where it is dropped, + residual.
+
+    An element is dropped with probability p, rounded to a multiple of 2^-16
+    (and x scaled by what that makes of 1 / (1 - p)).  Which ones goes by
+    seed, offset and the element's position in row-major order alone, so no
+    mask is stored and dropout_backward takes the same three: a seed for the
+    run, an offset for the layer and step.  seed may be an int64 tensor of two
+    on x's device, the seed and what is added to offset: a captured call draws
+    anew when that tensor has changed between replays.
+
+    x, residual: fp32 or bf16, one type and shape.  residual's gradient is dy.
+    """
+    return _drop(x, p, seed, offset, residual, "x")
+
+
+def dropout_backward(dy, p, seed, offset=0):
+    """dx of dropout with the same p, seed and offset."""
+    return _drop(dy, p, seed, offset, None, "dy")

@@ -446,6 +446,47 @@ mic_status mic_rms_norm_backward(mic_handle handle, mic_dtype dtype, int rows, i
                                  const void* dsum, int64_t ldd, void* dx, int64_t lddx, void* dweight,
                                  void* workspace, size_t workspace_bytes);
 
+/* Layer norm: s = x + residual (x alone when residual is null), mean = mean(s),
+ * rstd = 1/sqrt(mean((s - mean)^2) + eps), y = (s - mean) * rstd * weight + bias.
+ *
+ * Types, sum, scale and the pointers that may be null as mic_rms_norm's; bias
+ * and mean may be null too.  The variance is summed from distances to the mean. */
+mic_status mic_layer_norm(mic_handle handle, mic_dtype dtype, mic_dtype out_dtype, int rows, int cols, double eps,
+                          const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                          const void* bias, void* y, int64_t ldy, void* sum, int64_t lds, float* mean, float* rstd,
+                          float* scale);
+
+/* With u = (s - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean(g) - u * mean(g * u)) + dsum
+ *   dweight = sum over rows of dy * u    dbias = sum over rows of dy
+ * dx is the gradient of x and of residual alike; dsum, dweight and dbias may
+ * each be null. */
+mic_status mic_layer_norm_backward_workspace(mic_handle handle, int rows, int cols, size_t* bytes);
+mic_status mic_layer_norm_backward(mic_handle handle, mic_dtype dtype, int rows, int cols, const void* dy, int64_t lddy,
+                                   const void* sum, int64_t lds, const void* weight, const float* mean,
+                                   const float* rstd, const void* dsum, int64_t ldd, void* dx, int64_t lddx,
+                                   void* dweight, void* dbias, void* workspace, size_t workspace_bytes);
+
+/* y[i] = (lot(i) >= T ? x[i] * 65536 / (65536 - T) : 0) + residual[i], T = p * 65536
+ * rounded to the nearest whole number; all are dropped at T = 65536.  A dropped
+ * element is 0 whatever x holds there.
+ *
+ * i is the element's position in row-major order, row * cols + column, and
+ * lot(i) the 16-bit number in half i % 2 of word (i % 8) / 2 of the Philox4x32
+ * generator's block of ten rounds with key seed and counter (i / 8, offset), low
+ * words first.  The gradient of x is the same call, without a residual, on dy;
+ * the residual's is dy.
+ *
+ * state (may be null) points to two numbers in device memory, 8-byte aligned:
+ * the first takes seed's place, the second is added to offset; a captured call
+ * then draws anew at every replay that finds them changed.
+ *
+ * F32 or BF16 throughout.  rows * cols and rows times each pitch below 2^40; no other limit to a pitch.
+ * residual may be null; y may be x or residual. */
+mic_status mic_dropout(mic_handle handle, mic_dtype dtype, int64_t rows, int64_t cols, double p, uint64_t seed,
+                       uint64_t offset, const uint64_t* state, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                       void* y, int64_t ldy);
+
 /* y[m,n] = act(x_scale[m] w_scale[n] sum_k x[m,k] w[n,k] + bias[n]) + residual[m,n].
  *
  * Types: F32 or BF16 throughout, or x and w F8_E4M3 with both scales (fp32)
