@@ -276,6 +276,7 @@ struct LayerNormArgs {
     float* mean;
     float* rstd;
     float* scale;             // e4m3 output only
+    int num_cu;
 };
 struct LayerNormGradArgs {
     int rows, cols;

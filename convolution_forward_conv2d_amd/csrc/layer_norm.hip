@@ -45,12 +45,217 @@ template <int WAVES> __device__ __forceinline__ void block_sums(float& a, float&
     for (int w = 0; w < WAVES; ++w) a += part[w][0], b += part[w][1];
 }
 
-// One row per workgroup, NV vectors of eight columns per thread; past them
-// (LOOP) the rest of a longer row is read again in every pass.
-template <class T, bool E4M3, int WAVES, int NV, bool LOOP>
+// How a row's columns end: with a whole vector of eight, or inside one.  A cut
+// vector is loaded as the row's last eight elements and shifted into place where
+// it is used: element by element its loads would wait for each other, and for the
+// next row's on their way (8192 x 4095 bf16 then takes 110 us instead of 54).  Rows of
+// fewer than eight columns have no such eight.
+enum RowEnd : int { END_WHOLE, END_CUT, END_SHORT };
+
+// Eight columns as they lie in memory, so that a row on its way takes half the registers of its values in bf16.
+template <class T, int END> struct Vec {
+    static constexpr int E = sizeof(T), WORDS = 2 * E;
+    uint32_t word[WORDS];
+    // the first nv exist
+    __device__ __forceinline__ void load(const T* p, int nv)
+    {
+        if constexpr (END == END_SHORT) {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const u32x4 t = load_piece<E>(reinterpret_cast<const uint8_t*>(p) + 16 * i, nv - i * (16 / E));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) word[4 * i + k] = t[k];
+            }
+        } else if (nv > 0) {
+            __builtin_memcpy(word, END == END_CUT && nv < 8 ? p + (nv - 8) : p, sizeof(word));
+        } else {
+            clear();
+        }
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) word[i] = 0;
+    }
+    // after load, before value: a cut vector's elements to their places, zeros behind them
+    __device__ __forceinline__ void settle(int nv)
+    {
+        if (END != END_CUT || nv <= 0 || nv >= 8) return;
+        const int by = 8 - nv;
+#pragma unroll
+        for (int step = 4; step > 0; step >>= 1) {
+            if (!(by & step)) continue;
+            if constexpr (E == 2)
+                if (step == 1) {
+#pragma unroll
+                    for (int i = 0; i < WORDS; ++i) word[i] = word[i] >> 16 | (i + 1 < WORDS ? word[i + 1] << 16 : 0);
+                    continue;
+                }
+            const int words = step * E / 4;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) word[i] = i + words < WORDS ? word[i + words] : 0;
+        }
+    }
+    // what was made of these before is made again from here on
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) asm volatile("" : "+v"(word[i]));
+    }
+    __device__ __forceinline__ float value(int i) const
+    {
+        if constexpr (E == 4) return __uint_as_float(word[i & (WORDS - 1)]);
+        return __uint_as_float(i & 1 ? word[(i >> 1) & 3] & 0xffff0000u : word[(i >> 1) & 3] << 16);
+    }
+};
+
+// The same number, no longer known to be: what follows from it is not kept in registers from row to row (the masks of a
+// cut vector's elements, two scalars each).
+__device__ __forceinline__ int anew(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// The scale of a row whose largest |y| is `most` (1 for a row of zeros, or one too small for a scale): stored at `to`,
+// its inverse as inv * shift.
+__device__ __forceinline__ float e4m3_scale(float most, float& shift, float* to)
+{
+    const float scale = most / E4M3_MAX > 0.0f ? most / E4M3_MAX : 1.0f;
+    shift = scale < 0x1p-100f ? 0x1p+64f : 1.0f;
+    if (to) *to = scale;
+    return 1.0f / (scale * shift);
+}
+
+// Rows blockIdx.x, + gridDim.x, ..., NV vectors of eight columns per thread;
+// weight and bias stay in registers, the next row is on its way while this one
+// is summed.
+template <class T, bool E4M3, int WAVES, int NV, int END>
 __global__ __launch_bounds__(64 * WAVES) void layer_norm_kernel(const LayerNormArgs p)
 {
-    constexpr int THREADS = 64 * WAVES, SPAN = THREADS * 8;
+    constexpr int SPAN = 64 * WAVES * 8;
+    __shared__ float part[2][WAVES][3], top[2][WAVES];
+    const int c0 = threadIdx.x * 8;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // columns of a wave: 512 at each of its NV places
+    auto columns = [&](int of) {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) n += min(max(p.cols - of * 512 - j * SPAN, 0), 512);
+        return (float)n;
+    };
+    Vec<T, END> w[NV], b[NV], x[NV], res[NV];
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * SPAN, nv = p.cols - c;
+            x[j].load(static_cast<const T*>(p.x) + row * p.ldx + c, nv);
+            if (p.residual) res[j].load(static_cast<const T*>(p.residual) + row * p.ldr + c, nv);
+        }
+    };
+    load(blockIdx.x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * SPAN;
+        w[j].load(static_cast<const T*>(p.weight) + c, p.cols - c);
+        if (p.bias) b[j].load(static_cast<const T*>(p.bias) + c, p.cols - c);
+        else b[j].clear();
+        w[j].settle(p.cols - c);
+        if (p.bias) b[j].settle(p.cols - c);
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+        float s[NV][8];
+        float total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int nv = anew(p.cols - c0 - j * SPAN);
+            x[j].settle(nv);
+            if (p.residual) res[j].settle(nv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[j][i] = x[j].value(i);
+                if (p.residual) s[j][i] += res[j].value(i);
+                total += s[j][i];
+            }
+        }
+        if (row + gridDim.x < p.rows) load(row + gridDim.x);
+        total = wave_sum(total);
+        const float own = columns(wave);
+        const float near = own > 0.0f ? total / own : 0.0f;
+        float spread = 0.0f, mean = near;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * SPAN;
+            const int nv = anew(p.cols - c);
+            if (END == END_WHOLE ? nv > 0 : nv >= 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) spread += (s[j][i] - near) * (s[j][i] - near);
+            } else if (END != END_WHOLE && nv > 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float apart = i < nv ? s[j][i] - near : 0.0f;
+                    spread += apart * apart;
+                }
+            }
+            if (p.sum && nv > 0)
+                store8(static_cast<T*>(p.sum) + row * p.lds + c, END == END_WHOLE ? 8 : nv, s[j]);
+        }
+        spread = wave_sum(spread);
+        if constexpr (WAVES > 1) {
+            // two parts in turn: a wave may be at the next row while another still reads this one's
+            if ((threadIdx.x & 63) == 0)
+                part[turn][wave][0] = total, part[turn][wave][1] = near, part[turn][wave][2] = spread;
+            __syncthreads();
+            mean = spread = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) mean += part[turn][v][0];
+            mean /= (float)p.cols;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) {
+                const float apart = part[turn][v][1] - mean;
+                spread += part[turn][v][2] + columns(v) * apart * apart;
+            }
+        }
+        const float rstd = 1.0f / sqrtf(spread / (float)p.cols + p.eps);
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // past the row's end weight and bias are 0, and so is y (or no number, as the row's own are)
+                s[j][i] = (s[j][i] - mean) * rstd * w[j].value(i) + b[j].value(i);
+                if constexpr (E4M3) most = fmaxf(most, fabsf(s[j][i]));
+            }
+        float inv = 1.0f, shift = 1.0f;
+        if constexpr (E4M3) {
+            most = block_max<WAVES>(most, top[turn]);
+            inv = e4m3_scale(most, shift, threadIdx.x == 0 ? p.scale + row : nullptr);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * SPAN;
+            const int nv = anew(p.cols - c);
+            if (nv <= 0) continue;
+            if constexpr (E4M3)
+                store8_e4m3(static_cast<uint8_t*>(p.y) + row * p.ldy + c, END == END_WHOLE ? 8 : nv, s[j], inv, shift);
+            else
+                store8(static_cast<T*>(p.y) + row * p.ldy + c, END == END_WHOLE ? 8 : nv, s[j]);
+        }
+    }
+}
+
+// A long row per workgroup: NV vectors of eight columns per thread stay in
+// registers, weight and bias do not; the rest of a row past them is read again in
+// every pass.
+template <class T, bool E4M3, int WAVES, int NV>
+__global__ __launch_bounds__(64 * WAVES) void layer_norm_long_kernel(const LayerNormArgs p)
+{
+    constexpr int SPAN = 64 * WAVES * 8;
     __shared__ float part[3][WAVES][2];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
@@ -58,7 +263,6 @@ __global__ __launch_bounds__(64 * WAVES) void layer_norm_kernel(const LayerNormA
     const T* weight = static_cast<const T*>(p.weight);
     const T* bias = static_cast<const T*>(p.bias);
     const int c0 = threadIdx.x * 8;
-
     auto fetch = [&](int c, float (&v)[8]) {
         const int nv = p.cols - c;
         load8(x + c, nv, v);
@@ -69,250 +273,220 @@ __global__ __launch_bounds__(64 * WAVES) void layer_norm_kernel(const LayerNormA
             for (int i = 0; i < 8; ++i) v[i] += r[i];
         }
     };
-    auto factors = [&](int c, float (&w)[8], float (&b)[8]) {
-        load8(weight + c, p.cols - c, w);
-        if (bias) load8(bias + c, p.cols - c, b);
-        else {
+    // over all of this thread's columns: the kept ones, then those read again
+    float s[NV][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = 0.0f;
-        }
-    };
-    float s[NV][8], w[NV][8], b[NV][8];
+    for (int j = 0; j < NV; ++j) fetch(c0 + j * SPAN, s[j]);
+    auto each = [&](auto&& f) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = c0 + j * SPAN;
-        if (c < p.cols) {
-            fetch(c, s[j]);
-            factors(c, w[j], b[j]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[j][i] = w[j][i] = b[j][i] = 0.0f;
-        }
-    }
-    float total = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = c0 + j * SPAN;
-        if (p.sum && c < p.cols) store8(static_cast<T*>(p.sum) + row * p.lds + c, p.cols - c, s[j]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) total += s[j][i];
-    }
-    auto squares = [&](float from) {
-        float q = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float apart = c0 + j * SPAN + i < p.cols ? s[j][i] - from : 0.0f;
-                q += apart * apart;
-            }
-        return q;
-    };
-    float mean, spread;
-    if constexpr (LOOP) {
+        for (int j = 0; j < NV; ++j) f(c0 + j * SPAN, s[j]);
         for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
             float v[8];
             fetch(c, v);
-            if (p.sum) store8(static_cast<T*>(p.sum) + row * p.lds + c, p.cols - c, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) total += v[i];
+            f(c, v);
         }
-        float unused = 0.0f;
-        block_sums<WAVES>(total, unused, part[0]);
-        mean = total / (float)p.cols;
-        spread = squares(mean);
-        for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
-            float v[8];
-            fetch(c, v);
+    };
+    float total = 0.0f, spread = 0.0f, unused = 0.0f;
+    each([&](int c, const float (&v)[8]) {
+        if (p.sum && c < p.cols) store8(static_cast<T*>(p.sum) + row * p.lds + c, p.cols - c, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float apart = c + i < p.cols ? v[i] - mean : 0.0f;
-                spread += apart * apart;
-            }
+        for (int i = 0; i < 8; ++i) total += v[i];
+    });
+    block_sums<WAVES>(total, unused, part[0]);
+    const float mean = total / (float)p.cols;
+    each([&](int c, const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float apart = c + i < p.cols ? v[i] - mean : 0.0f;
+            spread += apart * apart;
         }
-        block_sums<WAVES>(spread, unused, part[1]);
-    } else {
-        // columns of a wave: 512 at each of its NV places
-        auto columns = [&](int wave) {
-            int n = 0;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) n += min(max(p.cols - wave * 512 - j * SPAN, 0), 512);
-            return (float)n;
-        };
-        total = wave_sum(total);
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const float own = columns(wave);
-        const float near = own > 0.0f ? total / own : 0.0f;
-        spread = wave_sum(squares(near));
-        if constexpr (WAVES == 1) {
-            mean = near;
-        } else {
-            if ((threadIdx.x & 63) == 0) part[0][wave][0] = total, part[0][wave][1] = spread;
-            __syncthreads();
-            mean = spread = 0.0f;
-#pragma unroll
-            for (int v = 0; v < WAVES; ++v) mean += part[0][v][0];
-            mean /= (float)p.cols;
-#pragma unroll
-            for (int v = 0; v < WAVES; ++v) {
-                const float n = columns(v), apart = n > 0.0f ? part[0][v][0] / n - mean : 0.0f;
-                spread += part[0][v][1] + n * apart * apart;
-            }
-        }
-    }
+    });
+    block_sums<WAVES>(spread, unused, part[1]);
     const float rstd = 1.0f / sqrtf(spread / (float)p.cols + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-
-    float most = 0.0f;
+    auto result = [&](int c, const float (&v)[8], float (&y)[8]) {
+        float w[8], b[8] = {};
+        load8(weight + c, p.cols - c, w);
+        if (bias) load8(bias + c, p.cols - c, b);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s[j][i] = (s[j][i] - mean) * rstd * w[j][i] + b[j][i];
-            if constexpr (E4M3) most = fmaxf(most, fabsf(s[j][i]));
-        }
-    auto again = [&](int c, float (&v)[8]) {
-        float g[8], h[8];
-        fetch(c, v);
-        factors(c, g, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * rstd * g[i] + h[i];
+        for (int i = 0; i < 8; ++i) y[i] = (v[i] - mean) * rstd * w[i] + b[i];
     };
     float inv = 1.0f, shift = 1.0f;
     if constexpr (E4M3) {
-        // columns past the row's end have weight and bias 0, so their y is 0 (or no number, as the row's own are)
-        if constexpr (LOOP)
-            for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
-                float v[8];
-                again(c, v);
+        float most = 0.0f;
+        each([&](int c, const float (&v)[8]) {
+            float y[8];
+            result(c, v, y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]));
-            }
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(y[i]));
+        });
         most = block_max<WAVES>(most, &part[2][0][0]);
-        // a row of zeros (or one too small for a scale) keeps the scale 1
-        const float scale = most / E4M3_MAX > 0.0f ? most / E4M3_MAX : 1.0f;
-        shift = scale < 0x1p-100f ? 0x1p+64f : 1.0f;
-        inv = 1.0f / (scale * shift);
-        if (threadIdx.x == 0) p.scale[row] = scale;
+        inv = e4m3_scale(most, shift, threadIdx.x == 0 ? p.scale + row : nullptr);
     }
-    auto put = [&](int c, const float (&v)[8]) {
+    each([&](int c, const float (&v)[8]) {
+        if (c >= p.cols) return;
+        float y[8];
+        result(c, v, y);
         if constexpr (E4M3)
-            store8_e4m3(static_cast<uint8_t*>(p.y) + row * p.ldy + c, p.cols - c, v, inv, shift);
+            store8_e4m3(static_cast<uint8_t*>(p.y) + row * p.ldy + c, p.cols - c, y, inv, shift);
         else
-            store8(static_cast<T*>(p.y) + row * p.ldy + c, p.cols - c, v);
-    };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = c0 + j * SPAN;
-        if (c < p.cols) put(c, s[j]);
-    }
-    if constexpr (LOOP)
-        for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
-            float v[8];
-            again(c, v);
-            put(c, v);
-        }
+            store8(static_cast<T*>(p.y) + row * p.ldy + c, p.cols - c, y);
+    });
 }
 
 // dx, and this workgroup's share of dweight and dbias, for rows blockIdx.x,
-// + gridDim.x, ...  The shares stay in registers until the last row (LOOP:
-// rows too long for that get them from layer_norm_weight_kernel).
-template <class T, int WAVES, int NV, bool LOOP>
-__global__ __launch_bounds__(64 * WAVES) void layer_norm_grad_kernel(const LayerNormGradArgs p)
+// + gridDim.x, ...: the shares and the weight stay in registers until the last
+// row, the next row is on its way while this one is summed (NEXT, where the
+// registers hold both).  ROWS > 1: short rows, one to each wave at a time.
+template <class T, int WAVES, int ROWS, int NV, bool NEXT, int END>
+__global__ __launch_bounds__(64 * WAVES * ROWS) void layer_norm_grad_kernel(const LayerNormGradArgs p)
 {
-    constexpr int THREADS = 64 * WAVES, SPAN = THREADS * 8;
+    static_assert(ROWS == 1 || (WAVES == 1 && NV == 1), "a wave to a row");
+    constexpr int SPAN = 64 * WAVES * 8;
     __shared__ float part[2][WAVES][2];
-    const T* weight = static_cast<const T*>(p.weight);
-    const int c0 = threadIdx.x * 8;
-    float w[NV][8], dw[NV][8], db[NV][8];
+    const int c0 = (ROWS > 1 ? threadIdx.x & 63 : threadIdx.x) * 8;
+    const int64_t start = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x >> 6 : 0);
+    const int64_t hop = (int64_t)gridDim.x * ROWS;
+    Vec<T, END> w[NV], dy[NV], sum[NV], dsum[NV];
+    float dw[NV][8], db[NV][8], mean, rstd;
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * SPAN, nv = p.cols - c;
+            dy[j].load(static_cast<const T*>(p.dy) + row * p.lddy + c, nv);
+            sum[j].load(static_cast<const T*>(p.sum) + row * p.lds + c, nv);
+            if (p.dsum) dsum[j].load(static_cast<const T*>(p.dsum) + row * p.ldd + c, nv);
+        }
+        mean = p.mean[row], rstd = p.rstd[row];
+    };
+    if (start < p.rows) load(start);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        load8(weight + c0 + j * SPAN, p.cols - c0 - j * SPAN, w[j]);
+        const int nv = p.cols - c0 - j * SPAN;
+        w[j].load(static_cast<const T*>(p.weight) + c0 + j * SPAN, nv);
+        w[j].settle(nv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = db[j][i] = 0.0f;
     }
     const float per = 1.0f / (float)p.cols;
     int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-        const T* sum = static_cast<const T*>(p.sum) + row * p.lds;
-        const T* dsum = p.dsum ? static_cast<const T*>(p.dsum) + row * p.ldd : nullptr;
-        T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        float u[NV][8], g[NV][8], d[NV][8];
+    for (int64_t row = start; row < p.rows; row += hop, turn ^= 1) {
+        float u[NV][8], g[NV][8];
+        const float scale = rstd;
         float level = 0.0f, along = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = c0 + j * SPAN, nv = p.cols - c;
-            load8(dy + c, nv, g[j]);
-            load8(sum + c, nv, u[j]);
-            if (dsum) load8(dsum + c, nv, d[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
+            const int nv = anew(p.cols - c0 - j * SPAN);
+            dy[j].settle(nv);
+            sum[j].settle(nv);
+            if (p.dsum) dsum[j].settle(nv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                u[j][i] = (u[j][i] - mean) * rstd;             // past the row's end g is 0
-                dw[j][i] += g[j][i] * u[j][i];
-                db[j][i] += g[j][i];
-                g[j][i] *= w[j][i];
+                const float v = dy[j].value(i);                // past the row's end 0
+                u[j][i] = (sum[j].value(i) - mean) * scale;
+                dw[j][i] += v * u[j][i];
+                db[j][i] += v;
+                g[j][i] = v * w[j].value(i);
                 level += g[j][i];
                 along += g[j][i] * u[j][i];
             }
-        if constexpr (LOOP)
-            for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
-                float a[8], b[8], e[8];
-                load8(dy + c, p.cols - c, a);
-                load8(sum + c, p.cols - c, b);
-                load8(weight + c, p.cols - c, e);
+        }
+        Vec<T, END> add[NV];
+        if constexpr (NEXT) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    a[i] *= e[i];
-                    level += a[i];
-                    along += a[i] * ((b[i] - mean) * rstd);
-                }
-            }
+            for (int j = 0; j < NV; ++j) add[j] = dsum[j];
+            if (row + hop < p.rows) load(row + hop);
+        }
         // two parts in turn: a wave may start the next row's sums while another still reads this one's
         block_sums<WAVES>(level, along, part[turn]);
         level *= per, along *= per;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = c0 + j * SPAN;
+            const int c = c0 + j * SPAN, nv = anew(p.cols - c);
+            float v[8];
+            if constexpr (!NEXT) {
+                // from the row as it came: its products do not stay in registers over the exchange
+                dy[j].forget();
+                sum[j].forget();
+                add[j] = dsum[j];
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                g[j][i] = rstd * (g[j][i] - level - u[j][i] * along);
-                if (dsum) g[j][i] += d[j][i];
+                const float gi = NEXT ? g[j][i] : dy[j].value(i) * w[j].value(i);
+                const float ui = NEXT ? u[j][i] : (sum[j].value(i) - mean) * scale;
+                v[i] = scale * (gi - level - ui * along);
+                if (p.dsum) v[i] += add[j].value(i);
             }
-            if (c < p.cols) store8(dx + c, p.cols - c, g[j]);
+            if (nv > 0) store8(static_cast<T*>(p.dx) + row * p.lddx + c, END == END_WHOLE ? 8 : nv, v);
         }
-        if constexpr (LOOP)
-            for (int c = c0 + NV * SPAN; c < p.cols; c += SPAN) {
-                float a[8], b[8], e[8];
-                load8(dy + c, p.cols - c, a);
-                load8(sum + c, p.cols - c, b);
-                load8(weight + c, p.cols - c, e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = rstd * (a[i] * e[i] - level - (b[i] - mean) * rstd * along);
-                if (dsum) {
-                    load8(dsum + c, p.cols - c, e);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] += e[i];
-                }
-                store8(dx + c, p.cols - c, a);
-            }
+        if (!NEXT && row + hop < p.rows) load(row + hop);
     }
-    if constexpr (!LOOP) {
-        float* out = p.partial + (int64_t)blockIdx.x * 2 * p.cols;
+    float* out = p.partial + (int64_t)blockIdx.x * 2 * p.cols;
+    if constexpr (ROWS > 1) {
+        __shared__ float shares[ROWS][2][512 + 8];
+        const int wave = threadIdx.x >> 6;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = c0 + j * SPAN;
-            if (c >= p.cols) continue;
-            if (p.dweight) store8(out + c, p.cols - c, dw[j]);
-            if (p.dbias) store8(out + p.cols + c, p.cols - c, db[j]);
+        for (int i = 0; i < 8; ++i) shares[wave][0][c0 + i] = dw[0][i], shares[wave][1][c0 + i] = db[0][i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.cols; c += 64 * ROWS) {
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) a += shares[r][0][c], b += shares[r][1][c];
+            if (p.dweight) out[c] = a;
+            if (p.dbias) out[p.cols + c] = b;
         }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = c0 + j * SPAN;
+        if (c >= p.cols) continue;
+        if (p.dweight) store8(out + c, p.cols - c, dw[j]);
+        if (p.dbias) store8(out + p.cols + c, p.cols - c, db[j]);
+    }
+}
+
+// dx of rows past the registers, read twice.
+template <class T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void layer_norm_grad_long_kernel(const LayerNormGradArgs p)
+{
+    constexpr int SPAN = 64 * WAVES * 8;
+    __shared__ float part[2][WAVES][2];
+    const T* weight = static_cast<const T*>(p.weight);
+    const float per = 1.0f / (float)p.cols;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+        const T* sum = static_cast<const T*>(p.sum) + row * p.lds;
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        auto each = [&](auto&& f) {
+            for (int c = threadIdx.x * 8; c < p.cols; c += SPAN) {
+                float g[8], u[8], w[8];
+                load8(dy + c, p.cols - c, g);
+                load8(sum + c, p.cols - c, u);
+                load8(weight + c, p.cols - c, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] *= w[i], u[i] = (u[i] - mean) * rstd;
+                f(c, g, u);
+            }
+        };
+        float level = 0.0f, along = 0.0f;
+        each([&](int, const float (&g)[8], const float (&u)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) level += g[i], along += g[i] * u[i];
+        });
+        block_sums<WAVES>(level, along, part[turn]);
+        level *= per, along *= per;
+        each([&](int c, float (&g)[8], const float (&u)[8]) {
+            float d[8] = {};
+            if (p.dsum) load8(static_cast<const T*>(p.dsum) + row * p.ldd + c, p.cols - c, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = rstd * (g[i] - level - u[i] * along) + d[i];
+            store8(static_cast<T*>(p.dx) + row * p.lddx + c, p.cols - c, g);
+        });
     }
 }
 
@@ -361,52 +535,74 @@ template <class T> __global__ __launch_bounds__(1024) void layer_norm_join_kerne
     if (threadIdx.y == 0 && c < p.cols) out[c] = from_f32<T>(s);
 }
 
-// HIP takes grids of fewer than 2^32 threads; a workgroup per row of at most 512 threads reaches that at 2^23 rows.
+// Workgroups that walk `rows` rows, at most `most`, all with as many rows but the last one's.
+int even_groups(int rows, int most)
+{
+    const int per = (rows + most - 1) / most;
+    return per > 1 ? (rows + per - 1) / per : rows;
+}
+
+template <class T, bool E4M3, int WAVES, int NV> void launch_waves(const LayerNormArgs& p, int per_cu, hipStream_t stream)
+{
+    const int grid = even_groups(p.rows, per_cu * p.num_cu);
+    if (p.cols % 8 == 0) layer_norm_kernel<T, E4M3, WAVES, NV, END_WHOLE><<<grid, 64 * WAVES, 0, stream>>>(p);
+    else layer_norm_kernel<T, E4M3, WAVES, NV, END_CUT><<<grid, 64 * WAVES, 0, stream>>>(p);
+}
+
+// HIP takes grids of fewer than 2^32 threads; a workgroup per row of 512 threads reaches that at 2^23 rows.
 constexpr int GRID_ROWS = 1 << 22;
 
-template <class T, bool E4M3> hipError_t launch_rows(const LayerNormArgs& p, hipStream_t stream)
+template <class T, bool E4M3> hipError_t launch_type(const LayerNormArgs& p, hipStream_t stream)
 {
     const int v = (p.cols + 7) / 8;                            // vectors in a row
-    if (v <= 64) layer_norm_kernel<T, E4M3, 1, 1, false><<<p.rows, 64, 0, stream>>>(p);
-    else if (v <= 256) layer_norm_kernel<T, E4M3, 4, 1, false><<<p.rows, 256, 0, stream>>>(p);
-    else if (v <= 512) layer_norm_kernel<T, E4M3, 4, 2, false><<<p.rows, 256, 0, stream>>>(p);
-    else if (v <= 1024) layer_norm_kernel<T, E4M3, 4, 4, false><<<p.rows, 256, 0, stream>>>(p);
-    else if (v <= 2048) layer_norm_kernel<T, E4M3, 8, 4, false><<<p.rows, 512, 0, stream>>>(p);
-    else layer_norm_kernel<T, E4M3, 8, 4, true><<<p.rows, 512, 0, stream>>>(p);
+    if (p.cols < 8) layer_norm_kernel<T, E4M3, 1, 1, END_SHORT><<<even_groups(p.rows, 24 * p.num_cu), 64, 0, stream>>>(p);
+    else if (v <= 64) launch_waves<T, E4M3, 1, 1>(p, 24, stream);
+    else if (v <= 256) launch_waves<T, E4M3, 4, 1>(p, 6, stream);
+    else if (v <= 512) launch_waves<T, E4M3, 4, 2>(p, 4, stream);
+    else if (v <= 1024) launch_waves<T, E4M3, 8, 2>(p, 2, stream);
+    else if (v <= 1536) launch_waves<T, E4M3, 12, 2>(p, 1, stream);
+    else {
+        using Out = typename std::conditional<E4M3, uint8_t, T>::type;
+        for (int64_t first = 0; first < p.rows; first += GRID_ROWS) {
+            LayerNormArgs part = p;
+            part.rows = (int)(p.rows - first < GRID_ROWS ? p.rows - first : GRID_ROWS);
+            part.x = static_cast<const T*>(p.x) + first * p.ldx;
+            if (p.residual) part.residual = static_cast<const T*>(p.residual) + first * p.ldr;
+            part.y = static_cast<Out*>(p.y) + first * p.ldy;
+            if (p.sum) part.sum = static_cast<T*>(p.sum) + first * p.lds;
+            if (p.mean) part.mean = p.mean + first;
+            if (p.rstd) part.rstd = p.rstd + first;
+            if (p.scale) part.scale = p.scale + first;
+            layer_norm_long_kernel<T, E4M3, 8, 4><<<part.rows, 512, 0, stream>>>(part);
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
+    }
     return hipGetLastError();
 }
 
-template <class T, bool E4M3> hipError_t launch_type(const LayerNormArgs& all, hipStream_t stream)
+template <class T, int WAVES, int ROWS, int NV, bool NEXT> void launch_grad_waves(const LayerNormGradArgs& p, hipStream_t stream)
 {
-    using Out = typename std::conditional<E4M3, uint8_t, T>::type;
-    for (int64_t first = 0; first < all.rows; first += GRID_ROWS) {
-        LayerNormArgs p = all;
-        p.rows = (int)(all.rows - first < GRID_ROWS ? all.rows - first : GRID_ROWS);
-        p.x = static_cast<const T*>(all.x) + first * all.ldx;
-        if (p.residual) p.residual = static_cast<const T*>(all.residual) + first * all.ldr;
-        p.y = static_cast<Out*>(all.y) + first * all.ldy;
-        if (p.sum) p.sum = static_cast<T*>(all.sum) + first * all.lds;
-        if (p.mean) p.mean = all.mean + first;
-        if (p.rstd) p.rstd = all.rstd + first;
-        if (p.scale) p.scale = all.scale + first;
-        const hipError_t err = launch_rows<T, E4M3>(p, stream);
-        if (err != hipSuccess) return err;
-    }
-    return hipSuccess;
+    constexpr int THREADS = 64 * WAVES * ROWS;
+    if (p.cols % 8 == 0) layer_norm_grad_kernel<T, WAVES, ROWS, NV, NEXT, END_WHOLE><<<p.groups, THREADS, 0, stream>>>(p);
+    else layer_norm_grad_kernel<T, WAVES, ROWS, NV, NEXT, END_CUT><<<p.groups, THREADS, 0, stream>>>(p);
 }
 
-constexpr int GRAD_MOST = 16384;   // columns whose shares of dweight and dbias a workgroup keeps in registers
+constexpr int SHORT_ROWS = 4;      // rows of up to 512 columns that a workgroup walks side by side
 
 template <class T> hipError_t launch_grad_type(const LayerNormGradArgs& p, hipStream_t stream)
 {
     const int v = (p.cols + 7) / 8;
-    if (v <= 64) layer_norm_grad_kernel<T, 1, 1, false><<<p.groups, 64, 0, stream>>>(p);
-    else if (v <= 256) layer_norm_grad_kernel<T, 4, 1, false><<<p.groups, 256, 0, stream>>>(p);
-    else if (v <= 512) layer_norm_grad_kernel<T, 4, 2, false><<<p.groups, 256, 0, stream>>>(p);
-    else if (v <= 1024) layer_norm_grad_kernel<T, 8, 2, false><<<p.groups, 512, 0, stream>>>(p);
-    else if (p.cols <= GRAD_MOST) layer_norm_grad_kernel<T, 16, 2, false><<<p.groups, 1024, 0, stream>>>(p);
+    if (p.cols < 8)
+        layer_norm_grad_kernel<T, 1, SHORT_ROWS, 1, true, END_SHORT><<<p.groups, 64 * SHORT_ROWS, 0, stream>>>(p);
+    else if (v <= 64) launch_grad_waves<T, 1, SHORT_ROWS, 1, true>(p, stream);
+    else if (v <= 256) launch_grad_waves<T, 4, 1, 1, true>(p, stream);
+    else if (v <= 512) launch_grad_waves<T, 8, 1, 1, true>(p, stream);
+    else if (v <= 1024) launch_grad_waves<T, 16, 1, 1, true>(p, stream);
+    else if (v <= 1536) launch_grad_waves<T, 12, 1, 2, sizeof(T) == 2>(p, stream);
+    else if (v <= 2048) launch_grad_waves<T, 16, 1, 2, false>(p, stream);
     else {
-        layer_norm_grad_kernel<T, 8, 2, true><<<p.groups, 512, 0, stream>>>(p);
+        if (p.rows) layer_norm_grad_long_kernel<T, 8><<<p.groups, 512, 0, stream>>>(p);
         if (p.dweight || p.dbias)
             layer_norm_weight_kernel<T><<<dim3(p.groups, (v + 63) / 64), 64, 0, stream>>>(p);
     }
@@ -425,8 +621,9 @@ hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStr
 
 int layer_norm_grad_groups(int rows, int cols, int num_cu)
 {
-    const int per_cu = cols <= 512 ? 16 : cols <= 4096 ? 4 : cols <= 8192 ? 2 : 1;
-    return rows < num_cu * per_cu ? (rows > 1 ? rows : 1) : num_cu * per_cu;
+    const int per_cu = cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
+    const int walks = cols <= 512 ? (rows + SHORT_ROWS - 1) / SHORT_ROWS : rows;
+    return walks > 1 ? even_groups(walks, per_cu * num_cu) : 1;
 }
 
 hipError_t launch_layer_norm_grad(DType dt, const LayerNormGradArgs& p, hipStream_t stream)

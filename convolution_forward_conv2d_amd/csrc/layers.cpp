@@ -28,7 +28,8 @@ mic_status mic_layer_norm(mic_handle handle, mic_dtype dtype, mic_dtype out_dtyp
     if (!weight || !aligned(weight, e) || !aligned(bias, e)) return MIC_STATUS_BAD_PARAM;
     if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(scale, 4)) return MIC_STATUS_BAD_PARAM;
     if (e4m3 && !scale) return MIC_STATUS_BAD_PARAM;
-    const LayerNormArgs p = {rows, cols, (float)eps, x, ldx, residual, ldr, weight, bias, y, ldy, sum, lds, mean, rstd, scale};
+    const LayerNormArgs p = {rows, cols, (float)eps, x, ldx, residual, ldr, weight, bias, y, ldy, sum, lds, mean, rstd, scale,
+                             handle->num_cu};
     return launched(launch_layer_norm(device_type(dtype), e4m3, p, handle->stream));
 }
 

@@ -26,9 +26,11 @@ def pitched(t, pad, offset=0):
     return v
 
 
-# one column; each kernel's last width and the next: 512, 2048, 4096, 8192, 16384
+# one column, fewer than eight; each kernel's last width and the next: 512, 2048, 4096, 8192, 12288, 16384; rows cut at every place of
+# a vector of eight
 SIZES = [(1, 1), (1, 8), (3, 7), (5, 512), (2, 513), (4, 2048), (3, 2049), (2, 4096), (3, 4097), (2, 8192), (1, 8195),
-         (2, 16384), (2, 16385), (1, 20001), (601, 300), (1030, 1001)]
+         (2, 16384), (2, 16385), (1, 20001), (601, 300), (1030, 1001), (9, 510), (7, 1027), (4, 4092), (5, 8190), (3, 9213),
+         (2, 12288), (2, 12295), (2, 14001)]
 
 
 @pytest.mark.parametrize("m,c", SIZES)
