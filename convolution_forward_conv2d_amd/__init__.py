@@ -9,7 +9,8 @@ ctypes handles); ``conv2d_forward`` / ``ConvPlan`` and
 ``conv2d_backward_data`` / ``DgradPlan`` and ``conv2d_backward_filter`` /
 ``WgradPlan`` wrap them for torch tensors.  The feed-forward operators'
 tensor functions (``rms_norm``, ``linear``, ``gated_linear`` and their
-``_backward``) are in ``feed_forward.py`` and exported here.
+``_backward``) are in ``feed_forward.py``, ``layer_norm``, ``dropout`` and
+``linear_cross_entropy`` with theirs in ``training.py``; both are exported here.
 
 There is no fallback: if the library is missing the import fails.
 """
@@ -52,6 +53,11 @@ MIC_ACT_GELU_TANH = 3
 MIC_ACT_SILU = 4
 ACTIVATIONS = {"none": MIC_ACT_NONE, "relu": MIC_ACT_RELU, "gelu": MIC_ACT_GELU, "gelu_tanh": MIC_ACT_GELU_TANH,
                "silu": MIC_ACT_SILU}
+
+MIC_REDUCTION_NONE = 0
+MIC_REDUCTION_SUM = 1
+MIC_REDUCTION_MEAN = 2
+REDUCTIONS = {"none": MIC_REDUCTION_NONE, "sum": MIC_REDUCTION_SUM, "mean": MIC_REDUCTION_MEAN}
 
 _TORCH_DTYPE = {torch.float32: MIC_DTYPE_F32, torch.float64: MIC_DTYPE_F64,
                 torch.bfloat16: MIC_DTYPE_BF16}
@@ -133,6 +139,16 @@ _SIGS = {
                                  ctypes.c_size_t], _i),
     "mic_dropout": ([_vp, _i, _i64, _i64, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _vp, _vp, _i64, _vp, _i64, _vp,
                      _i64], _i),
+    "mic_linear_cross_entropy_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_cross_entropy_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_cross_entropy": ([_vp, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _i64, ctypes.c_double, _vp, _vp,
+                                  _vp, _vp, ctypes.c_size_t], _i),
+    "mic_linear_cross_entropy_kernel_name": ([_vp, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
+    "mic_linear_cross_entropy_backward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_cross_entropy_backward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
+    "mic_linear_cross_entropy_backward": ([_vp, _i, _i, _i, _i, _vp, _i, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                                           ctypes.c_double, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_size_t], _i),
+    "mic_linear_cross_entropy_backward_kernel_name": ([_vp, _i, _i, _i, _i, _i, ctypes.c_char_p, ctypes.c_size_t], _i),
     "mic_linear_forward_workspace": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward_workspace_aligned": ([_vp, _i, _i, _i, _i, _szp], _i),
     "mic_linear_forward": ([_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
@@ -432,6 +448,33 @@ def mic_dropout(*args):
     _check(lib().mic_dropout(*args), "mic_dropout")
 
 
+def mic_linear_cross_entropy_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_cross_entropy_workspace, "mic_linear_cross_entropy_workspace", handle, dtype, m, n, k)
+
+
+def mic_linear_cross_entropy_workspace_aligned(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_cross_entropy_workspace_aligned, "mic_linear_cross_entropy_workspace_aligned", handle,
+                  dtype, m, n, k)
+
+
+def mic_linear_cross_entropy(*args):
+    _check(lib().mic_linear_cross_entropy(*args), "mic_linear_cross_entropy")
+
+
+def mic_linear_cross_entropy_backward_workspace(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_cross_entropy_backward_workspace, "mic_linear_cross_entropy_backward_workspace", handle,
+                  dtype, m, n, k)
+
+
+def mic_linear_cross_entropy_backward_workspace_aligned(handle, dtype, m, n, k):
+    return _bytes(lib().mic_linear_cross_entropy_backward_workspace_aligned,
+                  "mic_linear_cross_entropy_backward_workspace_aligned", handle, dtype, m, n, k)
+
+
+def mic_linear_cross_entropy_backward(*args):
+    _check(lib().mic_linear_cross_entropy_backward(*args), "mic_linear_cross_entropy_backward")
+
+
 def mic_linear_forward_workspace(handle, dtype, m, n, k):
     return _bytes(lib().mic_linear_forward_workspace, "mic_linear_forward_workspace", handle, dtype, m, n, k)
 
@@ -506,6 +549,14 @@ def mic_linear_backward_kernel_name(handle, dtype, act, m, n, k, aligned=True):
 
 def mic_gated_linear_backward_kernel_name(handle, dtype, m, n, k, aligned=True):
     return _name("mic_gated_linear_backward_kernel_name", handle, dtype, m, n, k, aligned)
+
+
+def mic_linear_cross_entropy_kernel_name(handle, dtype, m, n, k, aligned=True):
+    return _name("mic_linear_cross_entropy_kernel_name", handle, dtype, m, n, k, aligned)
+
+
+def mic_linear_cross_entropy_backward_kernel_name(handle, dtype, m, n, k, aligned=True):
+    return _name("mic_linear_cross_entropy_backward_kernel_name", handle, dtype, m, n, k, aligned)
 
 
 # ---------------------------------------------------------------- torch-facing helpers
@@ -956,4 +1007,5 @@ class BlockedConvPlan(ConvPlan):
 
 from .feed_forward import (RmsNorm, gated_linear, gated_linear_backward, linear, linear_backward,  # noqa: E402,F401
                            rms_norm, rms_norm_backward)
-from .training import (LayerNorm, dropout, dropout_backward, layer_norm, layer_norm_backward)  # noqa: E402,F401
+from .training import (LayerNorm, LinearCrossEntropy, dropout, dropout_backward, layer_norm,  # noqa: E402,F401
+                       layer_norm_backward, linear_cross_entropy, linear_cross_entropy_backward)

@@ -536,10 +536,116 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
+// Numbers of a loss; false: to be looked at by the Python checks.
+bool loss_numbers(PyObject* index, PyObject* share, int64_t& ignore, double& smoothing)
+{
+    if (!PyLong_Check(index) || PyBool_Check(index) || !(PyFloat_Check(share) || (PyLong_Check(share) && !PyBool_Check(share))))
+        return false;
+    ignore = PyLong_AsLongLong(index);
+    smoothing = PyFloat_AsDouble(share);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    return true;
+}
+
+// The operands of a loss: w (n, k), target of x's leading shape, bias (n) or none.
+bool loss_operands(const Tensor& x, const Tensor& w, const Tensor& target, const Tensor* bias, int64_t n, int64_t k)
+{
+    const auto type = x.scalar_type();
+    return n > 0 && n < INT32_MAX && plain(w, type, x, {n, k}) && target.scalar_type() == at::kLong
+           && target.device() == x.device() && target.is_contiguous() && target.sizes() == x.sizes().slice(0, x.dim() - 1)
+           && (!bias || plain(*bias, type, x, {n}));
+}
+
+// (x, w, target, bias, reduction, ignore_index, label_smoothing) -> (loss, lse, count)
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *x, *w, *target, *bias;
+    int64_t m, k, ignore;
+    double smoothing;
+    mic_dtype d;
+    if (n_args != 7 || !plain_rows(x = tensor(a[0]), m, k) || !(w = tensor(a[1])) || !(target = tensor(a[2]))
+        || !maybe(a[3], bias) || !dtype_of(*x, d) || d == MIC_DTYPE_F8_E4M3 || w->dim() != 2
+        || !loss_numbers(a[5], a[6], ignore, smoothing))
+        return none();
+    const long reduction = PyLong_AsLong(a[4]);
+    if (reduction == -1 && PyErr_Occurred()) return nullptr;
+    const int64_t n = w->size(0);
+    if (!loss_operands(*x, *w, *target, bias, n, k)) return none();
+    const mic_handle h = handle_on(x->get_device());
+    const bool aligned = even(*x) && even(*w);
+    Tensor space;
+    size_t bytes;
+    if (!h || !workspace(aligned ? 11 : 12, d, m, n, k, *x, space, bytes, [&](size_t* b) {
+            return aligned ? mic_linear_cross_entropy_workspace_aligned(h, d, (int)m, (int)n, (int)k, b)
+                           : mic_linear_cross_entropy_workspace(h, d, (int)m, (int)n, (int)k, b);
+        }))
+        return none();
+    const bool each = reduction == MIC_REDUCTION_NONE;
+    Tensor lse = at::empty(target->sizes(), x->options().dtype(at::kFloat)), loss, count;
+    if (each) loss = like(lse, at::kFloat);
+    else loss = at::empty({}, lse.options()), count = at::empty({}, lse.options());
+    if (mic_linear_cross_entropy(h, d, (mic_reduction)reduction, (int)m, (int)n, (int)k, x->data_ptr(), k, w->data_ptr(), k,
+                                 data(bias), static_cast<const int64_t*>(target->data_ptr()), ignore, smoothing, floats(&loss),
+                                 floats(&lse), each ? nullptr : floats(&count), bytes ? space.data_ptr() : nullptr, bytes)
+        != MIC_STATUS_SUCCESS)
+        return none();
+    return pack({wrap(loss), wrap(lse), each ? none() : wrap(count)});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dloss, x, w, target, lse, bias, count, ignore_index, label_smoothing, need_dx, need_dw, need_dbias) -> (dx, dw, dbias)
+PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *dloss, *x, *w, *target, *lse, *bias, *count;
+    int64_t m, k, ignore;
+    double smoothing;
+    mic_dtype d;
+    if (n_args != 12 || !(dloss = tensor(a[0])) || !plain_rows(x = tensor(a[1]), m, k) || !(w = tensor(a[2]))
+        || !(target = tensor(a[3])) || !(lse = tensor(a[4])) || !maybe(a[5], bias) || !maybe(a[6], count) || !dtype_of(*x, d)
+        || d == MIC_DTYPE_F8_E4M3 || w->dim() != 2 || !loss_numbers(a[7], a[8], ignore, smoothing))
+        return none();
+    bool need_dx, need_dw, need_db;
+    if (!flag(a[9], "need_dx", need_dx) || !flag(a[10], "need_dw", need_dw) || !flag(a[11], "need_dbias", need_db)) return nullptr;
+    const int64_t n = w->size(0);
+    const bool each = dloss->dim() > 0 && dloss->sizes() == target->sizes();
+    if (!loss_operands(*x, *w, *target, bias, n, k) || !plain_scale(*lse, *x, m) || !plain_scale(*dloss, *x, each ? m : 1)
+        || (count && !plain_scale(*count, *x, 1)))
+        return none();
+    const mic_handle h = handle_on(x->get_device());
+    const bool aligned = even(*x) && even(*w);
+    Tensor space;
+    size_t bytes;
+    if (!h || !workspace(aligned ? 13 : 14, d, m, n, k, *x, space, bytes, [&](size_t* b) {
+            return aligned ? mic_linear_cross_entropy_backward_workspace_aligned(h, d, (int)m, (int)n, (int)k, b)
+                           : mic_linear_cross_entropy_backward_workspace(h, d, (int)m, (int)n, (int)k, b);
+        }))
+        return none();
+    const auto type = x->scalar_type();
+    need_db = need_db && bias;
+    Tensor dx, dw, db;
+    if (need_dx) dx = like(*x, type);
+    if (need_dw) dw = like(*w, type);
+    if (need_db) db = like(*bias, type);
+    if (mic_linear_cross_entropy_backward(h, d, (int)m, (int)n, (int)k, floats(dloss), each, x->data_ptr(), k, w->data_ptr(), k,
+                                          data(bias), static_cast<const int64_t*>(target->data_ptr()), ignore, smoothing,
+                                          floats(lse), floats(count), need_dx ? dx.data_ptr() : nullptr, k,
+                                          need_dw ? dw.data_ptr() : nullptr, k, need_db ? db.data_ptr() : nullptr,
+                                          bytes ? space.data_ptr() : nullptr, bytes)
+        != MIC_STATUS_SUCCESS)
+        return none();
+    return pack({need_dx ? wrap(dx) : none(), need_dw ? wrap(dw) : none(), need_db ? wrap(db) : none()});
+    END_HANDLE_TH_ERRORS
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(rms_norm), FAST(rms_norm_backward), FAST(linear), FAST(linear_backward),
                          FAST(gated_linear), FAST(gated_linear_backward), FAST(layer_norm),
-                         FAST(layer_norm_backward), FAST(dropout), {nullptr, nullptr, 0, nullptr}};
+                         FAST(layer_norm_backward), FAST(dropout), FAST(linear_cross_entropy), FAST(linear_cross_entropy_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The feed-forward operators on plainly laid out tensors.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 

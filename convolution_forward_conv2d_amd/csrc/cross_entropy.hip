@@ -1,0 +1,237 @@
+// cross_entropy.hip -- cross entropy around the products that make the logits:
+// logits that are in memory, for the products too small for the fused epilogues
+// (loss_tile.h), and what follows the pieces of a row:
+//
+//   largest = max over runs,  sum = sum over runs of sum_run e^(largest_run - largest)
+//   lse = largest + log(sum)
+//   loss = log(sum) + (1 - a) (largest - z_t) + a (largest - mean(z))
+//
+// so a confident row's loss is not the difference of two large numbers.  All
+// fp32, joined in a fixed order.
+#include "linear_common.h"
+#include "kernels.h"
+
+namespace miconv {
+
+namespace {
+
+// (largest, sum of e^(z - largest)) of two sets of logits together.
+__device__ __forceinline__ void join_runs(float& most, float& sum, float most2, float sum2)
+{
+    const float top = fmaxf(most, most2);
+    // equal ones need no factor, two empty ones (-infinity) have none
+    sum = (most == top ? sum : sum * exponential<true>(most - top)) + (most2 == top ? sum2 : sum2 * exponential<true>(most2 - top));
+    most = top;
+}
+
+constexpr int THREADS = 256;
+
+template <class T> __device__ __forceinline__ float logit(const LossRowsArgs& p, int64_t row, int c)
+{
+    const float* z = p.z + row * p.ld + c;
+    float v = z[0];
+    for (int s = 1; s < p.splits; ++s) v += z[s * p.rows * p.ld];
+    return p.bias ? v + to_f32(static_cast<const T*>(p.bias)[c]) : v;
+}
+
+// A workgroup per row and run of its columns.
+template <class T> __global__ __launch_bounds__(THREADS) void loss_rows_kernel(const LossRowsArgs p)
+{
+    __shared__ float part[THREADS / 64][3];
+    const int runs = (p.cols + p.run - 1) / p.run;
+    for (int64_t item = blockIdx.x; item < (int64_t)p.rows * runs; item += gridDim.x) {
+        const int64_t row = item / runs;
+        const int run = (int)(item - row * runs), first = run * p.run, last = min(first + p.run, p.cols);
+        const int at = loss_column(p.loss, p.loss.target[row]);
+        float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
+        for (int c = first + threadIdx.x; c < last; c += 4 * THREADS) {
+            float z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) z[u] = c + u * THREADS < last ? logit<T>(p, row, c + u * THREADS) : -__builtin_inff();
+            float top = most;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                top = fmaxf(top, z[u]);
+                if (c + u * THREADS < last) total += z[u];
+                if (c + u * THREADS == at) p.loss.hit[row] = z[u];
+            }
+            const float from = top == -__builtin_inff() ? 0.0f : top;
+            sum *= exponential<true>(most - from);             // nothing before: 0 e^-infinity
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sum += exponential<true>(z[u] - from);
+            most = top;
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            join_runs(most, sum, __shfl_xor(most, o), __shfl_xor(sum, o));
+            total += __shfl_xor(total, o);
+        }
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) part[wave][0] = most, part[wave][1] = sum, part[wave][2] = total;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int w = 1; w < THREADS / 64; ++w) {
+                join_runs(most, sum, part[w][0], part[w][1]);
+                total += part[w][2];
+            }
+            const int64_t to = (int64_t)(p.loss.part_first + run) * p.rows + row;
+            reinterpret_cast<float2*>(p.loss.part)[to] = float2{most, sum};
+            if (p.loss.part_z) p.loss.part_z[to] = total;
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int COLS = 32;           // groups of eight columns per block
+constexpr int LANES = 8;           // rows a block walks side by side
+
+// dz of logits in memory, and its column sums.
+template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient_kernel(const LossRowsArgs p)
+{
+    constexpr bool EXACT = sizeof(T) == 4;
+    const int c = (blockIdx.x * COLS + threadIdx.x) * 8, nv = p.cols - c;
+    const float every = p.loss.smooth / (float)p.loss.classes, goal = 1.0f - p.loss.smooth + every;
+    float total[8] = {};
+    if (c < p.dz_pitch) {
+        float bias[8] = {};
+        if (p.bias) load8(static_cast<const T*>(p.bias) + c, nv, bias);
+        for (int r = blockIdx.y * LANES + threadIdx.y; r < p.rows; r += gridDim.y * LANES) {
+            const float* z = p.z + (int64_t)r * p.ld + c;
+            float v[8];
+            load8(z, nv, v);
+            for (int s = 1; s < p.splits; ++s) {
+                float more[8];
+                load8(z + (int64_t)s * p.rows * p.ld, nv, more);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += more[i];
+            }
+            const LossRow row = loss_row(p.loss, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = i < nv ? loss_gradient<EXACT>(row, v[i] + bias[i], c + i, goal, every) : 0.0f;
+                total[i] += v[i];
+            }
+            store8(static_cast<T*>(p.dz) + (int64_t)r * p.dz_pitch + c, 8, v);
+        }
+    }
+    if (!p.sums) return;
+    __shared__ float part[LANES][COLS * 8 + 4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[threadIdx.y][threadIdx.x * 8 + i] = total[i];
+    __syncthreads();
+    const int k = threadIdx.y * COLS + threadIdx.x;
+    float s = 0.0f;
+#pragma unroll
+    for (int y = 0; y < LANES; ++y) s += part[y][k];
+    const int col = blockIdx.x * COLS * 8 + k;
+    if (col < p.cols) p.sums[(int64_t)blockIdx.y * p.cols + col] = s;
+}
+
+__device__ __forceinline__ void finish_row(const LossArgs& p, int64_t row, float most, float sum, float total, float* lse, float* loss)
+{
+    const int64_t target = p.target[row];
+    const float log_sum = logf(sum);
+    lse[row] = most + log_sum;
+    float v = 0.0f;
+    if (target != p.ignore) {
+        if (loss_column(p, target) < 0) {
+            v = __builtin_nanf("");
+        } else if (most == -__builtin_inff() && sum == 0.0f) {
+            v = __builtin_inff();                              // no class left: the target's share is nothing
+        } else {
+            v = log_sum + (1.0f - p.smooth) * (most - p.hit[row]);
+            if (p.smooth > 0.0f) v += p.smooth * (most - total / (float)p.classes);
+        }
+    }
+    loss[row] = v;
+}
+
+// 32 rows a block, 32 lanes of runs.
+__global__ __launch_bounds__(1024) void loss_join_kernel(const LossArgs p, int rows, int runs, float* lse, float* loss)
+{
+    __shared__ float part[32][32][3];
+    for (int64_t first = (int64_t)blockIdx.x * 32; first < rows; first += (int64_t)gridDim.x * 32) {
+        const int64_t row = first + threadIdx.x;
+        float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
+        if (row < rows) {
+#pragma unroll 4
+            for (int r = threadIdx.y; r < runs; r += 32) {
+                const float2 v = reinterpret_cast<const float2*>(p.part)[(int64_t)r * rows + row];
+                join_runs(most, sum, v.x, v.y);
+                if (p.part_z) total += p.part_z[(int64_t)r * rows + row];
+            }
+        }
+        float* mine = part[threadIdx.y][threadIdx.x];
+        mine[0] = most, mine[1] = sum, mine[2] = total;
+        __syncthreads();
+        if (threadIdx.y == 0 && row < rows) {
+            for (int y = 1; y < 32; ++y) {
+                join_runs(most, sum, part[y][threadIdx.x][0], part[y][threadIdx.x][1]);
+                total += part[y][threadIdx.x][2];
+            }
+            finish_row(p, row, most, sum, total, lse, loss);
+        }
+        __syncthreads();
+    }
+}
+
+__global__ __launch_bounds__(1024) void loss_reduce_kernel(const LossArgs p, int rows, const float* loss, bool mean, float* total,
+                                                           float* count)
+{
+    __shared__ float part[16];
+    __shared__ int many[16];
+    float sum = 0.0f;
+    int n = 0;
+    for (int64_t r = threadIdx.x; r < rows; r += 1024) {
+        sum += loss[r];
+        n += p.target[r] != p.ignore;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o), n += __shfl_xor(n, o);
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) part[wave] = sum, many[wave] = n;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < 16; ++w) sum += part[w], n += many[w];
+    *total = !mean ? sum : n ? sum / (float)n : 0.0f;
+    *count = (float)n;
+}
+
+}  // namespace
+
+hipError_t launch_loss_rows(DType dt, const LossRowsArgs& p, hipStream_t stream)
+{
+    const int64_t items = (int64_t)p.rows * ((p.cols + p.run - 1) / p.run);
+    const uint32_t grid = (uint32_t)(items < 1 << 20 ? items : 1 << 20);
+    if (dt == DType::F32) loss_rows_kernel<float><<<grid, THREADS, 0, stream>>>(p);
+    else loss_rows_kernel<Bf16><<<grid, THREADS, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_gradient(DType dt, const LossRowsArgs& p, hipStream_t stream)
+{
+    const int groups = slope_row_groups(p.rows, p.cols);
+    const dim3 grid((uint32_t)((p.dz_pitch + COLS * 8 - 1) / (COLS * 8)), groups), block(COLS, LANES);
+    if (dt == DType::F32) loss_gradient_kernel<float><<<grid, block, 0, stream>>>(p);
+    else loss_gradient_kernel<Bf16><<<grid, block, 0, stream>>>(p);
+    hipError_t err = hipGetLastError();
+    if (err == hipSuccess && p.sums) err = launch_column_join(dt, p.sums, groups, p.cols, p.dbias, stream);
+    return err;
+}
+
+hipError_t launch_loss_join(const LossArgs& p, int rows, int runs, float* lse, float* loss, hipStream_t stream)
+{
+    const int64_t grid = ((int64_t)rows + 31) / 32;
+    loss_join_kernel<<<(uint32_t)(grid < 1 << 20 ? grid : 1 << 20), dim3(32, 32), 0, stream>>>(p, rows, runs, lse, loss);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_reduce(const LossArgs& p, int rows, const float* loss, bool mean, float* total, float* count,
+                              hipStream_t stream)
+{
+    loss_reduce_kernel<<<1, 1024, 0, stream>>>(p, rows, loss, mean, total, count);
+    return hipGetLastError();
+}
+
+}  // namespace miconv

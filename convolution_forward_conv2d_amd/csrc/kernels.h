@@ -172,10 +172,12 @@ hipError_t launch_bwd_filter_rows(Variant v, const ConvParams& p, hipStream_t st
 //
 // A product with its epilogue (linear_common.h): x W^T of a linear or gated
 // layer, dz W for dx, dz^T x for dW.
-enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD };
+// A classifier's head and its loss: x W^T with each row reduced to its softmax's
+// statistics (LOSS) or turned into the gradient of the loss (LOGITS_GRAD).
+enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD, LOSS, LOGITS_GRAD };
 // Operands, and the outputs where they differ; SHORT: e4m3's own matrix
 // instruction (its sums are short, see linear_common.h).
-enum class ProductType : int { F32, BF16, E4M3_BF16, E4M3_F32, E4M3_BF16_SHORT, E4M3_F32_SHORT };
+enum class ProductType : int { F32, BF16, E4M3_BF16, E4M3_F32, E4M3_BF16_SHORT, E4M3_F32_SHORT, BF16_F32 };
 
 struct ProductArgs;
 // Any sizes, pitches and alignments (linear_any.hip); tile 64 or 128.
@@ -192,6 +194,11 @@ enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T1
 hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream);
 hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
+// LOSS, LOGITS_GRAD and bf16 products with fp32 outputs (linear_fast_loss.hip).
+hipError_t launch_product_fast_loss(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
+                                    hipStream_t stream);
+// Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them.
+int loss_columns(ProductType type, FastTile tile);
 // Rows of `bytes` bytes at any pitch into rows of `to_pitch` (a multiple of 16), zeros behind each (linear_pack.hip).
 constexpr int PACK_JOBS = 3;
 struct PackJob {
@@ -223,6 +230,47 @@ struct SlopeArgs {
 };
 int slope_row_groups(int rows, int cols);
 hipError_t launch_slope(DType dt, const SlopeArgs& p, hipStream_t stream);
+
+// Cross entropy of logits z (cross_entropy.hip; the arguments' meaning in linear_common.h).
+struct LossArgs {
+    const int64_t* target;    // class of each row
+    int64_t ignore;           // a target that marks a row without one
+    int classes;              // in all
+    int first;                // class of the product's first column
+    float smooth;             // share of the goal that goes to all classes alike
+    // forward: of each row and each run of columns the largest logit and the sum of e^(z - largest), [run][row], and with
+    // smoothing the sum of z; of each row the target's logit
+    float* part;
+    float* part_z;
+    float* hit;
+    int part_first;           // run of the product's first column
+    // gradient
+    const float* lse;
+    const float* dloss;       // one for all rows, or each row's
+    int dloss_rows;
+    const float* count;       // what the loss was divided by, or null
+};
+struct LossRowsArgs {
+    LossArgs loss;
+    int rows, cols;           // of the logits here
+    const float* z;           // `splits` partial sums of the logits, rows of ld
+    int64_t ld;
+    int splits;
+    const void* bias;         // of the classes from the first column on, or null
+    int run;                  // columns of a run
+    // gradient: dz in the tensors' type, zeros from cols to its pitch; column sums as SlopeArgs'
+    void* dz;
+    int64_t dz_pitch;
+    float* sums;
+    void* dbias;
+};
+hipError_t launch_loss_rows(DType dt, const LossRowsArgs& p, hipStream_t stream);
+hipError_t launch_loss_gradient(DType dt, const LossRowsArgs& p, hipStream_t stream);
+// A row's runs joined: its lse, and its loss (0 where it has no target, no number where that is no class).
+hipError_t launch_loss_join(const LossArgs& p, int rows, int runs, float* lse, float* loss, hipStream_t stream);
+// The losses' sum, or mean over the rows that have a target, and their number.
+hipError_t launch_loss_reduce(const LossArgs& p, int rows, const float* loss, bool mean, float* total, float* count,
+                              hipStream_t stream);
 
 // Root-mean-square norm of s = x + residual (rms_norm.hip).
 struct NormArgs {

@@ -13,28 +13,13 @@
 #include "host_checks.h"
 #include "linear_common.h"
 #include "kernels.h"
+#include "product.h"
 
 namespace {
 
 using namespace miconv;
 
 bool valid_act(mic_activation a) { return (int)a >= 0 && (int)a <= (int)MIC_ACT_SILU; }
-
-// How a product runs.
-struct Plan {
-    bool few;                // linear_few.hip
-    bool fast;               // linear_fast.h, else linear_any.hip
-    miconv::FastTile fast_tile;
-    int tile;                // linear_any.hip's
-    int splits;
-    int64_t part_ld;
-    int64_t pack_a, pack_b;  // bytes of a packed operand's row, 0: read where it is
-    size_t a_bytes, b_bytes; // of the packed copies (b_bytes: each of a gated layer's two)
-    size_t bytes;            // workspace: the copies, then the partial sums
-    double us;
-};
-
-int element_bytes(ProductType t) { return t == ProductType::F32 ? 4 : t == ProductType::BF16 ? 2 : 1; }
 
 // Operands' rows (as they lie in memory) and their lengths in elements.
 struct Extent {
@@ -56,7 +41,7 @@ Extent extent_of(Product kind, int m, int n, int k)
 // outputs of 8192 terms take 754 us in four rounds of 256 x 256 and 859 in 5.4
 // of 256 x 192; 4096 x 9216 of 4096 terms, 2.25 rounds of the one and exactly
 // three of the other, 311 and 258.
-constexpr double kLaunchUs = 4.0, kBytesPerUs = 4.0e6, kReadPerUs = 4.5e6;
+constexpr double kReadPerUs = 4.5e6;
 struct TileCost {
     int bm, bn;
     double step, tile;
@@ -76,6 +61,10 @@ double few_us(int num_cu, int m, int raw_n, bool gated, double row_bytes, bool a
     const double x_rows = (m + 15) / 16 * 16;
     return 2.5 + std::max(raw_n * row_bytes / kReadPerUs, groups * (columns + x_rows) * row_bytes / rate);
 }
+
+}  // namespace
+
+namespace miconv {
 
 // The cheapest way through a product of m x n outputs and k_segments * k terms.
 // `aligned_a` / `aligned_b`: the operand's rows can be read 16 bytes at a time.
@@ -97,6 +86,8 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const double b_bytes = (double)raw_n * k * k_segments * e, read_us = (b_bytes + (double)m * k * k_segments * e) / kReadPerUs;
     Plan best = {};
     best.us = 1e30;
+    // a loss's epilogues need a row's whole sums, and only the large tiles have them
+    const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
     if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED)) {
         best.few = true;
         best.splits = 1;
@@ -113,7 +104,7 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         if (t * (pl.fast ? 512 : 256) >= int64_t(1) << 32) return;
         // weights that one or two row tiles read come from memory at its latency, two steps in flight
         if (m <= 2 * bm) step = std::max(step, 0.9);
-        for (int s = 1, most = most_splits(t); s <= most; ++s) {
+        for (int s = 1, most = whole ? 1 : most_splits(t); s <= most; ++s) {
             const double us = std::max(rounds(t * s, slots) * ((steps + s - 1) / s * step + tile), read_us) + join_us(s) + pl.us + 1.5;
             if (us < best.us) {
                 best = pl;
@@ -125,12 +116,12 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     };
     // linear_any.hip: two workgroups per CU on 128 x 128 tiles, four on 64 x 64; fp32's matrix instructions take
     // sixteen times bf16's time for the same bytes
-    const double slow = type == ProductType::F32 ? 4.0 : type == ProductType::BF16 ? 1.0 : 1.2;
+    const double slow = type == ProductType::F32 ? 4.0 : element_bytes(type) == 2 ? 1.0 : 1.2;
     Plan any = {};
     any.tile = 128;
-    consider(any, tiles(128, 128), 128, 128, 2 * num_cu, 1.45 * slow, 2.0);
+    if (!whole) consider(any, tiles(128, 128), 128, 128, 2 * num_cu, 1.45 * slow, 2.0);
     any.tile = 64;
-    consider(any, tiles(64, 64), 64, 64, 4 * num_cu, 1.10 * slow, 1.5);
+    if (!whole) consider(any, tiles(64, 64), 64, 64, 4 * num_cu, 1.10 * slow, 1.5);
 
     const Extent x = extent_of(kind, m, n, k);
     const bool short_rows = (int64_t)std::max(x.a_cols, x.b_cols) * e < kMaxPitchBytes / 2 - 64;
@@ -169,8 +160,71 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     return best;
 }
 
-// Whether any kernel's grid holds the product.
-bool planned(const Plan& pl) { return pl.us < 1e30; }
+void describe(const Plan& pl, char* text, size_t size)
+{
+    constexpr const char* kFastNames[] = {"256x256", "256x192", "192x256", "256x128", "128x256", "128x128", "128x64", "64x128"};
+    static_assert(sizeof(kFastNames) / sizeof(*kFastNames) == (size_t)miconv::FastTile::COUNT, "one name a tile");
+    int at;
+    if (pl.few) at = snprintf(text, size, "few");
+    else if (pl.fast) at = snprintf(text, size, "fast %s", kFastNames[(int)pl.fast_tile]);
+    else at = snprintf(text, size, "any %dx%d", pl.tile, pl.tile);
+    if (pl.splits > 1) at += snprintf(text + at, size - at, " split %d", pl.splits);
+    if (pl.pack_a) at += snprintf(text + at, size - at, " pack a");
+    if (pl.pack_b) snprintf(text + at, size - at, " pack b");
+}
+
+static bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes) { return aligned_matrix(p, ld) && bytes % 16 == 0; }
+
+mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes, Sums* sums)
+{
+    if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
+    const int e = element_bytes(type);
+    const bool a_across = kind == Product::WEIGHT_GRAD, b_across = a_across || kind == Product::INPUT_GRAD;
+    if (p.a_K < p.K) p.a_K = p.K;
+    if (p.a_rows < p.M) p.a_rows = p.M;
+    if (p.b_rows < p.N) p.b_rows = p.N;
+    const bool two_b = kind == Product::GATED || p.k_segments > 1;
+    bool aligned_a = fast_rows(p.a, p.lda, (int64_t)(a_across ? p.a_rows : p.a_K) * e);
+    const int64_t b_bytes = (int64_t)(b_across ? p.b_rows : p.a_K) * e;
+    bool aligned_b = fast_rows(p.b, p.ldb, b_bytes);
+    if (two_b) aligned_b = aligned_b && fast_rows(p.b2, p.ldb2, b_bytes);
+    if (p.k_segments > 1) aligned_b = aligned_b && p.ldb == p.ldb2;
+    const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b);
+    if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
+    if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Extent x = extent_of(kind, p.M, p.N, p.K);
+    miconv::PackJob jobs[miconv::PACK_JOBS];
+    int packs = 0;
+    auto pack = [&](const uint8_t*& from, int64_t& ld, int64_t rows, int64_t bytes, int64_t pitch, size_t size) {
+        jobs[packs++] = {from, ld, rows, bytes, ws, pitch};
+        from = ws, ld = pitch;
+        ws += size;
+    };
+    if (pl.pack_a) {
+        pack(p.a, p.lda, x.a_rows, (int64_t)x.a_cols * e, pl.pack_a, pl.a_bytes);
+        if (a_across) p.a_rows = (int)(pl.pack_a / e);
+    }
+    if (pl.pack_b) {
+        pack(p.b, p.ldb, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
+        if (two_b) pack(p.b2, p.ldb2, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
+        if (b_across) p.b_rows = (int)(pl.pack_b / e);
+    }
+    if (packs) MIC_TRY(launched(miconv::launch_pack(jobs, packs, h->stream)));
+    p.splits = pl.splits;
+    p.part = reinterpret_cast<float*>(ws);
+    p.part_ld = pl.part_ld;
+    hipError_t err = pl.few    ? miconv::launch_product_few(kind, type, p, h->num_cu, h->stream)
+                     : pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
+                               : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
+    if (sums) *sums = pl.splits > 1 ? Sums{p.part, p.part_ld, pl.splits} : Sums{static_cast<const float*>(p.y), p.ldy, 1};
+    if (err == hipSuccess && pl.splits > 1 && !sums) err = miconv::launch_product_join(kind, type, p, h->stream);
+    return launched(err);
+}
+
+}  // namespace miconv
+
+namespace {
 
 // Workspace for any alignment of the operands.
 size_t product_bytes(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments)
@@ -202,78 +256,6 @@ Aligned aligned_operands(Product kind, ProductType type, int n, int k, bool alig
 size_t aligned_bytes(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, Aligned al)
 {
     return m && n ? plan_product(num_cu, kind, type, m, n, k, k_segments, al.a, al.b).bytes : 0;
-}
-
-// A matrix that counts as aligned (its rows' length is looked at where it matters).
-bool aligned_matrix(const void* p, int64_t ld_bytes) { return aligned(p, 16) && ld_bytes % 16 == 0 && ld_bytes < kMaxPitchBytes / 2; }
-bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes) { return aligned_matrix(p, ld) && bytes % 16 == 0; }
-
-void describe(const Plan& pl, char* text, size_t size)
-{
-    constexpr const char* kFastNames[] = {"256x256", "256x192", "192x256", "256x128", "128x256", "128x128", "128x64", "64x128"};
-    static_assert(sizeof(kFastNames) / sizeof(*kFastNames) == (size_t)miconv::FastTile::COUNT, "one name a tile");
-    int at;
-    if (pl.few) at = snprintf(text, size, "few");
-    else if (pl.fast) at = snprintf(text, size, "fast %s", kFastNames[(int)pl.fast_tile]);
-    else at = snprintf(text, size, "any %dx%d", pl.tile, pl.tile);
-    if (pl.splits > 1) at += snprintf(text + at, size - at, " split %d", pl.splits);
-    if (pl.pack_a) at += snprintf(text + at, size - at, " pack a");
-    if (pl.pack_b) snprintf(text + at, size - at, " pack b");
-}
-
-mic_status give_name(const char* text, char* buf, size_t buflen)
-{
-    const size_t len = strlen(text);
-    if (!buf || len + 1 > buflen) return MIC_STATUS_BAD_PARAM;
-    memcpy(buf, text, len + 1);
-    return MIC_STATUS_SUCCESS;
-}
-
-int cus_of(mic_handle h) { return h ? h->num_cu : kCuCounts[0]; }
-
-mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes)
-{
-    if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
-    const int e = element_bytes(type);
-    const bool a_across = kind == Product::WEIGHT_GRAD, b_across = a_across || kind == Product::INPUT_GRAD;
-    if (p.a_K < p.K) p.a_K = p.K;
-    if (p.a_rows < p.M) p.a_rows = p.M;
-    p.b_rows = p.N;
-    const bool two_b = kind == Product::GATED || p.k_segments > 1;
-    bool aligned_a = fast_rows(p.a, p.lda, (int64_t)(a_across ? p.a_rows : p.a_K) * e);
-    bool aligned_b = fast_rows(p.b, p.ldb, (int64_t)(b_across ? p.N : p.K) * e);
-    if (two_b) aligned_b = aligned_b && fast_rows(p.b2, p.ldb2, (int64_t)(b_across ? p.N : p.K) * e);
-    if (p.k_segments > 1) aligned_b = aligned_b && p.ldb == p.ldb2;
-    const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b);
-    if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
-    if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const Extent x = extent_of(kind, p.M, p.N, p.K);
-    miconv::PackJob jobs[miconv::PACK_JOBS];
-    int packs = 0;
-    auto pack = [&](const uint8_t*& from, int64_t& ld, int64_t rows, int64_t bytes, int64_t pitch, size_t size) {
-        jobs[packs++] = {from, ld, rows, bytes, ws, pitch};
-        from = ws, ld = pitch;
-        ws += size;
-    };
-    if (pl.pack_a) {
-        pack(p.a, p.lda, x.a_rows, (int64_t)x.a_cols * e, pl.pack_a, pl.a_bytes);
-        if (a_across) p.a_rows = (int)(pl.pack_a / e);
-    }
-    if (pl.pack_b) {
-        pack(p.b, p.ldb, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
-        if (two_b) pack(p.b2, p.ldb2, x.b_rows, (int64_t)x.b_cols * e, pl.pack_b, pl.b_bytes);
-        if (b_across) p.b_rows = (int)(pl.pack_b / e);
-    }
-    if (packs) MIC_TRY(launched(miconv::launch_pack(jobs, packs, h->stream)));
-    p.splits = pl.splits;
-    p.part = reinterpret_cast<float*>(ws);
-    p.part_ld = pl.part_ld;
-    hipError_t err = pl.few    ? miconv::launch_product_few(kind, type, p, h->num_cu, h->stream)
-                     : pl.fast ? miconv::launch_product_fast(kind, type, p, pl.fast_tile, h->stream)
-                               : miconv::launch_product_any(kind, type, p, pl.tile, h->stream);
-    if (err == hipSuccess && pl.splits > 1) err = miconv::launch_product_join(kind, type, p, h->stream);
-    return launched(err);
 }
 
 mic_status product_type(mic_dtype in, mic_dtype out, ProductType* type, bool fast = false)

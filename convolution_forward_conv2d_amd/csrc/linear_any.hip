@@ -160,6 +160,7 @@ template <class Mul> hipError_t launch_type(Product kind, const ProductArgs& p, 
     case Product::GATED: return launch_one<Mul, false, false, EPI_GATED>(p, tile, stream);
     case Product::INPUT_GRAD: return launch_one<Mul, false, true, EPI_PLAIN>(p, tile, stream);
     case Product::WEIGHT_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+    default: break;
     }
     return hipErrorInvalidValue;
 }
@@ -220,6 +221,9 @@ hipError_t launch_product_any(Product kind, ProductType type, const ProductArgs&
     case ProductType::E4M3_F32: return launch_e4m3<MulE4m3<float, false>>(kind, p, tile, stream);
     case ProductType::E4M3_BF16_SHORT: return launch_e4m3<MulE4m3<Bf16, true>>(kind, p, tile, stream);
     case ProductType::E4M3_F32_SHORT: return launch_e4m3<MulE4m3<float, true>>(kind, p, tile, stream);
+    case ProductType::BF16_F32:
+        if (kind != Product::FORWARD) return hipErrorInvalidValue;
+        return launch_one<MulBf16F32, false, false, EPI_LINEAR>(p, tile, stream);
     }
     return hipErrorInvalidValue;
 }
@@ -228,7 +232,8 @@ hipError_t launch_product_join(Product kind, ProductType type, const ProductArgs
 {
     const int64_t work = (int64_t)p.M * ((p.N + 7) / 8);
     const int blocks = (int)(work / 256 + 1 < 4096 ? work / 256 + 1 : 4096);
-    if (type == ProductType::F32 || type == ProductType::E4M3_F32 || type == ProductType::E4M3_F32_SHORT)
+    if (type == ProductType::F32 || type == ProductType::E4M3_F32 || type == ProductType::E4M3_F32_SHORT
+        || type == ProductType::BF16_F32)
         return join_type<float>(kind, p, blocks, stream);
     return join_type<Bf16>(kind, p, blocks, stream);
 }

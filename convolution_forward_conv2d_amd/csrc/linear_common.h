@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include "mfma_common.h"
+#include "kernels.h"
 
 namespace miconv {
 
@@ -226,9 +227,17 @@ struct ProductArgs {
     int splits;
     float* part;
     int64_t part_ld;
+    // EPI_PLAIN: one of several products that add up to y.  Their sum so far, fp32, rows of ld_sum; the first writes it,
+    // the last adds to it and writes y instead
+    float* sum;
+    int64_t ld_sum;
+    bool sum_first, sum_last;
+    // EPI_LOSS, EPI_LOGITS_GRAD (y: dz, whose columns up to y_columns are written, zeros past N)
+    LossArgs loss;
+    int y_columns;
 };
 
-enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2 };
+enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_LOSS = 3, EPI_LOGITS_GRAD = 4 };
 
 // A gated layer's raw columns come in blocks of 32, 16 of the gate's and the
 // same 16 of the other product's, so both meet in one workgroup (and one wave)
@@ -275,6 +284,40 @@ __device__ __forceinline__ float scaled(float v, Scale a, Scale b)
     return __builtin_ldexpf(v * (a.part * b.part), a.power + b.power);
 }
 
+// ------------------------------------------------------------------ cross entropy
+//
+// z the logits of a row, t its target, a the smoothing's share:
+//   lse = log sum_j e^z_j      loss = lse - (1 - a) z_t - a mean(z)
+//   dz_j = gain (e^(z_j - lse) - (1 - a) [j = t] - a / classes),  gain = dloss / count
+// A row without a target (loss.ignore) has neither loss nor gradient, whatever its logits; a target that is no class
+// makes both no number; a row of which a bias of -infinity leaves no class has no gradient.
+struct LossRow {
+    float lse, gain;
+    int at;                   // the target's column in this product, outside it if it is not there
+    bool counts;
+};
+__device__ __forceinline__ int loss_column(const LossArgs& p, int64_t target)
+{
+    return target >= 0 && target < p.classes ? (int)target - p.first : -1;
+}
+__device__ __forceinline__ LossRow loss_row(const LossArgs& p, int m)
+{
+    const int64_t target = p.target[m];
+    LossRow r;
+    r.lse = p.lse[m];
+    r.counts = target != p.ignore && r.lse != -__builtin_inff();
+    r.gain = p.dloss[p.dloss_rows ? m : 0];
+    if (p.count) r.gain = *p.count > 0.0f ? r.gain / *p.count : 0.0f;
+    if (target < 0 || target >= p.classes) r.gain = __builtin_nanf("");
+    r.at = loss_column(p, target);
+    return r;
+}
+template <bool EXACT> __device__ __forceinline__ float loss_gradient(const LossRow& r, float z, int n, float goal, float every)
+{
+    const float v = (exponential<EXACT>(z - r.lse) - (n == r.at ? goal : every)) * r.gain;
+    return r.counts ? v : 0.0f;
+}
+
 // Eight finished columns n..n+7 of row m: v the raw sums (u the second product's).
 template <class Out, int EPI>
 __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, float (&v)[8], float (&u)[8])
@@ -284,8 +327,24 @@ __device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, floa
         const bool second = m >= p.m_pitch;
         const int r = second ? m - p.m_pitch : m;
         if (r >= p.m_valid || n >= p.N) return;
+        if (p.sum) {
+            float* sum = p.sum + (int64_t)r * p.ld_sum + n;
+            if (!p.sum_first) {
+                load8(sum, p.N - n, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += u[i];
+            }
+            if (!p.sum_last) {
+                store8(sum, p.N - n, v);
+                return;
+            }
+        }
         Out* y = second ? static_cast<Out*>(p.y2) + (int64_t)r * p.ldy2 : static_cast<Out*>(p.y) + (int64_t)r * p.ldy;
         store8(y + n, p.N - n, v);
+        return;
+    }
+    if constexpr (EPI == EPI_LOGITS_GRAD) {
+        if (m < p.M && n < p.y_columns) store8(static_cast<Out*>(p.y) + (int64_t)m * p.ldy + n, 8, v);
         return;
     }
     if (m >= p.M || n >= p.N) return;
@@ -359,6 +418,11 @@ struct MulBf16 {
     }
     // one vector a lane, of row l % 16, for 16 x 16 (the lane groups and a vector's elements walk k in one order)
     __device__ static f32x4 mac16(u32x4 rows, u32x4 cols, f32x4 c) { return block(&rows, &cols, c); }
+};
+
+// The same with outputs in fp32.
+struct MulBf16F32 : MulBf16 {
+    using Out = float;
 };
 
 struct MulF32 {

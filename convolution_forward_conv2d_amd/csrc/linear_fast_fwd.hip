@@ -7,6 +7,8 @@ hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs
 {
     if (kind == Product::INPUT_GRAD || kind == Product::WEIGHT_GRAD)
         return launch_product_fast_grad(kind, type, p, tile, stream);
+    if (kind == Product::LOSS || kind == Product::LOGITS_GRAD || type == ProductType::BF16_F32)
+        return launch_product_fast_loss(kind, type, p, tile, stream);
     const bool gated = kind == Product::GATED;
     switch (type) {
     case ProductType::BF16:
@@ -27,6 +29,7 @@ hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs
     case ProductType::E4M3_F32_SHORT:
         return gated ? launch_one<MulE4m3<float, true>, false, false, EPI_GATED>(p, tile, stream)
                      : launch_one<MulE4m3<float, true>, false, false, EPI_LINEAR>(p, tile, stream);
+    default: break;
     }
     return hipErrorInvalidValue;
 }

@@ -302,6 +302,9 @@ hipError_t launch_product_few(Product kind, ProductType type, const ProductArgs&
     case ProductType::E4M3_BF16_SHORT: return launch_kind<MulE4m3<Bf16, false>>(kind, p, num_cu, stream);
     case ProductType::E4M3_F32:
     case ProductType::E4M3_F32_SHORT: return launch_kind<MulE4m3<float, false>>(kind, p, num_cu, stream);
+    case ProductType::BF16_F32:
+        if (kind != Product::FORWARD) return hipErrorInvalidValue;
+        return launch_rows<MulBf16F32, EPI_LINEAR>(p, num_cu, stream);
     }
     return hipErrorInvalidValue;
 }

@@ -201,7 +201,7 @@ __device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, 
     static_assert(ROWS % 32 == 0, "32 rows at a time");
     // a linear or gated layer's whole tile takes its bias and scales once, and its residual 32 rows ahead
     using Rows = WholeRows<Out, EPI, W>;
-    bool whole = EPI != EPI_PLAIN && p.splits == 1 && (EPI == EPI_GATED ? (j0 + W) / 2 : j0 + W) <= p.N;
+    bool whole = (EPI == EPI_LINEAR || EPI == EPI_GATED) && p.splits == 1 && (EPI == EPI_GATED ? (j0 + W) / 2 : j0 + W) <= p.N;
     const Rows rows(lane, EPI == EPI_GATED ? j0 / 2 : j0);
     typename Rows::Columns columns;
     u32x4 residual[2][Rows::PASSES][sizeof(Out) / 2];

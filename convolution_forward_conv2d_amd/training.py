@@ -10,12 +10,19 @@ import collections
 
 import torch
 
+import convolution_forward_conv2d_amd as mic
 from . import feed_forward as ff
-from .feed_forward import E4M3, _CODE, _call, _empty, _flag, _gpu, _handle, _matrix, _ptr, _rows, _vector, _workspace
+from .feed_forward import (E4M3, _CODE, _call, _empty, _even, _flag, _gpu, _handle, _matrix, _ptr, _rows, _vector, _weights,
+                           _workspace)
 
 LayerNorm = collections.namedtuple("LayerNorm", ["y", "sum", "mean", "rstd", "scale"])
 LayerNorm.__doc__ = """layer_norm's results: y; sum = x + residual (x itself without a residual), mean and rstd, fp32 per
 row, which layer_norm_backward takes; scale, fp32 per row, where y is e4m3 (else None)."""
+
+LinearCrossEntropy = collections.namedtuple("LinearCrossEntropy", ["loss", "lse", "count"])
+LinearCrossEntropy.__doc__ = """linear_cross_entropy's results: loss, fp32; lse, the logarithm of each row's sum of
+exponentials, fp32 per row, and count, the number of rows that have a target (None without a reduction), which
+linear_cross_entropy_backward takes."""
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
@@ -168,3 +175,110 @@ def dropout(x, p, seed, offset=0, residual=None):
 def dropout_backward(dy, p, seed, offset=0):
     """dx of dropout with the same p, seed and offset."""
     return _drop(dy, p, seed, offset, None, "dy")
+
+
+# ---------------------------------------------------------------- loss
+
+def _targets(target, shape, device):
+    if target.dtype is not torch.int64:
+        raise TypeError("target must be %s, got %s" % (torch.int64, target.dtype))
+    if target.device != device:
+        raise ValueError("target is on %s, not on %s" % (target.device, device))
+    if target.shape != shape:
+        raise ValueError("target has shape %s, expected %s" % (tuple(target.shape), tuple(shape)))
+    if not target.is_contiguous():
+        raise ValueError("target must be contiguous")
+    return target.data_ptr()
+
+
+def _smoothing(label_smoothing):
+    if isinstance(label_smoothing, torch.Tensor) or not 0 <= label_smoothing < 1:
+        raise ValueError("label_smoothing must be a number from 0 and below 1, got %s" % (label_smoothing,))
+    return float(label_smoothing)
+
+
+def _ignored(ignore_index):
+    if isinstance(ignore_index, bool) or not isinstance(ignore_index, int):
+        raise TypeError("ignore_index must be a whole number, got %s" % type(ignore_index).__name__)
+    if not -1 << 63 <= ignore_index < 1 << 63:
+        raise ValueError("ignore_index does not fit int64")
+    return ignore_index
+
+
+def linear_cross_entropy(x, w, target, bias=None, reduction="mean", ignore_index=-100, label_smoothing=0.0):
+    """The cross entropy of softmax(x w^T + bias) and one class per row, without keeping the logits.
+
+    x (..., k), w (classes, k), bias (classes): fp32 or bf16, one type; target
+    (...): int64.  With z the logits, a = label_smoothing:
+        loss = log sum e^z - (1 - a) z[target] - a mean(z)
+    per row (reduction "none"), its "sum" or its "mean" over the rows whose
+    target is not ignore_index (0 over no rows).  A target that is neither
+    that nor a class makes its loss NaN.
+    Returns LinearCrossEntropy(loss, lse, count).
+    """
+    mode = mic.REDUCTIONS.get(reduction)
+    if mode is not None:
+        r = _native().linear_cross_entropy(x, w, target, bias, mode, ignore_index, label_smoothing)
+        if r is not None:
+            return LinearCrossEntropy(*r)
+    _gpu(x, "x", _FLOATS)
+    if mode is None:
+        raise ValueError("unknown reduction %r (one of %s)" % (reduction, ", ".join(mic.REDUCTIONS)))
+    dtype, device = x.dtype, x.device
+    k = x.shape[-1] if x.dim() else 0
+    m, ldx = _rows(x, k, "x")
+    ldw = _weights(w, k, dtype, device, "w")
+    n = w.shape[0]
+    if n < 1:
+        raise ValueError("w must have at least one class")
+    bp = 0 if bias is None else _vector(bias, n, dtype, device, "bias")
+    tp = _targets(target, x.shape[:-1], device)
+    smoothing, ignore_index = _smoothing(label_smoothing), _ignored(ignore_index)
+    h = _handle(device)
+    lse = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    loss = torch.empty_like(lse) if mode == 0 else x.new_empty((), dtype=torch.float32)
+    count = None if mode == 0 else torch.empty_like(loss)
+    fn = "mic_linear_cross_entropy_workspace" + ("_aligned" if _even((x, ldx), (w, ldw)) else "")
+    wk, wkp, wkn = _workspace(fn, h, x, _CODE[dtype], m, n, k)
+    _call("mic_linear_cross_entropy", h, _CODE[dtype], mode, m, n, k, x.data_ptr(), ldx, w.data_ptr(), ldw, bp, tp,
+          ignore_index, smoothing, loss.data_ptr(), lse.data_ptr(), _ptr(count), wkp, wkn)
+    return LinearCrossEntropy(loss, lse, count)
+
+
+def linear_cross_entropy_backward(dloss, x, w, target, lse, bias=None, count=None, ignore_index=-100, label_smoothing=0.0,
+                                  need_dx=True, need_dw=True, need_dbias=True):
+    """(dx, dw, dbias) of linear_cross_entropy, from its inputs and its lse and, of a mean, its count.
+
+    dloss: the gradient of the loss, fp32, a single value or (reduction
+    "none") one per row.  dbias is None without a bias; dx, dw and dbias are
+    where need_dx, need_dw and need_dbias are false: what is None is not
+    computed.
+    """
+    r = _native().linear_cross_entropy_backward(dloss, x, w, target, lse, bias, count, ignore_index, label_smoothing,
+                                                need_dx, need_dw, need_dbias)
+    if r is not None:
+        return r
+    need_dx, need_dw, need_dbias = _flag(need_dx, "need_dx"), _flag(need_dw, "need_dw"), _flag(need_dbias, "need_dbias")
+    _gpu(x, "x", _FLOATS)
+    dtype, device = x.dtype, x.device
+    k = x.shape[-1] if x.dim() else 0
+    m, ldx = _rows(x, k, "x")
+    ldw = _weights(w, k, dtype, device, "w")
+    n = w.shape[0]
+    if n < 1:
+        raise ValueError("w must have at least one class")
+    bp = 0 if bias is None else _vector(bias, n, dtype, device, "bias")
+    tp, lp = _targets(target, x.shape[:-1], device), _per_row(lse, m, device, "lse")
+    each = dloss.shape == x.shape[:-1] and dloss.dim() > 0
+    dp = _per_row(dloss, m if each else 1, device, "dloss")
+    cp = 0 if count is None else _per_row(count, 1, device, "count")
+    smoothing, ignore_index = _smoothing(label_smoothing), _ignored(ignore_index)
+    h = _handle(device)
+    dx = _empty(x.shape, x, dtype) if need_dx else None
+    dw = _empty(w.shape, w, dtype) if need_dw else None
+    dbias = torch.empty_like(bias) if need_dbias and bias is not None else None
+    fn = "mic_linear_cross_entropy_backward_workspace" + ("_aligned" if _even((x, ldx), (w, ldw)) else "")
+    wk, wkp, wkn = _workspace(fn, h, x, _CODE[dtype], m, n, k)
+    _call("mic_linear_cross_entropy_backward", h, _CODE[dtype], m, n, k, dp, each, x.data_ptr(), ldx, w.data_ptr(), ldw, bp, tp,
+          ignore_index, smoothing, lp, cp, _ptr(dx), k, _ptr(dw), k, _ptr(dbias), wkp, wkn)
+    return dx, dw, dbias

@@ -547,6 +547,58 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
                                      int64_t lddg, void* dw_up, int64_t lddu, void* workspace,
                                      size_t workspace_bytes);
 
+/* A classifier's head and its loss: with z[m,j] = sum_k x[m,k] w[j,k] + bias[j],
+ * j < n classes, t = target[m] and a = label_smoothing (0 <= a < 1)
+ *
+ *   lse[m] = log sum_j e^z[m,j]
+ *   l[m] = lse[m] - (1 - a) z[m,t] - a mean_j z[m,j],  0 where t is ignore_index
+ *
+ * loss receives l (MIC_REDUCTION_NONE: m values), its sum, or its mean over the
+ * rows whose target is not ignore_index, whose number count receives (fp32; for
+ * the last two; a mean over no rows is 0).  lse: m values.  All fp32.
+ *
+ * x and w F32 or BF16, bias (may be null) of their type; the logits are summed
+ * in fp32 and never rounded.  They are not kept: large products reduce each row
+ * of a tile where it is computed, others pass at most 256 MB of them at a time
+ * through the workspace.  A bias of -infinity takes a class out (of a row whose
+ * target it is the loss is infinite, with smoothing every row's).  A target that
+ * is neither a class nor ignore_index makes its row's loss NaN; it reads nothing
+ * out of bounds. */
+typedef enum {
+    MIC_REDUCTION_NONE = 0,
+    MIC_REDUCTION_SUM = 1,
+    MIC_REDUCTION_MEAN = 2
+} mic_reduction;
+
+mic_status mic_linear_cross_entropy_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_linear_cross_entropy_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_reduction reduction, int m, int n, int k,
+                                    const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                    const int64_t* target, int64_t ignore_index, double label_smoothing, float* loss,
+                                    float* lse, float* count, void* workspace, size_t workspace_bytes);
+
+/* With g[m] = dloss[m] (dloss_rows not 0), or dloss[0] for every row, divided by
+ * count[0] where count is not null (a mean's; 0 if that is 0), and 0 where the
+ * target is ignore_index:
+ *
+ *   dz[m,j] = g[m] (e^(z[m,j] - lse[m]) - (1 - a) [j = t] - a / n)
+ *   dx[m,k] = sum_j dz[m,j] w[j,k]    dw[j,k] = sum_m dz[m,j] x[m,k]    dbias[j] = sum_m dz[m,j]
+ *
+ * dx, dw and dbias may each be null.  z is computed again and dz enters the
+ * products in the tensors' type, at most 512 MB of it (or 1024 classes) at a
+ * time; dx's sums over several such pieces are fp32.  A row whose target is
+ * ignore_index, or all of whose classes a bias takes out, has dz = 0 whatever
+ * its logits; x still enters dw's product, so its values there must be finite. */
+mic_status mic_linear_cross_entropy_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
+mic_status mic_linear_cross_entropy_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k,
+                                                               size_t* bytes);
+mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype, int m, int n, int k, const float* dloss,
+                                             int dloss_rows, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                             const void* bias, const int64_t* target, int64_t ignore_index,
+                                             double label_smoothing, const float* lse, const float* count, void* dx,
+                                             int64_t lddx, void* dw, int64_t lddw, void* dbias, void* workspace,
+                                             size_t workspace_bytes);
+
 /* How a call runs its products, host only, NUL-terminated into buf of buflen
  * bytes (MIC_STATUS_BAD_PARAM if it does not fit; 128 do): "few" rows, large
  * tiles ("fast 256x192") or small ones through registers ("any 64x64"), in how
@@ -562,6 +614,14 @@ mic_status mic_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, m
                                            int aligned, char* buf, size_t buflen);
 mic_status mic_gated_linear_backward_kernel_name(mic_handle handle, mic_dtype dtype, int m, int n, int k, int aligned,
                                                  char* buf, size_t buflen);
+
+/* The same for the logits of a cross entropy: "fused ..." where they stay in
+ * the tiles that compute them, "copies" where unaligned rows are copied first,
+ * and in how many pieces of the classes. */
+mic_status mic_linear_cross_entropy_kernel_name(mic_handle handle, mic_dtype dtype, int m, int n, int k, int aligned, char* buf,
+                                                size_t buflen);
+mic_status mic_linear_cross_entropy_backward_kernel_name(mic_handle handle, mic_dtype dtype, int m, int n, int k, int aligned,
+                                                         char* buf, size_t buflen);
 
 #ifdef __cplusplus
 }

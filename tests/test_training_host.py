@@ -1,4 +1,4 @@
-"""Layer norm and dropout without a GPU: refusals, workspaces, and the tests' own formulas against differences."""
+"""Layer norm, dropout and cross entropy without a GPU: refusals, workspaces, and the tests' own formulas against differences."""
 import pytest
 import torch
 
@@ -67,11 +67,12 @@ def test_workspaces():
 def test_tensor_functions_refuse_before_the_gpu():
     x, w = torch.zeros(4, 8), torch.zeros(8)
     for f, args in ((mic.layer_norm, (x, w)), (mic.layer_norm_backward, (x, x, w, x[:, 0], x[:, 0])), (mic.dropout, (x, 0.5, 1)),
-                    (mic.dropout_backward, (x, 0.5, 1))):
+                    (mic.dropout_backward, (x, 0.5, 1)), (mic.linear_cross_entropy, (x, x, x[:, 0].long())),
+                    (mic.linear_cross_entropy_backward, (x[0, 0], x, x, x[:, 0].long(), x[:, 0]))):
         with pytest.raises(ValueError, match="GPU"):
             f(*args)
         with pytest.raises(TypeError):
-            f(*(a.double() if torch.is_tensor(a) else a for a in args))
+            f(*(a.double() if torch.is_tensor(a) and a.is_floating_point() else a for a in args))
 
 
 def test_generator():
@@ -111,3 +112,84 @@ def test_norm_formula_against_differences():
     assert abs(float((dx * v).sum() - differences(lambda t: value(t, w, b), s, v))) < 1e-6
     assert abs(float((dw * vw).sum() - differences(lambda t: value(s, t, b), w, vw))) < 1e-6
     assert abs(float((db * vw).sum() - differences(lambda t: value(s, w, t), b, vw))) < 1e-6
+
+
+LOSS = "h dtype red m n k x ldx w ldw bias target ignore smooth loss lse count work bytes".split()
+LOSS_OK = dict(h=None, dtype=BF16, red=2, m=4, n=8, k=16, x=P, ldx=16, w=P, ldw=16, bias=0, target=P, ignore=-100, smooth=0.0,
+               loss=P, lse=P, count=P, work=P, bytes=BIG)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(h=0), BAD), (dict(m=-1), BAD), (dict(n=-1), BAD), (dict(n=0), BAD), (dict(k=-1), BAD), (dict(x=0), BAD), (dict(w=0), BAD),
+    (dict(ldx=15), BAD), (dict(ldw=15), BAD), (dict(x=P + 1), BAD), (dict(bias=P + 1), BAD), (dict(target=0), BAD),
+    (dict(target=P + 4), BAD), (dict(loss=0), BAD), (dict(loss=P + 2), BAD), (dict(lse=0), BAD), (dict(lse=P + 2), BAD),
+    (dict(count=0), BAD), (dict(count=P + 2), BAD), (dict(smooth=1.0), BAD), (dict(smooth=-0.5), BAD),
+    (dict(smooth=float("nan")), BAD), (dict(work=0), BAD), (dict(work=P + 8), BAD), (dict(bytes=16), BAD),
+    (dict(red=3), UNSUPPORTED), (dict(red=-1), UNSUPPORTED), (dict(dtype=E4M3), UNSUPPORTED), (dict(dtype=F64), UNSUPPORTED),
+    (dict(m=1 << 30), UNSUPPORTED), (dict(n=1 << 30), UNSUPPORTED), (dict(ldx=1 << 22), UNSUPPORTED)])
+def test_loss_refusals(change, want):
+    assert call("mic_linear_cross_entropy", LOSS, dict(LOSS_OK, h=handle()), **change) == want
+
+
+LGRAD = "h dtype m n k dloss rows x ldx w ldw bias target ignore smooth lse count dx lddx dw lddw db work bytes".split()
+LGRAD_OK = dict(h=None, dtype=F32, m=4, n=8, k=16, dloss=P, rows=0, x=P, ldx=16, w=P, ldw=16, bias=0, target=P, ignore=-100,
+                smooth=0.0, lse=P, count=0, dx=P, lddx=16, dw=P, lddw=16, db=P, work=P, bytes=BIG)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(h=0), BAD), (dict(m=-1), BAD), (dict(n=0), BAD), (dict(dloss=0), BAD), (dict(dloss=P + 2), BAD), (dict(x=0), BAD),
+    (dict(w=0), BAD), (dict(ldx=15), BAD), (dict(ldw=15), BAD), (dict(lddx=15), BAD), (dict(lddw=15), BAD), (dict(dx=P + 2), BAD),
+    (dict(dw=P + 2), BAD), (dict(db=P + 2), BAD), (dict(bias=P + 2), BAD), (dict(target=0), BAD), (dict(target=P + 4), BAD),
+    (dict(lse=0), BAD), (dict(count=P + 2), BAD), (dict(smooth=1.5), BAD), (dict(work=0), BAD), (dict(bytes=16), BAD),
+    (dict(dtype=E4M3), UNSUPPORTED), (dict(k=1 << 30), UNSUPPORTED), (dict(lddw=1 << 21), UNSUPPORTED)])
+def test_loss_backward_refusals(change, want):
+    assert call("mic_linear_cross_entropy_backward", LGRAD, dict(LGRAD_OK, h=handle()), **change) == want
+
+
+def test_loss_with_nothing_to_do():
+    assert call("mic_linear_cross_entropy", LOSS, dict(LOSS_OK, h=handle()), red=0, m=0, x=0, w=0, loss=0) == 0
+    assert call("mic_linear_cross_entropy_backward", LGRAD, dict(LGRAD_OK, h=handle()), dx=0, dw=0, db=0, work=0) == 0
+    assert call("mic_linear_cross_entropy_backward", LGRAD, dict(LGRAD_OK, h=handle()), m=0, n=0, work=0) == 0
+
+
+def test_loss_workspaces():
+    """The logits of 8192 x 131072 would be 4 GB in fp32; no call holds that much."""
+    sizes = [(1, 1, 1), (7, 33, 65), (128, 1000, 4096), (4096, 50021, 4096), (8192, 131072, 4096), (0, 5, 5), (5, 5, 0)]
+    fs = ((mic.mic_linear_cross_entropy_workspace, mic.mic_linear_cross_entropy_workspace_aligned),
+          (mic.mic_linear_cross_entropy_backward_workspace, mic.mic_linear_cross_entropy_backward_workspace_aligned))
+    for any_rows, aligned in fs:
+        for dtype in (F32, BF16):
+            for m, n, k in sizes:
+                size = 4 if dtype == F32 else 2
+                most = (1 << 30) + size * (m + min(n, 1 << 19)) * (k + 16) + 4 * m * (k + 8)
+                assert 0 <= aligned(None, dtype, m, n, k) <= any_rows(None, dtype, m, n, k) <= 2 * most
+                assert aligned(handle(), dtype, m, n, k) <= aligned(None, dtype, m, n, k)
+    assert mic.mic_linear_cross_entropy_workspace_aligned(None, BF16, 8192, 131072, 4096) < 8192 * 131072
+    for f in fs[0] + fs[1]:
+        with pytest.raises(mic.MicError) as e:
+            f(None, E4M3, 4, 4, 4)
+        assert e.value.status == UNSUPPORTED
+
+
+def test_loss_formula_against_differences():
+    g = torch.Generator().manual_seed(6)
+    m, n, k, a = 5, 11, 7, 0.2
+    x, w, b = torch.randn(m, k, generator=g).double(), torch.randn(n, k, generator=g).double(), torch.randn(n, generator=g).double()
+    vx, vw, vb = (torch.randn(t.shape, generator=g).double() for t in (x, w, b))
+    target = torch.tensor([0, 10, -100, 3, 3])
+    T.HALF[torch.float64] = 0.0
+    try:
+        for reduction in ("mean", "sum", "none"):
+            weight = torch.randn(m, generator=g) if reduction == "none" else torch.ones(())
+
+            def value(x, w, b):
+                return (T.cross_entropy(x, w, b, target, reduction, a=a)["loss"][0] * weight.double()).sum()
+
+            lse = torch.logsumexp(x @ w.t() + b, 1)
+            count = torch.tensor(4.0) if reduction == "mean" else None
+            (dx, _), (dw, _), (db, _) = T.cross_entropy_backward(weight, x, w, b, target, lse, count, a=a)
+            assert abs(float((dx * vx).sum() - differences(lambda t: value(t, w, b), x, vx))) < 1e-6
+            assert abs(float((dw * vw).sum() - differences(lambda t: value(x, t, b), w, vw))) < 1e-6
+            assert abs(float((db * vb).sum() - differences(lambda t: value(x, w, t), b, vb))) < 1e-6
+    finally:
+        del T.HALF[torch.float64]

@@ -90,3 +90,93 @@ def dropout(x, p, seed, offset, residual):
         y = y + d(residual)
         e = e + U * y.abs()
     return (y, e + HALF[x.dtype] * y.abs()), kept
+
+
+# ---------------------------------------------------------------- cross entropy
+#
+# On the device of the tensors.  The exponential is within 2^-21 (1 + its
+# argument's size) of itself (bf16: the argument's rounding), the sums of a row
+# are joined in trees: a lane's terms, lanes, 32 lanes of runs, at most DEPTH +
+# classes / 1000 additions one after the other.
+
+DEPTH = 96
+EXP = 2.0 ** -21
+
+
+def logits(x, w, bias):
+    """(z, bound)"""
+    x, w = x.double(), w.double()
+    z = x @ w.t()
+    e = (x.shape[1] + 8) * U * (x.abs() @ w.abs().t())
+    if bias is not None:
+        z = z + bias.double()
+        e = e + U * torch.where(z.isfinite(), z.abs() + bias.double().abs(), torch.zeros_like(z))
+    return z, e
+
+
+def cross_entropy(x, w, bias, target, reduction, ignore=-100, a=0.0):
+    """dict of (value, bound): loss, lse"""
+    z, ez = logits(x, w, bias)
+    n = z.shape[1]
+    top = z.amax(1, keepdim=True)
+    p = torch.softmax(z, 1)
+    lse = torch.logsumexp(z, 1)
+    below = torch.where(p > 0, top - z, torch.zeros_like(z))
+    e_log = (p * ez).sum(1) + (DEPTH + n / 1000) * U + EXP * (1 + (p * below).sum(1))
+    e_lse = e_log + 4 * U * (lse.abs() + top[:, 0].abs())
+    counts = target != ignore
+    at = torch.where(counts, target, torch.zeros_like(target))[:, None]
+    zt, et = z.gather(1, at)[:, 0], ez.gather(1, at)[:, 0]
+    each = lse - (1 - a) * zt
+    e = e_log + et + 4 * U * ((lse - top[:, 0]).abs() + (top[:, 0] - zt).abs())
+    if a:
+        each = each - a * z.mean(1)
+        e = e + a * (ez.mean(1) + (DEPTH + n / 1000) * U * z.abs().mean(1)) + 4 * U * (top[:, 0].abs() + z.abs().mean(1))
+    each, e = torch.where(counts, each, torch.zeros_like(each)), torch.where(counts, e, torch.zeros_like(e))
+    e = e + U * each.abs() + 1e-38
+    if reduction != "none":
+        m = each.numel()
+        total, e_total = each.sum(), e.sum() + (m / 1024 + 32) * U * each.abs().sum()
+        many = float(counts.sum()) if reduction == "mean" else 1.0
+        each, e = total / many, e_total / many + 2 * U * total.abs() / many
+    return {"loss": (each, e), "lse": (lse, e_lse + 1e-38)}
+
+
+def cross_entropy_backward(dloss, x, w, bias, target, lse, count, ignore=-100, a=0.0):
+    """((dx, bound), (dw, bound), (dbias, bound))"""
+    t = x.dtype
+    z, ez = logits(x, w, bias)
+    n = z.shape[1]
+    counts = target != ignore
+    g = torch.where(counts, dloss.double().reshape(-1), torch.zeros((), dtype=torch.float64, device=z.device))[:, None]
+    if count is not None:
+        g = g / count.double()
+    away = z - lse.double()[:, None]
+    p = away.exp()
+    goal = torch.full_like(z, a / n)
+    goal.scatter_add_(1, torch.where(counts, target, torch.zeros_like(target))[:, None], torch.full_like(z[:, :1], 1 - a))
+    far = torch.where(p > 0, away.abs(), torch.zeros_like(away))
+    dz = (p - goal) * g
+    edz = g.abs() * (p * (ez * 1.01 + U * far + EXP * (1 + far)) + 4 * U * (p + goal)) + 3 * U * dz.abs()
+    # an exponential below fp32's least normal number, 2^-126 = 1.18e-38, is 0, and so is a product with one: e^z of -88
+    # to -103 would still be a subnormal, so that dz may miss up to 2^-126 (|g| + 1), whatever its own size
+    edz = edz + HALF[t] * (dz.abs() + edz) + 2.0 ** -126 * (g.abs() + 1)
+
+    def product(a, ea, b):
+        y = a @ b
+        return y, (a.shape[1] + 8) * U * ((a.abs() + ea) @ b.abs()) + ea @ b.abs() + HALF[t] * y.abs() + 1e-38
+
+    db = dz.sum(0)
+    edb = (dz.shape[0] + 8) * U * dz.abs().sum(0) + edz.sum(0) + HALF[t] * db.abs() + 1e-38
+    return product(dz, edz, w.double()), product(dz.t(), edz.t(), x.double()), (db, edb)
+
+
+def check(got, want, what=""):
+    value, bound = want
+    got = got.double().reshape(value.shape)
+    assert torch.isfinite(got).all(), "%s: not finite" % what
+    over = (got - value).abs() - bound
+    if over.numel():
+        i = int(over.argmax())
+        assert float(over.max()) <= 0, "%s: %.9g, expected %.9g +- %.3g (element %d of %s)" % (
+            what, float(got.reshape(-1)[i]), float(value.reshape(-1)[i]), float(bound.reshape(-1)[i]), i, tuple(value.shape))
