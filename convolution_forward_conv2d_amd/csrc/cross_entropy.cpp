@@ -10,7 +10,10 @@ namespace {
 
 using namespace miconv;
 
-constexpr int kRun = 4096;                                     // columns of a run of logits in memory
+// Columns of a run of logits in memory: 1024, four a thread, where a row is long and rows are few; a row of 4096 is one
+// run, finished where it is read.
+constexpr int kRun = 1024, kWholeRow = 4096;
+int run_of(int n) { return n <= kWholeRow ? kWholeRow : kRun; }
 // What is held of the logits at one time: fp32 where they pass through memory, dz in the tensors' type.  A piece is a
 // product's columns: at 4096 rows of 4096 features 16384 of them keep every tile busy 8 rounds long.
 constexpr int64_t kLogitsBytes = int64_t(1) << 28, kGradientBytes = int64_t(1) << 29;
@@ -94,7 +97,7 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
         w.copy_bytes = w.copies.x + w.copies.w;
     } else {
         w.runs = 0;
-        for (int v = 0; v < n; v += w.piece) w.runs += (std::min(w.piece, n - v) + kRun - 1) / kRun;
+        for (int v = 0; v < n; v += w.piece) w.runs += (std::min(w.piece, n - v) + run_of(n) - 1) / run_of(n);
         w.ld_logits = align_up(w.piece, 4);
         w.logits = (size_t)align_up((int64_t)m * w.ld_logits * 4, 256);
         w.product = over_pieces(n, w.piece, [&](int columns) {
@@ -286,12 +289,13 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
         r.rows = m, r.cols = columns;
         r.z = sums.data, r.ld = sums.ld, r.splits = sums.splits;
         r.bias = piece_bias;
-        r.run = kRun;
+        r.run = run_of(n);
+        if (way.runs == 1) r.lse = lse, r.row_loss = row_loss;
         MIC_TRY(launched(launch_loss_rows(device_type(dtype), r, handle->stream)));
-        run += (columns + kRun - 1) / kRun;
+        run += (columns + r.run - 1) / r.run;
     }
     a.first = 0;
-    MIC_TRY(launched(launch_loss_join(a, m, way.runs, lse, row_loss, handle->stream)));
+    if (way.fused || way.runs > 1) MIC_TRY(launched(launch_loss_join(a, m, way.runs, lse, row_loss, handle->stream)));
     if (each) return MIC_STATUS_SUCCESS;
     return launched(launch_loss_reduce(a, m, row_loss, reduction == MIC_REDUCTION_MEAN, loss, count, handle->stream));
 }

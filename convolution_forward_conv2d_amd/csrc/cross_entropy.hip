@@ -26,34 +26,53 @@ __device__ __forceinline__ void join_runs(float& most, float& sum, float most2, 
 
 constexpr int THREADS = 256;
 
-template <class T> __device__ __forceinline__ float logit(const LossRowsArgs& p, int64_t row, int c)
+__device__ __forceinline__ void finish_row(const LossArgs& p, int64_t row, float most, float sum, float total, float* lse, float* loss)
 {
-    const float* z = p.z + row * p.ld + c;
-    float v = z[0];
-    for (int s = 1; s < p.splits; ++s) v += z[s * p.rows * p.ld];
-    return p.bias ? v + to_f32(static_cast<const T*>(p.bias)[c]) : v;
+    const int64_t target = p.target[row];
+    const float log_sum = logf(sum);
+    lse[row] = most + log_sum;
+    float v = 0.0f;
+    if (target != p.ignore) {
+        if (loss_column(p, target) < 0) {
+            v = __builtin_nanf("");
+        } else if (most == -__builtin_inff() && sum == 0.0f) {
+            v = __builtin_inff();                              // no class left: the target's share is nothing
+        } else {
+            v = log_sum + (1.0f - p.smooth) * (most - p.hit[row]);
+            if (p.smooth > 0.0f) v += p.smooth * (most - total / (float)p.classes);
+        }
+    }
+    loss[row] = v;
 }
 
-// A workgroup per row and run of its columns.
+// A workgroup per row and run of its columns, four columns a thread at a time; rows of one run are finished here.
 template <class T> __global__ __launch_bounds__(THREADS) void loss_rows_kernel(const LossRowsArgs p)
 {
     __shared__ float part[THREADS / 64][3];
     const int runs = (p.cols + p.run - 1) / p.run;
+    const int64_t hop = p.rows * p.ld;
     for (int64_t item = blockIdx.x; item < (int64_t)p.rows * runs; item += gridDim.x) {
         const int64_t row = item / runs;
         const int run = (int)(item - row * runs), first = run * p.run, last = min(first + p.run, p.cols);
         const int at = loss_column(p.loss, p.loss.target[row]);
         float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
-        for (int c = first + threadIdx.x; c < last; c += 4 * THREADS) {
-            float z[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) z[u] = c + u * THREADS < last ? logit<T>(p, row, c + u * THREADS) : -__builtin_inff();
+        for (int c = first + 4 * threadIdx.x; c < last; c += 4 * THREADS) {
+            // rows start at multiples of four, so four columns from c on are there whether they exist or not
+            const float* at_c = p.z + row * p.ld + c;
+            f32x4 z = *reinterpret_cast<const f32x4*>(at_c);
+#pragma unroll 8                                               // loads of eight parts in flight together
+            for (int s = 1; s < p.splits; ++s) z += *reinterpret_cast<const f32x4*>(at_c + s * hop);
             float top = most;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
+                if (c + u < last) {
+                    if (p.bias) z[u] += to_f32(static_cast<const T*>(p.bias)[c + u]);
+                    total += z[u];
+                    if (c + u == at) p.loss.hit[row] = z[u];
+                } else {
+                    z[u] = -__builtin_inff();
+                }
                 top = fmaxf(top, z[u]);
-                if (c + u * THREADS < last) total += z[u];
-                if (c + u * THREADS == at) p.loss.hit[row] = z[u];
             }
             const float from = top == -__builtin_inff() ? 0.0f : top;
             sum *= exponential<true>(most - from);             // nothing before: 0 e^-infinity
@@ -68,16 +87,20 @@ template <class T> __global__ __launch_bounds__(THREADS) void loss_rows_kernel(c
         }
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) part[wave][0] = most, part[wave][1] = sum, part[wave][2] = total;
-        __syncthreads();
+        __syncthreads();                                       // hit[row] is another thread's, too
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int w = 1; w < THREADS / 64; ++w) {
                 join_runs(most, sum, part[w][0], part[w][1]);
                 total += part[w][2];
             }
-            const int64_t to = (int64_t)(p.loss.part_first + run) * p.rows + row;
-            reinterpret_cast<float2*>(p.loss.part)[to] = float2{most, sum};
-            if (p.loss.part_z) p.loss.part_z[to] = total;
+            if (p.lse) {
+                finish_row(p.loss, row, most, sum, total, p.lse, p.row_loss);
+            } else {
+                const int64_t to = (int64_t)(p.loss.part_first + run) * p.rows + row;
+                reinterpret_cast<float2*>(p.loss.part)[to] = float2{most, sum};
+                if (p.loss.part_z) p.loss.part_z[to] = total;
+            }
         }
         __syncthreads();
     }
@@ -100,6 +123,7 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
             const float* z = p.z + (int64_t)r * p.ld + c;
             float v[8];
             load8(z, nv, v);
+#pragma unroll 4                                               // loads of four parts in flight together
             for (int s = 1; s < p.splits; ++s) {
                 float more[8];
                 load8(z + (int64_t)s * p.rows * p.ld, nv, more);
@@ -128,49 +152,44 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
     if (col < p.cols) p.sums[(int64_t)blockIdx.y * p.cols + col] = s;
 }
 
-__device__ __forceinline__ void finish_row(const LossArgs& p, int64_t row, float most, float sum, float total, float* lse, float* loss)
-{
-    const int64_t target = p.target[row];
-    const float log_sum = logf(sum);
-    lse[row] = most + log_sum;
-    float v = 0.0f;
-    if (target != p.ignore) {
-        if (loss_column(p, target) < 0) {
-            v = __builtin_nanf("");
-        } else if (most == -__builtin_inff() && sum == 0.0f) {
-            v = __builtin_inff();                              // no class left: the target's share is nothing
-        } else {
-            v = log_sum + (1.0f - p.smooth) * (most - p.hit[row]);
-            if (p.smooth > 0.0f) v += p.smooth * (most - total / (float)p.classes);
-        }
-    }
-    loss[row] = v;
-}
-
-// 32 rows a block, 32 lanes of runs.
+// 16 rows a block, 64 lanes of runs: 4096 rows of 782 runs in 256 blocks (32 rows a block took 16.6 us).
 __global__ __launch_bounds__(1024) void loss_join_kernel(const LossArgs p, int rows, int runs, float* lse, float* loss)
 {
-    __shared__ float part[32][32][3];
-    for (int64_t first = (int64_t)blockIdx.x * 32; first < rows; first += (int64_t)gridDim.x * 32) {
+    __shared__ float part[16][16][3];
+    for (int64_t first = (int64_t)blockIdx.x * 16; first < rows; first += (int64_t)gridDim.x * 16) {
         const int64_t row = first + threadIdx.x;
         float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
+        auto join_lanes = [&] {                                // lanes 16 apart are a row's
+#pragma unroll
+            for (int o = 16; o < 64; o <<= 1) {
+                join_runs(most, sum, __shfl_xor(most, o), __shfl_xor(sum, o));
+                total += __shfl_xor(total, o);
+            }
+        };
         if (row < rows) {
 #pragma unroll 4
-            for (int r = threadIdx.y; r < runs; r += 32) {
+            for (int r = threadIdx.y; r < runs; r += 64) {
                 const float2 v = reinterpret_cast<const float2*>(p.part)[(int64_t)r * rows + row];
                 join_runs(most, sum, v.x, v.y);
                 if (p.part_z) total += p.part_z[(int64_t)r * rows + row];
             }
         }
-        float* mine = part[threadIdx.y][threadIdx.x];
-        mine[0] = most, mine[1] = sum, mine[2] = total;
+        join_lanes();
+        if (threadIdx.y % 4 == 0) {
+            float* to = part[threadIdx.y / 4][threadIdx.x];
+            to[0] = most, to[1] = sum, to[2] = total;
+        }
         __syncthreads();
-        if (threadIdx.y == 0 && row < rows) {
-            for (int y = 1; y < 32; ++y) {
-                join_runs(most, sum, part[y][threadIdx.x][0], part[y][threadIdx.x][1]);
-                total += part[y][threadIdx.x][2];
+        if (threadIdx.y < 4) {                                 // the first wave: four waves' results a lane
+            const float (*from)[16][3] = part + 4 * threadIdx.y;
+            most = from[0][threadIdx.x][0], sum = from[0][threadIdx.x][1], total = from[0][threadIdx.x][2];
+#pragma unroll
+            for (int y = 1; y < 4; ++y) {
+                join_runs(most, sum, from[y][threadIdx.x][0], from[y][threadIdx.x][1]);
+                total += from[y][threadIdx.x][2];
             }
-            finish_row(p, row, most, sum, total, lse, loss);
+            join_lanes();
+            if (threadIdx.y == 0 && row < rows) finish_row(p, row, most, sum, total, lse, loss);
         }
         __syncthreads();
     }
@@ -222,8 +241,8 @@ hipError_t launch_loss_gradient(DType dt, const LossRowsArgs& p, hipStream_t str
 
 hipError_t launch_loss_join(const LossArgs& p, int rows, int runs, float* lse, float* loss, hipStream_t stream)
 {
-    const int64_t grid = ((int64_t)rows + 31) / 32;
-    loss_join_kernel<<<(uint32_t)(grid < 1 << 20 ? grid : 1 << 20), dim3(32, 32), 0, stream>>>(p, rows, runs, lse, loss);
+    const int64_t grid = ((int64_t)rows + 15) / 16;
+    loss_join_kernel<<<(uint32_t)(grid < 1 << 20 ? grid : 1 << 20), dim3(16, 64), 0, stream>>>(p, rows, runs, lse, loss);
     return hipGetLastError();
 }
 

@@ -258,6 +258,8 @@ struct LossRowsArgs {
     int splits;
     const void* bias;         // of the classes from the first column on, or null
     int run;                  // columns of a run
+    float* lse;               // rows of one run are finished at once: their lse and loss; else null
+    float* row_loss;
     // gradient: dz in the tensors' type, zeros from cols to its pitch; column sums as SlopeArgs'
     void* dz;
     int64_t dz_pitch;
