@@ -58,6 +58,33 @@ Copies copies_of(ProductType type, int m, int n, int piece, int k, Rows rows)
     return c;
 }
 
+// A product over all the classes of a piece ends in a round of tiles that leaves most CUs idle.  The classes after its
+// whole rounds of 256 x 256 tiles are then a product of their own, on smaller tiles: the classes of the first, 0 for one
+// product.  WEIGHT_GRAD's classes are its rows, the others' its columns.
+Plan plan_classes(int cus, Product kind, ProductType type, int m, int n, int k)
+{
+    return kind == Product::WEIGHT_GRAD ? plan_product(cus, kind, type, n, k, m, 1, true, true)
+                                        : plan_product(cus, kind, type, m, n, k, 1, true, true);
+}
+int cut_of(int cus, Product kind, ProductType type, int m, int n, int k)
+{
+    if (type == ProductType::F32) return 0;
+    const int64_t across = ((kind == Product::WEIGHT_GRAD ? k : m) + 255) / 256, rounds = across * ((n + 255) / 256) / cus;
+    const int64_t first = rounds * cus / across * 256;
+    if (first <= 0 || first >= n) return 0;
+    const Plan whole = plan_classes(cus, kind, type, m, n, k), a = plan_classes(cus, kind, type, m, (int)first, k),
+               b = plan_classes(cus, kind, type, m, n - (int)first, k);
+    if (!planned(whole) || !planned(a) || !planned(b) || a.splits > 1) return 0;
+    return a.us + b.us + kLaunchUs < whole.us ? (int)first : 0;
+}
+
+// f(first class, classes) for one product or two.
+template <class F> mic_status in_cuts(int n, int cut, F f)
+{
+    MIC_TRY(f(0, cut ? cut : n));
+    return cut ? f(cut, n - cut) : MIC_STATUS_SUCCESS;
+}
+
 // How a call goes.
 struct Way {
     bool fused;              // the logits stay in the tiles that make them
@@ -78,6 +105,13 @@ template <class Bytes> size_t over_pieces(int n, int piece, Bytes bytes)
     return n % piece ? std::max(whole, bytes(n % piece)) : whole;
 }
 
+// Runs that a fused product over `classes` leaves.
+int runs_of(const Plan& pl, ProductType type, int classes)
+{
+    const int columns = loss_columns(type, pl.fast_tile);
+    return (classes + columns - 1) / columns;
+}
+
 Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
 {
     Way fused = {}, memory = {};
@@ -93,7 +127,11 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     const double memory_us = pieces * (memory.plan.us + kLaunchUs) + 2.0 * m * (double)n * 4 / kBytesPerUs;
     Way w = planned(fused.plan) && fused_us < memory_us ? fused : memory;
     if (w.fused) {
-        w.runs = (n + loss_columns(type, w.plan.fast_tile) - 1) / loss_columns(type, w.plan.fast_tile);
+        w.runs = 0;
+        in_cuts(n, cut_of(cus, Product::LOSS, type, m, n, k), [&](int, int classes) {
+            w.runs += runs_of(plan_product(cus, Product::LOSS, type, m, classes, k, 1, true, true), type, classes);
+            return MIC_STATUS_SUCCESS;
+        });
         w.copy_bytes = w.copies.x + w.copies.w;
     } else {
         w.runs = 0;
@@ -108,6 +146,11 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     // the runs' statistics, the targets' logits and the rows' losses
     w.total = w.copy_bytes + w.logits + w.product + (size_t)align_up((int64_t)m * (12 * (int64_t)w.runs + 8), 256);
     return w;
+}
+
+int weight_cut(int cus, const Way& w, ProductType type, int m, int columns, int k)
+{
+    return w.fused ? cut_of(cus, Product::WEIGHT_GRAD, type, m, columns, k) : 0;
 }
 
 Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool bias)
@@ -138,8 +181,11 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
         w.logits = (size_t)align_up((int64_t)m * w.ld_logits * 4, 256);
     }
     w.product = over_pieces(n, w.piece, [&](int columns) {
-        size_t most = std::max(plan_product(cus, Product::INPUT_GRAD, type, m, k, columns, 1, true, now.w).bytes,
-                               plan_product(cus, Product::WEIGHT_GRAD, type, columns, k, m, 1, true, now.x).bytes);
+        size_t most = plan_product(cus, Product::INPUT_GRAD, type, m, k, columns, 1, true, now.w).bytes;
+        in_cuts(columns, weight_cut(cus, w, type, m, columns, k), [&](int, int classes) {
+            most = std::max(most, plan_product(cus, Product::WEIGHT_GRAD, type, classes, k, m, 1, true, now.x).bytes);
+            return MIC_STATUS_SUCCESS;
+        });
         if (!w.fused)
             most = std::max(most, plan_product(cus, Product::FORWARD, logits_type(type), m, columns, k, 1, rows.x, rows.w).bytes);
         return most;
@@ -187,10 +233,20 @@ mic_status loss_name(mic_handle h, mic_dtype dtype, int m, int n, int k, bool ba
     const Rows rows = rows_of(type, k, aligned != 0, aligned != 0);
     const Way w = backward ? backward_way(cus_of(h), type, m, n, k, rows, true) : forward_way(cus_of(h), type, m, n, k, rows);
     if (!planned(w.plan)) return MIC_STATUS_NOT_SUPPORTED;
-    char text[128], product[64];
-    describe(w.plan, product, sizeof(product));
-    snprintf(text, sizeof(text), "%s%s%s, %d pieces", w.fused ? "fused " : "", product, w.copies.pitch ? " copies" : "",
-             (n + w.piece - 1) / w.piece);
+    char text[192], product[64];
+    if (w.fused) {
+        const Product kind = backward ? Product::LOGITS_GRAD : Product::LOSS;
+        int at = snprintf(text, sizeof(text), "fused");
+        in_cuts(w.piece, cut_of(cus_of(h), kind, type, m, w.piece, k), [&](int first, int classes) {
+            describe(plan_product(cus_of(h), kind, type, m, classes, k, 1, true, true), product, sizeof(product));
+            at += snprintf(text + at, sizeof(text) - at, "%s %s", first ? " +" : "", product);
+            return MIC_STATUS_SUCCESS;
+        });
+        snprintf(text + at, sizeof(text) - at, "%s, %d pieces", w.copies.pitch ? " copies" : "", (n + w.piece - 1) / w.piece);
+    } else {
+        describe(w.plan, product, sizeof(product));
+        snprintf(text, sizeof(text), "%s, %d pieces", product, (n + w.piece - 1) / w.piece);
+    }
     return give_name(text, buf, buflen);
 }
 
@@ -266,35 +322,43 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
         if (way.copies.w) o.w = copies + way.copies.x, o.ldw = way.copies.pitch;
         o.columns = (int)(way.copies.pitch / (int64_t)e);
     }
-    int run = 0;
-    for (int v = 0; v < n; v += way.piece) {
-        const int columns = std::min(way.piece, n - v);
+    auto product = [&](int first, int columns) {
         ProductArgs p = {};
         p.a = o.x, p.lda = o.ldx;
-        p.b = o.w + (int64_t)v * o.ldw, p.ldb = o.ldw;
+        p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
         p.M = m, p.N = columns, p.K = k, p.k_segments = 1, p.a_K = o.columns;
-        a.first = v, a.part_first = run;
-        const void* piece_bias = bias ? static_cast<const uint8_t*>(bias) + (int64_t)v * e : nullptr;
-        if (way.fused) {
+        return p;
+    };
+    auto bias_at = [&](int first) { return bias ? static_cast<const uint8_t*>(bias) + (int64_t)first * e : nullptr; };
+    int run = 0;
+    if (way.fused) {
+        MIC_TRY(in_cuts(n, cut_of(handle->num_cu, Product::LOSS, type, m, n, k), [&](int first, int columns) {
+            ProductArgs p = product(first, columns);
             p.loss = a;
-            p.bias = piece_bias;
-            MIC_TRY(run_product(handle, Product::LOSS, type, p, nullptr, 0));
-            continue;
+            p.loss.first = first, p.loss.part_first = run;
+            p.bias = bias_at(first);
+            run += runs_of(plan_product(handle->num_cu, Product::LOSS, type, m, columns, k, 1, true, true), type, columns);
+            return run_product(handle, Product::LOSS, type, p, nullptr, 0);
+        }));
+    } else {
+        for (int v = 0; v < n; v += way.piece) {
+            const int columns = std::min(way.piece, n - v);
+            ProductArgs p = product(v, columns);
+            p.y = logits, p.ldy = way.ld_logits;
+            Sums sums;
+            MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
+            LossRowsArgs r = {};
+            r.loss = a;
+            r.loss.first = v, r.loss.part_first = run;
+            r.rows = m, r.cols = columns;
+            r.z = sums.data, r.ld = sums.ld, r.splits = sums.splits;
+            r.bias = bias_at(v);
+            r.run = run_of(n);
+            if (way.runs == 1) r.lse = lse, r.row_loss = row_loss;
+            MIC_TRY(launched(launch_loss_rows(device_type(dtype), r, handle->stream)));
+            run += (columns + r.run - 1) / r.run;
         }
-        p.y = logits, p.ldy = way.ld_logits;
-        Sums sums;
-        MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
-        LossRowsArgs r = {};
-        r.loss = a;
-        r.rows = m, r.cols = columns;
-        r.z = sums.data, r.ld = sums.ld, r.splits = sums.splits;
-        r.bias = piece_bias;
-        r.run = run_of(n);
-        if (way.runs == 1) r.lse = lse, r.row_loss = row_loss;
-        MIC_TRY(launched(launch_loss_rows(device_type(dtype), r, handle->stream)));
-        run += (columns + r.run - 1) / r.run;
     }
-    a.first = 0;
     if (way.fused || way.runs > 1) MIC_TRY(launched(launch_loss_join(a, m, way.runs, lse, row_loss, handle->stream)));
     if (each) return MIC_STATUS_SUCCESS;
     return launched(launch_loss_reduce(a, m, row_loss, reduction == MIC_REDUCTION_MEAN, loss, count, handle->stream));
@@ -373,18 +437,24 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             if (way.copies.w) o.w = copies + way.copies.x, o.ldw = way.copies.pitch;
             o.columns = (int)(way.copies.pitch / (int64_t)e);
         }
-        a.first = v;
-        const void* piece_bias = bias ? static_cast<const uint8_t*>(bias) + (int64_t)v * e : nullptr;
+        auto product = [&](int first, int classes) {
+            ProductArgs p = {};
+            p.a = o.x, p.lda = o.ldx;
+            p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
+            p.M = m, p.N = classes, p.K = k, p.k_segments = 1, p.a_K = o.columns;
+            p.bias = bias ? static_cast<const uint8_t*>(bias) + (int64_t)(v + first) * e : nullptr;
+            return p;
+        };
         void* piece_dbias = dbias ? static_cast<uint8_t*>(dbias) + (int64_t)v * e : nullptr;
-        ProductArgs p = {};
-        p.a = o.x, p.lda = o.ldx;
-        p.b = o.w, p.ldb = o.ldw;
-        p.M = m, p.N = columns, p.K = k, p.k_segments = 1, p.a_K = o.columns;
         if (way.fused) {
-            p.loss = a;
-            p.bias = piece_bias;
-            p.y = dz, p.ldy = pitch, p.y_columns = (int)pitch;
-            MIC_TRY(run_product(handle, Product::LOGITS_GRAD, type, p, nullptr, 0));
+            MIC_TRY(in_cuts(columns, cut_of(handle->num_cu, Product::LOGITS_GRAD, type, m, columns, k), [&](int first, int classes) {
+                ProductArgs p = product(first, classes);
+                p.loss = a;
+                p.loss.first = v + first;
+                // the last classes' product also clears what pads dz's rows
+                p.y = dz + first * (int64_t)e, p.ldy = pitch, p.y_columns = first + classes == columns ? (int)pitch - first : classes;
+                return run_product(handle, Product::LOGITS_GRAD, type, p, nullptr, 0);
+            }));
             if (dbias) {
                 SlopeArgs s = {};
                 s.rows = m, s.cols = columns;
@@ -394,14 +464,17 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
                 MIC_TRY(launched(launch_slope(device_type(dtype), s, handle->stream)));
             }
         } else {
+            ProductArgs p = product(0, columns);
+            LossRowsArgs r = {};
+            r.bias = p.bias;
+            p.bias = nullptr;
             p.y = logits, p.ldy = way.ld_logits;
             Sums sums;
             MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
-            LossRowsArgs r = {};
             r.loss = a;
+            r.loss.first = v;
             r.rows = m, r.cols = columns;
             r.z = sums.data, r.ld = sums.ld, r.splits = sums.splits;
-            r.bias = piece_bias;
             r.dz = dz, r.dz_pitch = pitch;
             r.sums = dbias ? column_sums : nullptr, r.dbias = piece_dbias;
             MIC_TRY(launched(launch_loss_gradient(device_type(dtype), r, handle->stream)));
@@ -417,16 +490,18 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             if (way.piece < n) g.sum = sum, g.ld_sum = align_up(k, 8), g.sum_first = v == 0, g.sum_last = v + columns == n;
             MIC_TRY(run_product(handle, Product::INPUT_GRAD, type, g, space, way.product));
         }
-        if (dw && k) {
-            ProductArgs g = {};
-            g.a = dz, g.lda = pitch * (int64_t)e;
-            g.b = o.x, g.ldb = o.ldx;
-            g.M = columns, g.N = k, g.K = m, g.a_rows = (int)pitch, g.b_rows = o.columns;
-            g.k_segments = 1;
-            g.m_pitch = INT32_MAX, g.m_valid = columns;
-            g.y = static_cast<uint8_t*>(dw) + (int64_t)v * lddw * (int64_t)e, g.ldy = lddw;
-            MIC_TRY(run_product(handle, Product::WEIGHT_GRAD, type, g, space, way.product));
-        }
+        if (dw && k)
+            MIC_TRY(in_cuts(columns, weight_cut(handle->num_cu, way, type, m, columns, k), [&](int first, int classes) {
+                ProductArgs g = {};
+                g.a = dz + first * (int64_t)e, g.lda = pitch * (int64_t)e;
+                g.b = o.x, g.ldb = o.ldx;
+                g.M = classes, g.N = k, g.K = m, g.b_rows = o.columns;
+                g.a_rows = first + classes == columns ? (int)pitch - first : classes;
+                g.k_segments = 1;
+                g.m_pitch = INT32_MAX, g.m_valid = classes;
+                g.y = static_cast<uint8_t*>(dw) + (int64_t)(v + first) * lddw * (int64_t)e, g.ldy = lddw;
+                return run_product(handle, Product::WEIGHT_GRAD, type, g, space, way.product);
+            }));
     }
     return MIC_STATUS_SUCCESS;
 }
