@@ -69,7 +69,7 @@ namespace miconv {
 // The cheapest way through a product of m x n outputs and k_segments * k terms.
 // `aligned_a` / `aligned_b`: the operand's rows can be read 16 bytes at a time.
 Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, bool aligned_a,
-                  bool aligned_b)
+                  bool aligned_b, int least_splits)
 {
     const int raw_n = kind == Product::GATED ? miconv::gated_raw_columns(n) : n;
     const int e = element_bytes(type);
@@ -104,7 +104,8 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         if (t * (pl.fast ? 512 : 256) >= int64_t(1) << 32) return;
         // weights that one or two row tiles read come from memory at its latency, two steps in flight
         if (m <= 2 * bm) step = std::max(step, 0.9);
-        for (int s = 1, most = whole ? 1 : most_splits(t); s <= most; ++s) {
+        const int most = whole ? 1 : std::max(least_splits, most_splits(t));
+        for (int s = least_splits; s <= most; ++s) {
             const double us = std::max(rounds(t * s, slots) * ((steps + s - 1) / s * step + tile), read_us) + join_us(s) + pl.us + 1.5;
             if (us < best.us) {
                 best = pl;
@@ -193,7 +194,7 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
     bool aligned_b = fast_rows(p.b, p.ldb, b_bytes);
     if (two_b) aligned_b = aligned_b && fast_rows(p.b2, p.ldb2, b_bytes);
     if (p.k_segments > 1) aligned_b = aligned_b && p.ldb == p.ldb2;
-    const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b);
+    const Plan pl = plan_product(h->num_cu, kind, type, p.M, p.N, p.K, p.k_segments, aligned_a, aligned_b, p.splits > 1 ? p.splits : 1);
     if (!planned(pl)) return MIC_STATUS_NOT_SUPPORTED;
     if (pl.bytes > bytes || (pl.bytes && (!workspace || !aligned(workspace, 16)))) return MIC_STATUS_BAD_PARAM;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -33,8 +33,9 @@ inline int element_bytes(ProductType t)
 
 // The cheapest way through a product of m x n outputs and k_segments * k terms.
 // `aligned_a` / `aligned_b`: the operand's rows can be read 16 bytes at a time.
+// `least_splits`: the parts the reduction has at least.
 Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, bool aligned_a,
-                  bool aligned_b);
+                  bool aligned_b, int least_splits = 1);
 
 // Whether any kernel's grid holds the product.
 inline bool planned(const Plan& pl) { return pl.us < 1e30; }
@@ -49,7 +50,7 @@ struct Sums {
     int splits;
 };
 
-// Runs p in the workspace.  sums: the outputs are fp32 in p.y, or left there in parts.
+// Runs p in the workspace, in p.splits parts at least.  sums: the outputs are fp32 in p.y, or left there in parts.
 mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes,
                        Sums* sums = nullptr);
 
