@@ -71,6 +71,7 @@ def test_sizes(m, n, k, dtype):
 WAYS = [("fused fast 256x256, 1", BF16, 1500, 8200, 64), ("fused fast 256x192, 1", BF16, 1000, 8200, 64),
         ("fused fast 192x256, 1", BF16, 515, 20011, 40), ("fused fast 256x128, 1", BF16, 200, 2500, 64),
         ("fused fast 128x256, 1", BF16, 770, 8200, 64), ("fused fast 128x128, 1", BF16, 260, 135, 256),
+        ("fused fast 256x256 + fast 128x128, 1", BF16, 1024, 17003, 1024),
         ("fused fast 128x128, 1", F32, 200, 8200, 64), ("fused fast 128x64, 1", F32, 70, 130, 64),
         ("fused fast 64x128, 1", F32, 129, 8200, 64), ("fused fast 128x128 copies", BF16, 1000, 2000, 71),
         ("fused fast 128x64 copies", F32, 1000, 1001, 65), ("any 64x64 split 4", BF16, 64, 130, 1024),
