@@ -12,6 +12,7 @@
 #include <unordered_map>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -96,14 +97,22 @@ bool plain_scale(const Tensor& t, const Tensor& like, int64_t rows)
 void* data(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 float* floats(const Tensor* t) { return t ? static_cast<float*>(t->data_ptr()) : nullptr; }
 
+// An uninitialised tensor on the current device, from torch's own allocator without the dispatcher's way to it, which
+// takes longer than the allocation (a norm of one token allocates four).
+Tensor fresh(at::IntArrayRef sizes, at::ScalarType type)
+{
+    static c10::Allocator* const from = at::empty({0}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA)).storage().allocator();
+    return Tensor(at::detail::empty_generic(sizes, from, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
+}
+
 Tensor rows_of(const Tensor& x, int64_t cols, at::ScalarType type)
 {
     auto shape = x.sizes().vec();
     shape.back() = cols;
-    return at::empty(shape, x.options().dtype(type));
+    return fresh(shape, type);
 }
 
-Tensor like(const Tensor& t, at::ScalarType type) { return at::empty(t.sizes(), t.options().dtype(type)); }
+Tensor like(const Tensor& t, at::ScalarType type) { return fresh(t.sizes(), type); }
 
 // Whether the rows of a contiguous matrix count as aligned: a call on such operands copies none.
 bool even(const Tensor& t)
@@ -136,7 +145,7 @@ template <class Ask> bool workspace(int call, mic_dtype d, int64_t m, int64_t n,
         if (sizes.size() > 4096) sizes.clear();
         sizes.emplace(key, bytes);
     }
-    if (bytes) space = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
+    if (bytes) space = fresh({(int64_t)bytes}, at::kByte);
     return true;
 }
 
@@ -189,7 +198,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (!h) return none();
     Tensor y = like(*x, e4m3 ? at::kFloat8_e4m3fn : type), sum, scale;
     if (residual) sum = like(*x, type);
-    Tensor rstd = at::empty(x->sizes().slice(0, x->dim() - 1), x->options().dtype(at::kFloat));
+    Tensor rstd = fresh(x->sizes().slice(0, x->dim() - 1), at::kFloat);
     if (e4m3) scale = like(rstd, at::kFloat);
     if (mic_rms_norm(h, d, e4m3 ? MIC_DTYPE_F8_E4M3 : d, (int)rows, (int)cols, eps, x->data_ptr(), cols, data(residual), cols,
                      w->data_ptr(), y.data_ptr(), cols, residual ? sum.data_ptr() : nullptr, cols,
@@ -321,7 +330,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     Tensor dx, dw, db;
     if (need_dx) dx = like(*x, type);
     if (need_dw) dw = like(*w, type);
-    if (bias) db = at::empty({n}, dy->options());
+    if (bias) db = fresh({n}, type);
     if (mic_linear_backward(h, d, (mic_activation)act, (int)m, (int)n, (int)k, dy->data_ptr(), n, x->data_ptr(), k,
                             w->data_ptr(), k, act ? data(pre) : nullptr, n, need_dx ? dx.data_ptr() : nullptr, k,
                             need_dw ? dw.data_ptr() : nullptr, k,
@@ -439,7 +448,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (!h) return none();
     Tensor y = like(*x, e4m3 ? at::kFloat8_e4m3fn : type), sum, scale;
     if (residual) sum = like(*x, type);
-    Tensor mean = at::empty(x->sizes().slice(0, x->dim() - 1), x->options().dtype(at::kFloat));
+    Tensor mean = fresh(x->sizes().slice(0, x->dim() - 1), at::kFloat);
     Tensor rstd = like(mean, at::kFloat);
     if (e4m3) scale = like(mean, at::kFloat);
     if (mic_layer_norm(h, d, e4m3 ? MIC_DTYPE_F8_E4M3 : d, (int)rows, (int)cols, eps, x->data_ptr(), cols, data(residual), cols,
@@ -585,9 +594,9 @@ PyObject* linear_cross_entropy(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         }))
         return none();
     const bool each = reduction == MIC_REDUCTION_NONE;
-    Tensor lse = at::empty(target->sizes(), x->options().dtype(at::kFloat)), loss, count;
+    Tensor lse = fresh(target->sizes(), at::kFloat), loss, count;
     if (each) loss = like(lse, at::kFloat);
-    else loss = at::empty({}, lse.options()), count = at::empty({}, lse.options());
+    else loss = fresh({}, at::kFloat), count = fresh({}, at::kFloat);
     if (mic_linear_cross_entropy(h, d, (mic_reduction)reduction, (int)m, (int)n, (int)k, x->data_ptr(), k, w->data_ptr(), k,
                                  data(bias), static_cast<const int64_t*>(target->data_ptr()), ignore, smoothing, floats(&loss),
                                  floats(&lse), each ? nullptr : floats(&count), bytes ? space.data_ptr() : nullptr, bytes)

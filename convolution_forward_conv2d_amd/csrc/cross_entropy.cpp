@@ -152,6 +152,9 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     return w;
 }
 
+// The product that makes dx, or a piece of it.
+Product input_kind(const Way& w, int n) { return w.piece < n ? Product::INPUT_SUM : Product::INPUT_GRAD; }
+
 int weight_cut(int cus, const Way& w, ProductType type, int m, int columns, int k)
 {
     return w.fused ? cut_of(cus, Product::WEIGHT_GRAD, type, m, columns, k) : 0;
@@ -185,7 +188,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
         w.logits = (size_t)align_up((int64_t)m * w.ld_logits * 4, 256);
     }
     w.product = over_pieces(n, w.piece, [&](int columns) {
-        size_t most = plan_product(cus, Product::INPUT_GRAD, type, m, k, columns, 1, true, now.w, gradient_parts(type, columns)).bytes;
+        size_t most = plan_product(cus, input_kind(w, n), type, m, k, columns, 1, true, now.w, gradient_parts(type, columns)).bytes;
         in_cuts(columns, weight_cut(cus, w, type, m, columns, k), [&](int, int classes) {
             most = std::max(most, plan_product(cus, Product::WEIGHT_GRAD, type, classes, k, m, 1, true, now.x, gradient_parts(type, m)).bytes);
             return MIC_STATUS_SUCCESS;
@@ -327,7 +330,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
         o.columns = (int)(way.copies.pitch / (int64_t)e);
     }
     auto product = [&](int first, int columns) {
-        ProductArgs p = {};
+        LossProductArgs p = {};
         p.a = o.x, p.lda = o.ldx;
         p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
         p.M = m, p.N = columns, p.K = k, p.k_segments = 1, p.a_K = o.columns;
@@ -337,7 +340,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
     int run = 0;
     if (way.fused) {
         MIC_TRY(in_cuts(n, cut_of(handle->num_cu, Product::LOSS, type, m, n, k), [&](int first, int columns) {
-            ProductArgs p = product(first, columns);
+            LossProductArgs p = product(first, columns);
             p.loss = a;
             p.loss.first = first, p.loss.part_first = run;
             p.bias = bias_at(first);
@@ -347,7 +350,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
     } else {
         for (int v = 0; v < n; v += way.piece) {
             const int columns = std::min(way.piece, n - v);
-            ProductArgs p = product(v, columns);
+            LossProductArgs p = product(v, columns);
             p.y = logits, p.ldy = way.ld_logits;
             Sums sums;
             MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
@@ -442,7 +445,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             o.columns = (int)(way.copies.pitch / (int64_t)e);
         }
         auto product = [&](int first, int classes) {
-            ProductArgs p = {};
+            LossProductArgs p = {};
             p.a = o.x, p.lda = o.ldx;
             p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
             p.M = m, p.N = classes, p.K = k, p.k_segments = 1, p.a_K = o.columns;
@@ -452,7 +455,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
         void* piece_dbias = dbias ? static_cast<uint8_t*>(dbias) + (int64_t)v * e : nullptr;
         if (way.fused) {
             MIC_TRY(in_cuts(columns, cut_of(handle->num_cu, Product::LOGITS_GRAD, type, m, columns, k), [&](int first, int classes) {
-                ProductArgs p = product(first, classes);
+                LossProductArgs p = product(first, classes);
                 p.loss = a;
                 p.loss.first = v + first;
                 // the last classes' product also clears what pads dz's rows
@@ -468,7 +471,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
                 MIC_TRY(launched(launch_slope(device_type(dtype), s, handle->stream)));
             }
         } else {
-            ProductArgs p = product(0, columns);
+            LossProductArgs p = product(0, columns);
             LossRowsArgs r = {};
             r.bias = p.bias;
             p.bias = nullptr;
@@ -484,7 +487,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             MIC_TRY(launched(launch_loss_gradient(device_type(dtype), r, handle->stream)));
         }
         if (dx && k) {
-            ProductArgs g = {};
+            LossProductArgs g = {};
             g.a = dz, g.lda = pitch * (int64_t)e;
             g.b = o.w, g.ldb = o.ldw;
             g.M = m, g.N = k, g.K = columns, g.a_K = (int)pitch, g.b_rows = o.columns;
@@ -492,8 +495,8 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             g.m_pitch = INT32_MAX, g.m_valid = m;
             g.y = dx, g.ldy = lddx;
             g.splits = gradient_parts(type, columns);
-            if (way.piece < n) g.sum = sum, g.ld_sum = align_up(k, 8), g.sum_first = v == 0, g.sum_last = v + columns == n;
-            MIC_TRY(run_product(handle, Product::INPUT_GRAD, type, g, space, way.product));
+            g.sum = sum, g.ld_sum = align_up(k, 8), g.sum_first = v == 0, g.sum_last = v + columns == n;
+            MIC_TRY(run_product(handle, input_kind(way, n), type, g, space, way.product));
         }
         if (dw && k)
             MIC_TRY(in_cuts(columns, weight_cut(handle->num_cu, way, type, m, columns, k), [&](int first, int classes) {

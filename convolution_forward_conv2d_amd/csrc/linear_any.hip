@@ -65,7 +65,7 @@ template <int E, bool ACROSS, int R> struct Loader {
 };
 
 template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN>
-__global__ __launch_bounds__(THREADS) void linear_any_kernel(const ProductArgs p)
+__global__ __launch_bounds__(THREADS) void linear_any_kernel(const ArgsOf<EPI> p)
 {
     constexpr int E = Mul::E, BK = 128 / E, FM = BM / 64, FN = BN / 64;
     constexpr int STEP = (BM + BN) * 128;
@@ -146,10 +146,11 @@ hipError_t launch_one(const ProductArgs& p, int tile, hipStream_t stream)
     const int64_t tiles = (int64_t)((p.M + tile - 1) / tile) * ((raw_n + tile - 1) / tile);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     const dim3 grid((uint32_t)tiles, 1, (uint32_t)p.splits);
+    const auto& args = static_cast<const ArgsOf<EPI>&>(p);
     if (tile == 128)
-        linear_any_kernel<Mul, AACROSS, BACROSS, EPI, 128, 128><<<grid, THREADS, 0, stream>>>(p);
+        linear_any_kernel<Mul, AACROSS, BACROSS, EPI, 128, 128><<<grid, THREADS, 0, stream>>>(args);
     else
-        linear_any_kernel<Mul, AACROSS, BACROSS, EPI, 64, 64><<<grid, THREADS, 0, stream>>>(p);
+        linear_any_kernel<Mul, AACROSS, BACROSS, EPI, 64, 64><<<grid, THREADS, 0, stream>>>(args);
     return hipGetLastError();
 }
 
@@ -160,6 +161,7 @@ template <class Mul> hipError_t launch_type(Product kind, const ProductArgs& p, 
     case Product::GATED: return launch_one<Mul, false, false, EPI_GATED>(p, tile, stream);
     case Product::INPUT_GRAD: return launch_one<Mul, false, true, EPI_PLAIN>(p, tile, stream);
     case Product::WEIGHT_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+    case Product::INPUT_SUM: return launch_one<Mul, false, true, EPI_SUM>(p, tile, stream);
     default: break;
     }
     return hipErrorInvalidValue;
@@ -173,7 +175,7 @@ template <class Mul> hipError_t launch_e4m3(Product kind, const ProductArgs& p, 
 }
 
 template <class Out, int EPI>
-__global__ __launch_bounds__(256) void join_kernel(const ProductArgs p)
+__global__ __launch_bounds__(256) void join_kernel(const ArgsOf<EPI> p)
 {
     const int per = (p.N + 7) / 8;
     const int64_t total = (int64_t)p.M * per;
@@ -205,6 +207,9 @@ template <class Out> hipError_t join_type(Product kind, const ProductArgs& p, in
     switch (kind) {
     case Product::FORWARD: join_kernel<Out, EPI_LINEAR><<<blocks, 256, 0, stream>>>(p); break;
     case Product::GATED: join_kernel<Out, EPI_GATED><<<blocks, 256, 0, stream>>>(p); break;
+    case Product::INPUT_SUM:
+        join_kernel<Out, EPI_SUM><<<blocks, 256, 0, stream>>>(static_cast<const LossProductArgs&>(p));
+        break;
     default: join_kernel<Out, EPI_PLAIN><<<blocks, 256, 0, stream>>>(p); break;
     }
     return hipGetLastError();

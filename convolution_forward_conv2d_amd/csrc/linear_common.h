@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include <hip/hip_runtime.h>
 
 #include "mfma_common.h"
@@ -227,17 +229,21 @@ struct ProductArgs {
     int splits;
     float* part;
     int64_t part_ld;
-    // EPI_PLAIN: one of several products that add up to y.  Their sum so far, fp32, rows of ld_sum; the first writes it,
-    // the last adds to it and writes y instead
+};
+
+// A product of a loss's kinds.
+struct LossProductArgs : ProductArgs {
+    LossArgs loss;
+    int y_columns;            // EPI_LOGITS_GRAD: y is dz, whose columns up to y_columns are written, zeros past N
+    // EPI_SUM: one of several products that add up to y.  Their sum so far, fp32, rows of ld_sum: the first writes it, the
+    // last adds to it and writes y instead
     float* sum;
     int64_t ld_sum;
     bool sum_first, sum_last;
-    // EPI_LOSS, EPI_LOGITS_GRAD (y: dz, whose columns up to y_columns are written, zeros past N)
-    LossArgs loss;
-    int y_columns;
 };
 
-enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_LOSS = 3, EPI_LOGITS_GRAD = 4 };
+enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_LOSS = 3, EPI_LOGITS_GRAD = 4, EPI_SUM = 5 };
+template <int EPI> using ArgsOf = std::conditional_t<(EPI >= EPI_LOSS), LossProductArgs, ProductArgs>;
 
 // A gated layer's raw columns come in blocks of 32, 16 of the gate's and the
 // same 16 of the other product's, so both meet in one workgroup (and one wave)
@@ -320,27 +326,27 @@ template <bool EXACT> __device__ __forceinline__ float loss_gradient(const LossR
 
 // Eight finished columns n..n+7 of row m: v the raw sums (u the second product's).
 template <class Out, int EPI>
-__device__ __forceinline__ void finish8(const ProductArgs& p, int m, int n, float (&v)[8], float (&u)[8])
+__device__ __forceinline__ void finish8(const ArgsOf<EPI>& p, int m, int n, float (&v)[8], float (&u)[8])
 {
     constexpr bool EXACT = sizeof(Out) == 4;
     if constexpr (EPI == EPI_PLAIN) {
         const bool second = m >= p.m_pitch;
         const int r = second ? m - p.m_pitch : m;
         if (r >= p.m_valid || n >= p.N) return;
-        if (p.sum) {
-            float* sum = p.sum + (int64_t)r * p.ld_sum + n;
-            if (!p.sum_first) {
-                load8(sum, p.N - n, u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += u[i];
-            }
-            if (!p.sum_last) {
-                store8(sum, p.N - n, v);
-                return;
-            }
-        }
         Out* y = second ? static_cast<Out*>(p.y2) + (int64_t)r * p.ldy2 : static_cast<Out*>(p.y) + (int64_t)r * p.ldy;
         store8(y + n, p.N - n, v);
+        return;
+    }
+    if constexpr (EPI == EPI_SUM) {
+        if (m >= p.M || n >= p.N) return;
+        float* sum = p.sum + (int64_t)m * p.ld_sum + n;
+        if (!p.sum_first) {
+            load8(sum, p.N - n, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += u[i];
+        }
+        if (p.sum_last) store8(static_cast<Out*>(p.y) + (int64_t)m * p.ldy + n, p.N - n, v);
+        else store8(sum, p.N - n, v);
         return;
     }
     if constexpr (EPI == EPI_LOGITS_GRAD) {

@@ -132,7 +132,7 @@ template <int PENDING> __device__ __forceinline__ void landed()
 }
 
 template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const ProductArgs p)
+__global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const ArgsOf<EPI> p)
 {
     static_assert(WM * WN == 8 && BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "eight waves of 32 x 32 blocks");
     constexpr int E = Mul::E, BK = 128 / E, T = Mul::T, FM = BM / WM / T, FN = BN / WN / T;

@@ -14,7 +14,7 @@ hipError_t launch_tile(const ProductArgs& p, hipStream_t stream)
     const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((raw_n + BN - 1) / BN);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     linear_fast_kernel<Mul, AACROSS, BACROSS, EPI, BM, BN, WM, WN>
-        <<<dim3((uint32_t)tiles, 1, (uint32_t)p.splits), FAST_THREADS, 0, stream>>>(p);
+        <<<dim3((uint32_t)tiles, 1, (uint32_t)p.splits), FAST_THREADS, 0, stream>>>(static_cast<const ArgsOf<EPI>&>(p));
     return hipGetLastError();
 }
 

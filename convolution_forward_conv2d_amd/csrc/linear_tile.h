@@ -194,7 +194,7 @@ template <class Out, int EPI, int W> struct WholeRows {
 // 64- or 128-byte lines per row.  The caller has passed a barrier after the
 // last read of the operand tiles.
 template <class Out, int EPI, class Block, int FM, int FN>
-__device__ __forceinline__ void finish_wave(const ProductArgs& p, float* stage, Block (&acc)[FM][FN], int m0, int j0,
+__device__ __forceinline__ void finish_wave(const ArgsOf<EPI>& p, float* stage, Block (&acc)[FM][FN], int m0, int j0,
                                             int split, int lane)
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, W = T * FN, PITCH = W + 4, ROWS = T * FM;

@@ -34,7 +34,7 @@ __device__ __forceinline__ void add_bias(const ProductArgs& p, Block (&acc)[FM][
 // Each row's largest logit of these columns and the sum of e^(z - largest), [run][row]: run = the wave's columns; with
 // smoothing the sum of z; the target's logit where it is among them.
 template <bool EXACT, class Block, int FM, int FN>
-__device__ __forceinline__ void loss_wave(const ProductArgs& p, Block (&acc)[FM][FN], int m0, int j0, int lane)
+__device__ __forceinline__ void loss_wave(const LossProductArgs& p, Block (&acc)[FM][FN], int m0, int j0, int lane)
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, V = sizeof(Block) / 4, W = T * FN;
     using In = typename std::conditional<EXACT, float, Bf16>::type;
@@ -97,7 +97,7 @@ __device__ __forceinline__ void loss_wave(const ProductArgs& p, Block (&acc)[FM]
 
 // The logits' gradient in their place, zeros past N.
 template <bool EXACT, class Block, int FM, int FN>
-__device__ __forceinline__ void gradient_wave(const ProductArgs& p, Block (&acc)[FM][FN], int m0, int j0, int lane)
+__device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&acc)[FM][FN], int m0, int j0, int lane)
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, V = sizeof(Block) / 4, W = T * FN;
     using In = typename std::conditional<EXACT, float, Bf16>::type;
