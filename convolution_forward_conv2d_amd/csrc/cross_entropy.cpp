@@ -112,18 +112,30 @@ template <class Bytes> size_t over_pieces(int n, int piece, Bytes bytes)
 // Runs that a fused product over `classes` leaves.
 int runs_of(const Plan& pl, ProductType type, int classes)
 {
-    const int columns = loss_columns(type, pl.fast_tile);
+    const int columns = pl.few ? 8 : loss_columns(type, pl.fast_tile);
     return (classes + columns - 1) / columns;
+}
+
+// A fused forward product's cut, and the plan of one of its parts.
+int loss_cut(int cus, const Way& w, ProductType type, int m, int n, int k)
+{
+    return w.plan.few ? 0 : cut_of(cus, Product::LOSS, type, m, n, k);
+}
+Plan loss_plan(int cus, const Way& w, ProductType type, int m, int n, int classes, int k)
+{
+    return classes == n ? w.plan : plan_product(cus, Product::LOSS, type, m, classes, k, 1, true, true);
 }
 
 Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
 {
     Way fused = {}, memory = {};
-    // whole tiles from aligned rows, copied first where they are not
+    // few rows as they lie, whole tiles from aligned rows, copied first where they are not
     fused.fused = true;
     fused.piece = n;
     fused.copies = copies_of(type, m, n, n, k, rows);
     fused.plan = plan_product(cus, Product::LOSS, type, m, n, k, 1, true, true);
+    const Plan few = plan_product(cus, Product::LOSS, type, m, n, k, 1, rows.x && rows.w, rows.x && rows.w);
+    if (few.few && few.us <= fused.plan.us + fused.copies.us) fused.plan = few, fused.copies = {};
     memory.piece = piece_of(kLogitsBytes, m, n, 4);
     memory.plan = plan_product(cus, Product::FORWARD, logits_type(type), m, memory.piece, k, 1, rows.x, rows.w);
     const double pieces = (n + memory.piece - 1) / memory.piece;
@@ -132,8 +144,8 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     Way w = planned(fused.plan) && fused_us < memory_us ? fused : memory;
     if (w.fused) {
         w.runs = 0;
-        in_cuts(n, cut_of(cus, Product::LOSS, type, m, n, k), [&](int, int classes) {
-            w.runs += runs_of(plan_product(cus, Product::LOSS, type, m, classes, k, 1, true, true), type, classes);
+        in_cuts(n, loss_cut(cus, w, type, m, n, k), [&](int first, int classes) {
+            w.runs += runs_of(loss_plan(cus, w, type, m, n, classes, k), type, classes);
             return MIC_STATUS_SUCCESS;
         });
         w.copy_bytes = w.copies.x + w.copies.w;
@@ -150,6 +162,13 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     // the runs' statistics, the targets' logits and the rows' losses
     w.total = w.copy_bytes + w.logits + w.product + (size_t)align_up((int64_t)m * (12 * (int64_t)w.runs + 8), 256);
     return w;
+}
+
+// Sums of each column that a fused product over `classes` leaves.
+int sum_groups(int cus, ProductType type, int m, int classes, int k)
+{
+    const int rows = loss_rows(type, plan_product(cus, Product::LOGITS_GRAD, type, m, classes, k, 1, true, true).fast_tile);
+    return (m + rows - 1) / rows;
 }
 
 // The product that makes dx, or a piece of it.
@@ -170,8 +189,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
     fused.plan = plan_product(cus, Product::LOGITS_GRAD, type, m, fused.piece, k, 1, true, true);
     memory.plan = plan_product(cus, Product::FORWARD, logits_type(type), m, memory.piece, k, 1, rows.x, rows.w);
     const double pieces = (n + fused.piece - 1) / fused.piece;
-    const double fused_us = pieces * (fused.plan.us + (bias ? kLaunchUs : 0.0)) + fused.copies.us
-                            + (bias ? (double)m * n * e / kBytesPerUs : 0.0);
+    const double fused_us = pieces * (fused.plan.us + (bias ? kLaunchUs : 0.0)) + fused.copies.us;
     const double memory_us = pieces * (memory.plan.us + kLaunchUs) + (double)m * n * (8 + e) / kBytesPerUs;
     Way w = planned(fused.plan) && fused_us < memory_us ? fused : memory;
     const Rows now = w.fused ? Rows{true, true} : rows;
@@ -180,7 +198,15 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
     w.dz = (size_t)align_up((int64_t)m * w.dz_pitch * e, 256);
     if (bias)
         w.sums = over_pieces(n, w.piece, [&](int columns) {
-            return (size_t)align_up((int64_t)slope_row_groups(m, columns) * columns * 4, 256);
+            size_t most = (size_t)slope_row_groups(m, columns) * columns;
+            if (w.fused) {
+                most = 0;
+                in_cuts(columns, cut_of(cus, Product::LOGITS_GRAD, type, m, columns, k), [&](int, int classes) {
+                    most = std::max(most, (size_t)sum_groups(cus, type, m, classes, k) * classes);
+                    return MIC_STATUS_SUCCESS;
+                });
+            }
+            return (size_t)align_up(most * 4, 256);
         });
     if (w.piece < n) w.sum = (size_t)align_up((int64_t)m * align_up(k, 8) * 4, 256);
     if (!w.fused) {
@@ -244,8 +270,10 @@ mic_status loss_name(mic_handle h, mic_dtype dtype, int m, int n, int k, bool ba
     if (w.fused) {
         const Product kind = backward ? Product::LOGITS_GRAD : Product::LOSS;
         int at = snprintf(text, sizeof(text), "fused");
-        in_cuts(w.piece, cut_of(cus_of(h), kind, type, m, w.piece, k), [&](int first, int classes) {
-            describe(plan_product(cus_of(h), kind, type, m, classes, k, 1, true, true), product, sizeof(product));
+        const int cut = backward ? cut_of(cus_of(h), kind, type, m, w.piece, k) : loss_cut(cus_of(h), w, type, m, n, k);
+        in_cuts(w.piece, cut, [&](int first, int classes) {
+            describe(classes == w.piece ? w.plan : plan_product(cus_of(h), kind, type, m, classes, k, 1, true, true), product,
+                     sizeof(product));
             at += snprintf(text + at, sizeof(text) - at, "%s %s", first ? " +" : "", product);
             return MIC_STATUS_SUCCESS;
         });
@@ -339,12 +367,12 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
     auto bias_at = [&](int first) { return bias ? static_cast<const uint8_t*>(bias) + (int64_t)first * e : nullptr; };
     int run = 0;
     if (way.fused) {
-        MIC_TRY(in_cuts(n, cut_of(handle->num_cu, Product::LOSS, type, m, n, k), [&](int first, int columns) {
+        MIC_TRY(in_cuts(n, loss_cut(handle->num_cu, way, type, m, n, k), [&](int first, int columns) {
             LossProductArgs p = product(first, columns);
             p.loss = a;
             p.loss.first = first, p.loss.part_first = run;
             p.bias = bias_at(first);
-            run += runs_of(plan_product(handle->num_cu, Product::LOSS, type, m, columns, k, 1, true, true), type, columns);
+            run += runs_of(loss_plan(handle->num_cu, way, type, m, n, columns, k), type, columns);
             return run_product(handle, Product::LOSS, type, p, nullptr, 0);
         }));
     } else {
@@ -460,16 +488,13 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
                 p.loss.first = v + first;
                 // the last classes' product also clears what pads dz's rows
                 p.y = dz + first * (int64_t)e, p.ldy = pitch, p.y_columns = first + classes == columns ? (int)pitch - first : classes;
-                return run_product(handle, Product::LOGITS_GRAD, type, p, nullptr, 0);
+                p.sums = dbias ? column_sums : nullptr;
+                MIC_TRY(run_product(handle, Product::LOGITS_GRAD, type, p, nullptr, 0));
+                if (!dbias) return MIC_STATUS_SUCCESS;
+                return launched(launch_column_join(device_type(dtype), column_sums,
+                                                   sum_groups(handle->num_cu, type, m, classes, k), classes,
+                                                   static_cast<uint8_t*>(piece_dbias) + first * (int64_t)e, handle->stream));
             }));
-            if (dbias) {
-                SlopeArgs s = {};
-                s.rows = m, s.cols = columns;
-                s.dy = dz, s.lddy = pitch;
-                s.dz_pitch = s.up_at = pitch;
-                s.sums = column_sums, s.dbias = piece_dbias;
-                MIC_TRY(launched(launch_slope(device_type(dtype), s, handle->stream)));
-            }
         } else {
             LossProductArgs p = product(0, columns);
             LossRowsArgs r = {};

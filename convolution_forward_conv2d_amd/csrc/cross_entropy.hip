@@ -15,13 +15,10 @@ namespace miconv {
 
 namespace {
 
-// (largest, sum of e^(z - largest)) of two sets of logits together.
-__device__ __forceinline__ void join_runs(float& most, float& sum, float most2, float sum2)
+// e^(most - top), what a sum taken from `most` is worth at `top`, at least as large: 0 of nothing (-infinity).
+__device__ __forceinline__ float above(float most, float top)
 {
-    const float top = fmaxf(most, most2);
-    // equal ones need no factor, two empty ones (-infinity) have none
-    sum = (most == top ? sum : sum * exponential<true>(most - top)) + (most2 == top ? sum2 : sum2 * exponential<true>(most2 - top));
-    most = top;
+    return exponential<true>(most - (top == -__builtin_inff() ? 0.0f : top));
 }
 
 constexpr int THREADS = 256;
@@ -80,20 +77,22 @@ template <class T> __global__ __launch_bounds__(THREADS) void loss_rows_kernel(c
             for (int u = 0; u < 4; ++u) sum += exponential<true>(z[u] - from);
             most = top;
         }
+        // the largest first, so that each lane, and wave, brings its sum there once
+        float top = most;
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            join_runs(most, sum, __shfl_xor(most, o), __shfl_xor(sum, o));
-            total += __shfl_xor(total, o);
-        }
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        sum *= above(most, top);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o), total += __shfl_xor(total, o);
         const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) part[wave][0] = most, part[wave][1] = sum, part[wave][2] = total;
+        if ((threadIdx.x & 63) == 0) part[wave][0] = top, part[wave][1] = sum, part[wave][2] = total;
         __syncthreads();                                       // hit[row] is another thread's, too
         if (threadIdx.x == 0) {
+            most = -__builtin_inff(), sum = total = 0.0f;
 #pragma unroll
-            for (int w = 1; w < THREADS / 64; ++w) {
-                join_runs(most, sum, part[w][0], part[w][1]);
-                total += part[w][2];
-            }
+            for (int w = 0; w < THREADS / 64; ++w) most = fmaxf(most, part[w][0]);
+#pragma unroll
+            for (int w = 0; w < THREADS / 64; ++w) sum += part[w][1] * above(part[w][0], most), total += part[w][2];
             if (p.lse) {
                 finish_row(p.loss, row, most, sum, total, p.lse, p.row_loss);
             } else {
@@ -153,43 +152,56 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
 }
 
 // 16 rows a block, 64 lanes of runs: 4096 rows of 782 runs in 256 blocks (32 rows a block took 16.6 us).
+// A row a block (ROWS = 1) where rows are few and their runs many: one row of 8192 runs takes 5 us.
+template <int ROWS>
 __global__ __launch_bounds__(1024) void loss_join_kernel(const LossArgs p, int rows, int runs, float* lse, float* loss)
 {
-    __shared__ float part[16][16][3];
-    for (int64_t first = (int64_t)blockIdx.x * 16; first < rows; first += (int64_t)gridDim.x * 16) {
+    constexpr int LANES = 1024 / ROWS;
+    __shared__ float part[16][ROWS][3];
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < rows; first += (int64_t)gridDim.x * ROWS) {
         const int64_t row = first + threadIdx.x;
         float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
-        auto join_lanes = [&] {                                // lanes 16 apart are a row's
-#pragma unroll
-            for (int o = 16; o < 64; o <<= 1) {
-                join_runs(most, sum, __shfl_xor(most, o), __shfl_xor(sum, o));
-                total += __shfl_xor(total, o);
-            }
-        };
         if (row < rows) {
-#pragma unroll 4
-            for (int r = threadIdx.y; r < runs; r += 64) {
-                const float2 v = reinterpret_cast<const float2*>(p.part)[(int64_t)r * rows + row];
-                join_runs(most, sum, v.x, v.y);
-                if (p.part_z) total += p.part_z[(int64_t)r * rows + row];
+            for (int r0 = threadIdx.y; r0 < runs; r0 += 8 * LANES) {
+                float2 v[8];
+                float top = most;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int64_t at = (int64_t)(r0 + u * LANES) * rows + row;
+                    const bool some = r0 + u * LANES < runs;
+                    v[u] = some ? reinterpret_cast<const float2*>(p.part)[at] : float2{-__builtin_inff(), 0.0f};
+                    if (some && p.part_z) total += p.part_z[at];
+                    top = fmaxf(top, v[u].x);
+                }
+                sum *= above(most, top);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) sum += v[u].y * above(v[u].x, top);
+                most = top;
             }
         }
-        join_lanes();
-        if (threadIdx.y % 4 == 0) {
-            float* to = part[threadIdx.y / 4][threadIdx.x];
-            to[0] = most, to[1] = sum, to[2] = total;
+        // lanes ROWS apart are a row's: their largest first, so that each brings its sum there once
+        float top = most;
+#pragma unroll
+        for (int o = ROWS; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        sum *= above(most, top);
+#pragma unroll
+        for (int o = ROWS; o < 64; o <<= 1) sum += __shfl_xor(sum, o), total += __shfl_xor(total, o);
+        constexpr int PER = 64 / ROWS;                         // a wave's lanes of a row
+        if (threadIdx.y % PER == 0) {
+            float* to = part[threadIdx.y / PER][threadIdx.x];
+            to[0] = top, to[1] = sum, to[2] = total;
         }
         __syncthreads();
-        if (threadIdx.y < 4) {                                 // the first wave: four waves' results a lane
-            const float (*from)[16][3] = part + 4 * threadIdx.y;
-            most = from[0][threadIdx.x][0], sum = from[0][threadIdx.x][1], total = from[0][threadIdx.x][2];
+        if (threadIdx.y == 0 && row < rows) {
+            top = -__builtin_inff(), sum = total = 0.0f;
 #pragma unroll
-            for (int y = 1; y < 4; ++y) {
-                join_runs(most, sum, from[y][threadIdx.x][0], from[y][threadIdx.x][1]);
-                total += from[y][threadIdx.x][2];
+            for (int w = 0; w < 16; ++w) top = fmaxf(top, part[w][threadIdx.x][0]);
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                sum += part[w][threadIdx.x][1] * above(part[w][threadIdx.x][0], top);
+                total += part[w][threadIdx.x][2];
             }
-            join_lanes();
-            if (threadIdx.y == 0 && row < rows) finish_row(p, row, most, sum, total, lse, loss);
+            finish_row(p, row, top, sum, total, lse, loss);
         }
         __syncthreads();
     }
@@ -241,8 +253,12 @@ hipError_t launch_loss_gradient(DType dt, const LossRowsArgs& p, hipStream_t str
 
 hipError_t launch_loss_join(const LossArgs& p, int rows, int runs, float* lse, float* loss, hipStream_t stream)
 {
+    if (rows <= FEW_ROWS) {
+        loss_join_kernel<1><<<rows, dim3(1, 1024), 0, stream>>>(p, rows, runs, lse, loss);
+        return hipGetLastError();
+    }
     const int64_t grid = ((int64_t)rows + 15) / 16;
-    loss_join_kernel<<<(uint32_t)(grid < 1 << 20 ? grid : 1 << 20), dim3(16, 64), 0, stream>>>(p, rows, runs, lse, loss);
+    loss_join_kernel<16><<<(uint32_t)(grid < 1 << 20 ? grid : 1 << 20), dim3(16, 64), 0, stream>>>(p, rows, runs, lse, loss);
     return hipGetLastError();
 }
 

@@ -198,8 +198,10 @@ hipError_t launch_product_fast_grad(Product kind, ProductType type, const Produc
 // LOSS, LOGITS_GRAD, INPUT_SUM and bf16 products with fp32 outputs (linear_fast_loss.hip).
 hipError_t launch_product_fast_loss(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
-// Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them.
+// Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them; and rows: LOGITS_GRAD
+// leaves one column sum for them.
 int loss_columns(ProductType type, FastTile tile);
+int loss_rows(ProductType type, FastTile tile);
 // Rows of `bytes` bytes at any pitch into rows of `to_pitch` (a multiple of 16), zeros behind each (linear_pack.hip).
 constexpr int PACK_JOBS = 3;
 struct PackJob {

@@ -87,9 +87,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const double b_bytes = (double)raw_n * k * k_segments * e, read_us = (b_bytes + (double)m * k * k_segments * e) / kReadPerUs;
     Plan best = {};
     best.us = 1e30;
-    // a loss's epilogues need a row's whole sums, and only the large tiles have them
+    // a loss's epilogues need whole sums, in large tiles or few rows
     const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
-    if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED)) {
+    if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED || kind == Product::LOSS)) {
         best.few = true;
         best.splits = 1;
         // one or two rows on the vector units: faster at every size and alignment measured (4001 x 4093, rows of odd

@@ -235,6 +235,7 @@ struct ProductArgs {
 struct LossProductArgs : ProductArgs {
     LossArgs loss;
     int y_columns;            // EPI_LOGITS_GRAD: y is dz, whose columns up to y_columns are written, zeros past N
+    float* sums;              // its column sums over each wave's rows, or null
     // EPI_SUM: one of several products that add up to y.  Their sum so far, fp32, rows of ld_sum: the first writes it, the
     // last adds to it and writes y instead
     float* sum;
@@ -324,6 +325,28 @@ template <bool EXACT> __device__ __forceinline__ float loss_gradient(const LossR
     return r.counts ? v : 0.0f;
 }
 
+// Statistics of eight logits n..n+7 of row m, as loss_tile.h's of a tile's columns.
+template <bool EXACT> __device__ __forceinline__ void loss_run8(const LossProductArgs& p, int m, int n, float (&z)[8])
+{
+    using In = std::conditional_t<EXACT, float, Bf16>;
+    const int nv = p.N - n, at = loss_column(p.loss, p.loss.target[m]);
+    float bias[8] = {};
+    if (p.bias) load8(static_cast<const In*>(p.bias) + n, nv, bias);
+    float most = -__builtin_inff(), sum = 0.0f, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        z[i] += bias[i];
+        if (i < nv) most = fmaxf(most, z[i]), total += z[i];
+        if (n + i == at) p.loss.hit[m] = z[i];
+    }
+    const float from = most == -__builtin_inff() ? 0.0f : most;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += i < nv ? exponential<EXACT>(z[i] - from) : 0.0f;
+    const int64_t to = (int64_t)(p.loss.part_first + n / 8) * p.M + m;
+    reinterpret_cast<float2*>(p.loss.part)[to] = float2{most, sum};
+    if (p.loss.part_z) p.loss.part_z[to] = total;
+}
+
 // Eight finished columns n..n+7 of row m: v the raw sums (u the second product's).
 template <class Out, int EPI>
 __device__ __forceinline__ void finish8(const ArgsOf<EPI>& p, int m, int n, float (&v)[8], float (&u)[8])
@@ -335,6 +358,11 @@ __device__ __forceinline__ void finish8(const ArgsOf<EPI>& p, int m, int n, floa
         if (r >= p.m_valid || n >= p.N) return;
         Out* y = second ? static_cast<Out*>(p.y2) + (int64_t)r * p.ldy2 : static_cast<Out*>(p.y) + (int64_t)r * p.ldy;
         store8(y + n, p.N - n, v);
+        return;
+    }
+    if constexpr (EPI == EPI_LOSS) {
+        // few rows: eight columns are a run
+        if (m < p.M && n < p.N) loss_run8<EXACT>(p, m, n, v);
         return;
     }
     if constexpr (EPI == EPI_SUM) {

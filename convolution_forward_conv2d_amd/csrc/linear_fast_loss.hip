@@ -30,4 +30,11 @@ int loss_columns(ProductType type, FastTile tile)
     return tile == FastTile::T256x192 ? 96 : tile == FastTile::T128x128 ? 32 : 64;
 }
 
+// BM / WM
+int loss_rows(ProductType type, FastTile tile)
+{
+    if (type == ProductType::F32) return tile == FastTile::T128x128 ? 64 : 32;
+    return tile == FastTile::T256x256 ? 128 : tile == FastTile::T192x256 ? 96 : 64;
+}
+
 }  // namespace miconv

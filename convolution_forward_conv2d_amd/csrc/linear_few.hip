@@ -60,7 +60,7 @@ template <> struct Unpack<1> {
 };
 
 template <int E, class Out, int EPI, int MB>
-__global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const ProductArgs p)
+__global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const ArgsOf<EPI> p)
 {
     constexpr bool GATED = EPI == EPI_GATED;
     constexpr int CHUNK = 1024, U = 2;                         // bytes of a row per load, loads of it per turn
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const ProductArg
 }
 
 template <class Mul, int EPI, int MB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void linear_block_kernel(const ProductArgs p)
+__global__ __launch_bounds__(64 * WAVES) void linear_block_kernel(const ArgsOf<EPI> p)
 {
     constexpr int E = Mul::E, NB = EPI == EPI_GATED ? 2 : 1;
     constexpr int U = 4, TURN = 64 * U;                        // vectors per lane and turn, bytes of a row
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_block_kernel(const ProductA
 // Eight waves a workgroup.  Where they take more than 128 registers (e4m3's widened operands, two row blocks) only one
 // such workgroup runs on a CU, so past one a CU they come in fours: gated 9216 x 4096 on 16 rows in e4m3 22.9 -> 20.9 us,
 // on 32 in bf16 49.9 -> 47.1; with fewer registers eight are faster (bf16 on four rows 33.5, in fours 34.7).
-template <class Mul, int EPI, int MB> void launch_blocks(const ProductArgs& p, int num_cu, hipStream_t stream)
+template <class Mul, int EPI, int MB> void launch_blocks(const ArgsOf<EPI>& p, int num_cu, hipStream_t stream)
 {
     const int grid = (p.N + 15) / 16;
     if constexpr (Mul::E == 1 || MB == 2)
@@ -270,8 +270,9 @@ template <class Mul, int EPI, int MB> void launch_blocks(const ProductArgs& p, i
     linear_block_kernel<Mul, EPI, MB, 8><<<grid, 512, 0, stream>>>(p);
 }
 
-template <class Mul, int EPI> hipError_t launch_rows(const ProductArgs& p, int num_cu, hipStream_t stream)
+template <class Mul, int EPI> hipError_t launch_rows(const ProductArgs& args, int num_cu, hipStream_t stream)
 {
+    const auto& p = static_cast<const ArgsOf<EPI>&>(args);
     using Out = typename Mul::Out;
     constexpr int E = Mul::E, COLS = EPI == EPI_GATED ? WAVES : 2 * WAVES;
     const int rows_grid = (p.N + COLS - 1) / COLS;
@@ -287,6 +288,8 @@ template <class Mul> hipError_t launch_kind(Product kind, const ProductArgs& p, 
 {
     if (kind == Product::FORWARD) return launch_rows<Mul, EPI_LINEAR>(p, num_cu, stream);
     if (kind == Product::GATED) return launch_rows<Mul, EPI_GATED>(p, num_cu, stream);
+    if constexpr (Mul::E > 1)
+        if (kind == Product::LOSS) return launch_rows<Mul, EPI_LOSS>(p, num_cu, stream);
     return hipErrorInvalidValue;
 }
 

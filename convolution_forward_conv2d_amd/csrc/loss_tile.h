@@ -95,7 +95,7 @@ __device__ __forceinline__ void loss_wave(const LossProductArgs& p, Block (&acc)
     }
 }
 
-// The logits' gradient in their place, zeros past N.
+// The logits' gradient in their place, zeros past N; and of each column the sum over the wave's rows, [rows of a wave][column].
 template <bool EXACT, class Block, int FM, int FN>
 __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&acc)[FM][FN], int m0, int j0, int lane)
 {
@@ -106,7 +106,8 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
     const bool cut = j0 + W > p.N;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const LossRow r = loss_row(p.loss, min(m0 + T * i + lane % T, p.M - 1));
+        LossRow r = loss_row(p.loss, min(m0 + T * i + lane % T, p.M - 1));
+        r.counts = r.counts && m0 + T * i + lane % T < p.M;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -116,6 +117,20 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
                 acc[i][j][e] = cut && n >= p.N ? 0.0f : v;
             }
     }
+    if (!p.sums || m0 >= p.M) return;
+    float* sums = p.sums + (int64_t)(m0 / (T * FM)) * p.N;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) s += acc[i][j][e];
+#pragma unroll
+            for (int o = 1; o < T; o <<= 1) s += __shfl_xor(s, o);
+            const int n = j0 + T * j + column_of<T>(e, lane);
+            if (lane % T == 0 && n < p.N) sums[n] = s;
+        }
 }
 
 }  // namespace miconv

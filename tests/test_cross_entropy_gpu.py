@@ -75,8 +75,9 @@ WAYS = [("fused fast 256x256, 1", BF16, 1500, 8200, 64), ("fused fast 256x192, 1
         ("fused fast 128x128, 1", F32, 200, 8200, 64), ("fused fast 128x64, 1", F32, 70, 130, 64),
         ("fused fast 64x128, 1", F32, 129, 8200, 64), ("fused fast 128x128 copies", BF16, 1000, 2000, 71),
         ("fused fast 128x64 copies", F32, 1000, 1001, 65), ("any 64x64 split 4", BF16, 64, 130, 1024),
-        ("fast 128x128 split 4", BF16, 260, 130, 1024), ("fast 64x128 split 8", F32, 64, 2500, 1024), ("few", BF16, 2, 300, 100),
-        ("few", F32, 20, 300, 100)]
+        ("fast 128x128 split 4", BF16, 260, 130, 1024), ("fast 64x128 split 8", F32, 64, 2500, 1024), ("fused few", BF16, 2, 300, 100), ("fused few", BF16, 11, 3001, 100),
+        ("fused few", F32, 20, 300, 100), ("fused few", F32, 1, 9001, 33),
+        ("few", BF16, 16, 517, 2000), ("few", F32, 2, 700, 40)]
 
 
 @pytest.mark.parametrize("way,dtype,m,n,k", WAYS)
