@@ -64,16 +64,16 @@ int gradient_parts(ProductType type, int terms) { return type == ProductType::F3
 
 // A product over all the classes of a piece ends in a round of tiles that leaves most CUs idle.  The classes after its
 // whole rounds of 256 x 256 tiles are then a product of their own, on smaller tiles: the classes of the first, 0 for one
-// product.  WEIGHT_GRAD's classes are its rows, the others' its columns.
+// product.  CLASS_GRAD's classes are its rows, the others' its columns.
 Plan plan_classes(int cus, Product kind, ProductType type, int m, int n, int k)
 {
-    return kind == Product::WEIGHT_GRAD ? plan_product(cus, kind, type, n, k, m, 1, true, true, gradient_parts(type, m))
+    return kind == Product::CLASS_GRAD ? plan_product(cus, kind, type, n, k, m, 1, true, true, gradient_parts(type, m))
                                         : plan_product(cus, kind, type, m, n, k, 1, true, true);
 }
 int cut_of(int cus, Product kind, ProductType type, int m, int n, int k)
 {
     if (type == ProductType::F32) return 0;
-    const int64_t across = ((kind == Product::WEIGHT_GRAD ? k : m) + 255) / 256, rounds = across * ((n + 255) / 256) / cus;
+    const int64_t across = ((kind == Product::CLASS_GRAD ? k : m) + 255) / 256, rounds = across * ((n + 255) / 256) / cus;
     const int64_t first = rounds * cus / across * 256;
     if (first <= 0 || first >= n) return 0;
     const Plan whole = plan_classes(cus, kind, type, m, n, k), a = plan_classes(cus, kind, type, m, (int)first, k),
@@ -176,7 +176,7 @@ Product input_kind(const Way& w, int n) { return w.piece < n ? Product::INPUT_SU
 
 int weight_cut(int cus, const Way& w, ProductType type, int m, int columns, int k)
 {
-    return w.fused ? cut_of(cus, Product::WEIGHT_GRAD, type, m, columns, k) : 0;
+    return w.fused ? cut_of(cus, Product::CLASS_GRAD, type, m, columns, k) : 0;
 }
 
 Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool bias)
@@ -216,7 +216,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
     w.product = over_pieces(n, w.piece, [&](int columns) {
         size_t most = plan_product(cus, input_kind(w, n), type, m, k, columns, 1, true, now.w, gradient_parts(type, columns)).bytes;
         in_cuts(columns, weight_cut(cus, w, type, m, columns, k), [&](int, int classes) {
-            most = std::max(most, plan_product(cus, Product::WEIGHT_GRAD, type, classes, k, m, 1, true, now.x, gradient_parts(type, m)).bytes);
+            most = std::max(most, plan_product(cus, Product::CLASS_GRAD, type, classes, k, m, 1, true, now.x, gradient_parts(type, m)).bytes);
             return MIC_STATUS_SUCCESS;
         });
         if (!w.fused)
@@ -359,6 +359,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
     }
     auto product = [&](int first, int columns) {
         LossProductArgs p = {};
+        p.cus = handle->num_cu;
         p.a = o.x, p.lda = o.ldx;
         p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
         p.M = m, p.N = columns, p.K = k, p.k_segments = 1, p.a_K = o.columns;
@@ -474,6 +475,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
         }
         auto product = [&](int first, int classes) {
             LossProductArgs p = {};
+            p.cus = handle->num_cu;
             p.a = o.x, p.lda = o.ldx;
             p.b = o.w + (int64_t)first * o.ldw, p.ldb = o.ldw;
             p.M = m, p.N = classes, p.K = k, p.k_segments = 1, p.a_K = o.columns;
@@ -525,7 +527,8 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
         }
         if (dw && k)
             MIC_TRY(in_cuts(columns, weight_cut(handle->num_cu, way, type, m, columns, k), [&](int first, int classes) {
-                ProductArgs g = {};
+                LossProductArgs g = {};
+                g.cus = handle->num_cu;
                 g.a = dz + first * (int64_t)e, g.lda = pitch * (int64_t)e;
                 g.b = o.x, g.ldb = o.ldx;
                 g.M = classes, g.N = k, g.K = m, g.b_rows = o.columns;
@@ -534,7 +537,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
                 g.m_pitch = INT32_MAX, g.m_valid = classes;
                 g.y = static_cast<uint8_t*>(dw) + (int64_t)(v + first) * lddw * (int64_t)e, g.ldy = lddw;
                 g.splits = gradient_parts(type, m);
-                return run_product(handle, Product::WEIGHT_GRAD, type, g, space, way.product);
+                return run_product(handle, Product::CLASS_GRAD, type, g, space, way.product);
             }));
     }
     return MIC_STATUS_SUCCESS;

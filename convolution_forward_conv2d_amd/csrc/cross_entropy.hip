@@ -132,7 +132,7 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
             const LossRow row = loss_row(p.loss, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[i] = i < nv ? loss_gradient<EXACT>(row, v[i] + bias[i], c + i, goal, every) : 0.0f;
+                v[i] = i < nv ? loss_gradient<EXACT>(row, v[i] + bias[i], c + i == row.at, goal, every) : 0.0f;
                 total[i] += v[i];
             }
             store8(static_cast<T*>(p.dz) + (int64_t)r * p.dz_pitch + c, 8, v);

@@ -174,8 +174,9 @@ hipError_t launch_bwd_filter_rows(Variant v, const ConvParams& p, hipStream_t st
 // layer, dz W for dx, dz^T x for dW.
 // A classifier's head and its loss: x W^T with each row reduced to its softmax's
 // statistics (LOSS) or turned into the gradient of the loss (LOGITS_GRAD); dz W
-// of one piece of the classes, added to the others' (INPUT_SUM).
-enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD, LOSS, LOGITS_GRAD, INPUT_SUM };
+// of one piece of the classes, added to the others' (INPUT_SUM); dz^T x, many tiles
+// of it one after the other (CLASS_GRAD).
+enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD, LOSS, LOGITS_GRAD, INPUT_SUM, CLASS_GRAD };
 // Operands, and the outputs where they differ; SHORT: e4m3's own matrix
 // instruction (its sums are short, see linear_common.h).
 enum class ProductType : int { F32, BF16, E4M3_BF16, E4M3_F32, E4M3_BF16_SHORT, E4M3_F32_SHORT, BF16_F32 };
@@ -195,7 +196,7 @@ enum class FastTile : int { T256x256, T256x192, T192x256, T256x128, T128x256, T1
 hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs& p, FastTile tile, hipStream_t stream);
 hipError_t launch_product_fast_grad(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
-// LOSS, LOGITS_GRAD, INPUT_SUM and bf16 products with fp32 outputs (linear_fast_loss.hip).
+// LOSS, LOGITS_GRAD, INPUT_SUM, CLASS_GRAD and bf16 products with fp32 outputs (linear_fast_loss.hip).
 hipError_t launch_product_fast_loss(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
 // Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them; and rows: LOGITS_GRAD

@@ -31,7 +31,8 @@ Extent extent_of(Product kind, int m, int n, int k)
     switch (kind) {
     case Product::INPUT_GRAD:
     case Product::INPUT_SUM: return {m, k, k, n};             // dz (m, k), w (k, n)
-    case Product::WEIGHT_GRAD: return {k, m, k, n};            // dz (k, m), x (k, n)
+    case Product::WEIGHT_GRAD:
+    case Product::CLASS_GRAD: return {k, m, k, n};            // dz (k, m), x (k, n)
     default: return {m, k, n, k};
     }
 }
@@ -185,7 +186,8 @@ mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs
 {
     if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
     const int e = element_bytes(type);
-    const bool a_across = kind == Product::WEIGHT_GRAD, b_across = a_across || kind == Product::INPUT_GRAD || kind == Product::INPUT_SUM;
+    const bool a_across = kind == Product::WEIGHT_GRAD || kind == Product::CLASS_GRAD;
+    const bool b_across = a_across || kind == Product::INPUT_GRAD || kind == Product::INPUT_SUM;
     if (p.a_K < p.K) p.a_K = p.K;
     if (p.a_rows < p.M) p.a_rows = p.M;
     if (p.b_rows < p.N) p.b_rows = p.N;

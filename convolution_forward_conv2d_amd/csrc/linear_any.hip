@@ -160,7 +160,8 @@ template <class Mul> hipError_t launch_type(Product kind, const ProductArgs& p, 
     case Product::FORWARD: return launch_one<Mul, false, false, EPI_LINEAR>(p, tile, stream);
     case Product::GATED: return launch_one<Mul, false, false, EPI_GATED>(p, tile, stream);
     case Product::INPUT_GRAD: return launch_one<Mul, false, true, EPI_PLAIN>(p, tile, stream);
-    case Product::WEIGHT_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+    case Product::WEIGHT_GRAD:
+    case Product::CLASS_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
     case Product::INPUT_SUM: return launch_one<Mul, false, true, EPI_SUM>(p, tile, stream);
     default: break;
     }

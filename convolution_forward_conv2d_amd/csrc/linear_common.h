@@ -241,9 +241,10 @@ struct LossProductArgs : ProductArgs {
     float* sum;
     int64_t ld_sum;
     bool sum_first, sum_last;
+    int cus;                  // the device's compute units (linear_chain.h)
 };
 
-enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_LOSS = 3, EPI_LOGITS_GRAD = 4, EPI_SUM = 5 };
+enum Epilogue : int { EPI_PLAIN = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_LOSS = 3, EPI_LOGITS_GRAD = 4, EPI_SUM = 5, EPI_STORE = 6 };
 template <int EPI> using ArgsOf = std::conditional_t<(EPI >= EPI_LOSS), LossProductArgs, ProductArgs>;
 
 // A gated layer's raw columns come in blocks of 32, 16 of the gate's and the
@@ -300,9 +301,9 @@ __device__ __forceinline__ float scaled(float v, Scale a, Scale b)
 // makes both no number; a row of which a bias of -infinity leaves no class has no gradient.
 struct LossRow {
     float lse, gain;
-    int at;                   // the target's column in this product, outside it if it is not there
-    bool counts;
+    int at;                   // the target's column in this product, outside it if it is not there; NO_GRADIENT
 };
+constexpr int NO_GRADIENT = INT32_MIN;
 __device__ __forceinline__ int loss_column(const LossArgs& p, int64_t target)
 {
     return target >= 0 && target < p.classes ? (int)target - p.first : -1;
@@ -312,17 +313,16 @@ __device__ __forceinline__ LossRow loss_row(const LossArgs& p, int m)
     const int64_t target = p.target[m];
     LossRow r;
     r.lse = p.lse[m];
-    r.counts = target != p.ignore && r.lse != -__builtin_inff();
     r.gain = p.dloss[p.dloss_rows ? m : 0];
     if (p.count) r.gain = *p.count > 0.0f ? r.gain / *p.count : 0.0f;
     if (target < 0 || target >= p.classes) r.gain = __builtin_nanf("");
-    r.at = loss_column(p, target);
+    r.at = target == p.ignore || r.lse == -__builtin_inff() ? NO_GRADIENT : loss_column(p, target);
     return r;
 }
-template <bool EXACT> __device__ __forceinline__ float loss_gradient(const LossRow& r, float z, int n, float goal, float every)
+template <bool EXACT> __device__ __forceinline__ float loss_gradient(const LossRow& r, float z, bool hit, float goal, float every)
 {
-    const float v = (exponential<EXACT>(z - r.lse) - (n == r.at ? goal : every)) * r.gain;
-    return r.counts ? v : 0.0f;
+    const float v = (exponential<EXACT>(z - r.lse) - (hit ? goal : every)) * r.gain;
+    return r.at != NO_GRADIENT ? v : 0.0f;
 }
 
 // Statistics of eight logits n..n+7 of row m, as loss_tile.h's of a tile's columns.
@@ -375,10 +375,6 @@ __device__ __forceinline__ void finish8(const ArgsOf<EPI>& p, int m, int n, floa
         }
         if (p.sum_last) store8(static_cast<Out*>(p.y) + (int64_t)m * p.ldy + n, p.N - n, v);
         else store8(sum, p.N - n, v);
-        return;
-    }
-    if constexpr (EPI == EPI_LOGITS_GRAD) {
-        if (m < p.M && n < p.y_columns) store8(static_cast<Out*>(p.y) + (int64_t)m * p.ldy + n, 8, v);
         return;
     }
     if (m >= p.M || n >= p.N) return;

@@ -30,7 +30,6 @@
 #include <type_traits>
 
 #include "linear_tile.h"
-#include "loss_tile.h"
 #include "kernels.h"
 
 namespace miconv {
@@ -256,13 +255,8 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_fast_kernel(const Args
         }
         landed<0>();
     }
-    if constexpr (EPI == EPI_LOSS) {
-        loss_wave<E == 4>(p, acc, m0 + wm, j0 + wn, lane);
-    } else {
-        if constexpr (EPI == EPI_LOGITS_GRAD) gradient_wave<E == 4>(p, acc, m0 + wm, j0 + wn, lane);
-        finish_wave<typename Mul::Out, EPI>(p, reinterpret_cast<float*>(smem) + wave * 32 * (T * FN + 4), acc,
-                                                    m0 + wm, j0 + wn, blockIdx.z, lane);
-    }
+    finish_wave<typename Mul::Out, EPI>(p, reinterpret_cast<float*>(smem) + wave * 32 * (T * FN + 4), acc,
+                                                m0 + wm, j0 + wn, blockIdx.z, lane);
 }
 
 }  // namespace miconv

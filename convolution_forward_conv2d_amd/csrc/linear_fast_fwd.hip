@@ -7,7 +7,7 @@ hipError_t launch_product_fast(Product kind, ProductType type, const ProductArgs
 {
     if (kind == Product::INPUT_GRAD || kind == Product::WEIGHT_GRAD)
         return launch_product_fast_grad(kind, type, p, tile, stream);
-    if (kind == Product::LOSS || kind == Product::LOGITS_GRAD || kind == Product::INPUT_SUM || type == ProductType::BF16_F32)
+    if ((kind != Product::FORWARD && kind != Product::GATED) || type == ProductType::BF16_F32)
         return launch_product_fast_loss(kind, type, p, tile, stream);
     const bool gated = kind == Product::GATED;
     switch (type) {

@@ -2,33 +2,36 @@
 // loss's gradient, without passing through memory.
 //
 // The wave holds FM x FN blocks of T rows x T columns: lane l has row l % T of
-// each, and of its columns those that column_of() says.
+// each; its value e of block j is column j0 + lane_column() + column_of(j, e).
+// Rows are taken one after the other and compared by the distance from the
+// lane's first column, against constants: masks of all columns at once, and all
+// rows' values, would not fit the registers beside a tile's sums.
 #pragma once
 
 #include "linear_common.h"
 
 namespace miconv {
 
-// Column in a block of value e of lane l.
-template <int T> __device__ __forceinline__ int column_of(int e, int lane)
-{
-    return T == 32 ? 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) : 4 * (lane >> 4) + e;
-}
+template <int T> __device__ __forceinline__ int lane_column(int lane) { return 4 * (lane / T); }
+template <int T> __device__ constexpr int column_of(int j, int e) { return T * j + (T == 32 ? 8 * (e >> 2) + (e & 3) : e); }
 
 template <class In, class Block, int FM, int FN>
 __device__ __forceinline__ void add_bias(const ProductArgs& p, Block (&acc)[FM][FN], int j0, int lane)
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, V = sizeof(Block) / 4;
     if (!p.bias) return;
+    const int n0 = j0 + lane_column<T>(lane), left = p.N - n0;
+    const In* bias = static_cast<const In*>(p.bias) + n0;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+    for (int j = 0; j < FN; ++j) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const int n = j0 + T * j + column_of<T>(e, lane);
-            const float b = n < p.N ? to_f32(static_cast<const In*>(p.bias)[n]) : 0.0f;
+            const float b = column_of<T>(j, e) < left ? to_f32(bias[column_of<T>(j, e)]) : 0.0f;
 #pragma unroll
             for (int i = 0; i < FM; ++i) acc[i][j][e] += b;
         }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // Each row's largest logit of these columns and the sum of e^(z - largest), [run][row]: run = the wave's columns; with
@@ -38,22 +41,24 @@ __device__ __forceinline__ void loss_wave(const LossProductArgs& p, Block (&acc)
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, V = sizeof(Block) / 4, W = T * FN;
     using In = typename std::conditional<EXACT, float, Bf16>::type;
-    if (j0 >= p.N) return;
+    if (j0 >= p.N || m0 >= p.M) return;
     add_bias<In>(p, acc, j0, lane);
-    const bool cut = j0 + W > p.N;
     const float least = -__builtin_inff();
-    const int64_t run = p.loss.part_first + j0 / W;
+    const int n0 = j0 + lane_column<T>(lane), left = p.N - n0;
+    const int64_t run = (int64_t)(p.loss.part_first + j0 / W) * p.M;
+    int at[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) at[i] = loss_column(p.loss, p.loss.target[min(m0 + T * i + lane % T, p.M - 1)]);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + T * i + lane % T;
-        if (m0 + T * i >= p.M) break;
-        const int at = m < p.M ? loss_column(p.loss, p.loss.target[m]) : -1;
-        if (at >= j0 && at < j0 + W) {
+        if (at[i] >= j0 && at[i] < j0 + W && m < p.M) {
+            const int here = at[i] - n0;
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    if (j0 + T * j + column_of<T>(e, lane) == at) p.loss.hit[m] = acc[i][j][e];
+                    if (here == column_of<T>(j, e)) p.loss.hit[m] = acc[i][j][e];
         }
         float sum_z = 0.0f;
         if (p.loss.part_z) {
@@ -64,12 +69,12 @@ __device__ __forceinline__ void loss_wave(const LossProductArgs& p, Block (&acc)
 #pragma unroll
             for (int o = T; o < 64; o <<= 1) sum_z += __shfl_xor(sum_z, o);
         }
-        if (cut) {
+        if (j0 + W > p.N) {
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    if (j0 + T * j + column_of<T>(e, lane) >= p.N) acc[i][j][e] = least;
+                    if (column_of<T>(j, e) >= left) acc[i][j][e] = least;
         }
         float most = least;
 #pragma unroll
@@ -88,10 +93,10 @@ __device__ __forceinline__ void loss_wave(const LossProductArgs& p, Block (&acc)
 #pragma unroll
         for (int o = T; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
         if (lane < T && m < p.M) {
-            const int64_t to = run * p.M + m;
-            reinterpret_cast<float2*>(p.loss.part)[to] = float2{most, sum};
-            if (p.loss.part_z) p.loss.part_z[to] = sum_z;
+            reinterpret_cast<float2*>(p.loss.part)[run + m] = float2{most, sum};
+            if (p.loss.part_z) p.loss.part_z[run + m] = sum_z;
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -101,24 +106,36 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
 {
     constexpr int T = sizeof(Block) == sizeof(f32x16) ? 32 : 16, V = sizeof(Block) / 4, W = T * FN;
     using In = typename std::conditional<EXACT, float, Bf16>::type;
+    if (m0 >= p.M) return;
     add_bias<In>(p, acc, j0, lane);
     const float every = p.loss.smooth / (float)p.loss.classes, goal = 1.0f - p.loss.smooth + every;
-    const bool cut = j0 + W > p.N;
+    const int n0 = j0 + lane_column<T>(lane), left = p.N - n0;
+    LossRow rows[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        LossRow r = loss_row(p.loss, min(m0 + T * i + lane % T, p.M - 1));
-        r.counts = r.counts && m0 + T * i + lane % T < p.M;
+        const int m = m0 + T * i + lane % T;
+        rows[i] = loss_row(p.loss, min(m, p.M - 1));
+        if (m >= p.M) rows[i].at = NO_GRADIENT;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int here = rows[i].at - n0;                      // NO_GRADIENT wraps to no column
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int n = j0 + T * j + column_of<T>(e, lane);
-                const float v = loss_gradient<EXACT>(r, acc[i][j][e], n, goal, every);
-                acc[i][j][e] = cut && n >= p.N ? 0.0f : v;
-            }
+            for (int e = 0; e < V; ++e)
+                acc[i][j][e] = loss_gradient<EXACT>(rows[i], acc[i][j][e], here == column_of<T>(j, e), goal, every);
+        if (j0 + W > p.N) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (column_of<T>(j, e) >= left) acc[i][j][e] = 0.0f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    if (!p.sums || m0 >= p.M) return;
-    float* sums = p.sums + (int64_t)(m0 / (T * FM)) * p.N;
+    if (!p.sums) return;
+    float* sums = p.sums + (int64_t)(m0 / (T * FM)) * p.N + n0;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -128,8 +145,8 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
             for (int i = 0; i < FM; ++i) s += acc[i][j][e];
 #pragma unroll
             for (int o = 1; o < T; o <<= 1) s += __shfl_xor(s, o);
-            const int n = j0 + T * j + column_of<T>(e, lane);
-            if (lane % T == 0 && n < p.N) sums[n] = s;
+            if (lane % T == 0 && column_of<T>(j, e) < left) sums[column_of<T>(j, e)] = s;
+            __builtin_amdgcn_sched_barrier(0);
         }
 }
 
