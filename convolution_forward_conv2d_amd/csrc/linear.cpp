@@ -90,7 +90,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     best.us = 1e30;
     // a loss's epilogues need whole sums, in large tiles or few rows
     const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
-    if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED || kind == Product::LOSS)) {
+    // (a loss of more classes than a grid of 16 to a workgroup reaches goes on tiles)
+    const bool few_loss = kind == Product::LOSS && n < 1 << 26;
+    if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED || few_loss)) {
         best.few = true;
         best.splits = 1;
         // one or two rows on the vector units: faster at every size and alignment measured (4001 x 4093, rows of odd

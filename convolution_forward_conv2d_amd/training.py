@@ -7,6 +7,7 @@ workspaces as torch allocations on that stream, rows at any pitch and
 alignment, contiguous arguments that fit each other through ``_native.so``.
 """
 import collections
+import operator
 
 import torch
 
@@ -35,6 +36,12 @@ def _per_row(t, rows, device, what):
     if t.dtype != torch.float32 or t.device != device or t.numel() != rows or not t.is_contiguous():
         raise ValueError("%s must be %d packed fp32 values on %s" % (what, rows, device))
     return t.data_ptr()
+
+
+def _whole(v, name):
+    if isinstance(v, (bool, torch.Tensor)) or not hasattr(v, "__index__"):
+        raise TypeError("%s must be a whole number, got %s" % (name, type(v).__name__))
+    return operator.index(v)
 
 
 # ---------------------------------------------------------------- norm
@@ -129,9 +136,8 @@ def _drop(x, p, seed, offset, residual, what):
         if seed.dtype != torch.int64 or seed.device != device or seed.shape != (2,) or not seed.is_contiguous():
             raise ValueError("seed must be a number, or two packed int64 values on %s" % device)
         state, seed = seed.data_ptr(), 0
+    seed, offset = _whole(seed, "seed"), _whole(offset, "offset")
     for name, v in (("seed", seed), ("offset", offset)):
-        if isinstance(v, bool) or not isinstance(v, int):
-            raise TypeError("%s must be a whole number, got %s" % (name, type(v).__name__))
         if not 0 <= v < 1 << 64:
             raise ValueError("%s must be from 0 to 2^64 - 1, got %d" % (name, v))
     if residual is not None:
@@ -198,8 +204,7 @@ def _smoothing(label_smoothing):
 
 
 def _ignored(ignore_index):
-    if isinstance(ignore_index, bool) or not isinstance(ignore_index, int):
-        raise TypeError("ignore_index must be a whole number, got %s" % type(ignore_index).__name__)
+    ignore_index = _whole(ignore_index, "ignore_index")
     if not -1 << 63 <= ignore_index < 1 << 63:
         raise ValueError("ignore_index does not fit int64")
     return ignore_index

@@ -294,9 +294,52 @@ def test_nothing():
     dx, dw, db = mic.linear_cross_entropy_backward(torch.ones((), device=DEV), x, w, target, r.lse, bias=b, count=r.count)
     assert dx.shape == (0, 16) and dw.shape == (10, 16) and not dw.any() and not db.any()
     # no features: the bias alone
-    x0, w0 = torch.zeros(3, 0, device=DEV), torch.zeros(10, 0, device=DEV)
-    got = mic.linear_cross_entropy(x0, w0, torch.tensor([0, 3, 9], device=DEV), bias=b, reduction="none")
-    T.check(got.loss, T.cross_entropy(x0, w0, b, torch.tensor([0, 3, 9], device=DEV), "none")["loss"], "loss")
+    for m in (3, 70):
+        x0, w0, t = torch.zeros(m, 0, device=DEV), torch.zeros(10, 0, device=DEV), classes(4, m, 10)
+        got = mic.linear_cross_entropy(x0, w0, t, bias=b, reduction="none")
+        T.check(got.loss, T.cross_entropy(x0, w0, b, t, "none")["loss"], "loss")
+        dx, dw, db = mic.linear_cross_entropy_backward(torch.ones(m, device=DEV), x0, w0, t, got.lse, bias=b)
+        assert dx.shape == (m, 0) and dw.shape == (10, 0)
+        T.check(db, T.cross_entropy_backward(torch.ones(m, device=DEV), x0, w0, b, t, got.lse, None)[2], "dbias")
+    # a single row without a leading dimension
+    x1, w1 = values(5, 16), values(6, 10, 16)
+    one = mic.linear_cross_entropy(x1, w1, torch.tensor(7, device=DEV), reduction="none")
+    assert one.loss.shape == () and torch.equal(one.loss, mic.linear_cross_entropy(x1[None], w1, torch.tensor([7], device=DEV)).loss)
+    g = mic.linear_cross_entropy_backward(torch.ones((), device=DEV), x1, w1, torch.tensor(7, device=DEV), one.lse)
+    assert g[0].shape == (16,) and g[1].shape == (10, 16)
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, and from two threads, have workspaces of their own."""
+    import threading
+
+    x, w = [values(s, 300, 128, dtype=BF16) for s in (1, 2)], values(3, 3000, 128, std=0.2, dtype=BF16)
+    target = classes(4, 300, 3000)
+    one = torch.ones((), device=DEV)
+
+    def step(x):
+        r = mic.linear_cross_entropy(x, w, target)
+        return (r.loss, r.lse) + mic.linear_cross_entropy_backward(one, x, w, target, r.lse, count=r.count)[:2]
+
+    want = [step(v) for v in x]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got[i] = step(x[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, e in zip(got, want):
+        for a, b in zip(g, e):
+            assert torch.equal(a, b)
 
 
 def test_refusals():

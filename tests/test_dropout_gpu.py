@@ -94,6 +94,7 @@ def test_share_and_independence():
 
 def test_seed_in_device_memory():
     x = values(1, 300, 40)
+    assert torch.equal(mic.dropout(x, np.float32(0.5), np.int64(7), offset=np.int32(3)), mic.dropout(x, 0.5, 7, offset=3))
     state = torch.tensor([77, 1000], device=DEV)
     assert torch.equal(mic.dropout(x, 0.4, state, offset=5), mic.dropout(x, 0.4, 77, offset=1005))
     assert torch.equal(mic.dropout_backward(x, 0.4, state, offset=5), mic.dropout_backward(x, 0.4, 77, offset=1005))
