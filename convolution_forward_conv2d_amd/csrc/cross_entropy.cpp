@@ -171,9 +171,6 @@ int sum_groups(int cus, ProductType type, int m, int classes, int k)
     return (m + rows - 1) / rows;
 }
 
-// The product that makes dx, or a piece of it.
-Product input_kind(const Way& w, int n) { return w.piece < n ? Product::INPUT_SUM : Product::INPUT_GRAD; }
-
 int weight_cut(int cus, const Way& w, ProductType type, int m, int columns, int k)
 {
     return w.fused ? cut_of(cus, Product::CLASS_GRAD, type, m, columns, k) : 0;
@@ -214,7 +211,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
         w.logits = (size_t)align_up((int64_t)m * w.ld_logits * 4, 256);
     }
     w.product = over_pieces(n, w.piece, [&](int columns) {
-        size_t most = plan_product(cus, input_kind(w, n), type, m, k, columns, 1, true, now.w, gradient_parts(type, columns)).bytes;
+        size_t most = plan_product(cus, Product::INPUT_SUM, type, m, k, columns, 1, true, now.w, gradient_parts(type, columns)).bytes;
         in_cuts(columns, weight_cut(cus, w, type, m, columns, k), [&](int, int classes) {
             most = std::max(most, plan_product(cus, Product::CLASS_GRAD, type, classes, k, m, 1, true, now.x, gradient_parts(type, m)).bytes);
             return MIC_STATUS_SUCCESS;
@@ -523,7 +520,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             g.y = dx, g.ldy = lddx;
             g.splits = gradient_parts(type, columns);
             g.sum = sum, g.ld_sum = align_up(k, 8), g.sum_first = v == 0, g.sum_last = v + columns == n;
-            MIC_TRY(run_product(handle, input_kind(way, n), type, g, space, way.product));
+            MIC_TRY(run_product(handle, Product::INPUT_SUM, type, g, space, way.product));
         }
         if (dw && k)
             MIC_TRY(in_cuts(columns, weight_cut(handle->num_cu, way, type, m, columns, k), [&](int first, int classes) {

@@ -174,8 +174,8 @@ hipError_t launch_bwd_filter_rows(Variant v, const ConvParams& p, hipStream_t st
 // layer, dz W for dx, dz^T x for dW.
 // A classifier's head and its loss: x W^T with each row reduced to its softmax's
 // statistics (LOSS) or turned into the gradient of the loss (LOGITS_GRAD); dz W
-// of one piece of the classes, added to the others' (INPUT_SUM); dz^T x, many tiles
-// of it one after the other (CLASS_GRAD).
+// of all the classes, or of a piece of them added to the others' (INPUT_SUM); dz^T
+// x, many tiles of it one after the other (CLASS_GRAD).
 enum class Product : int { FORWARD, GATED, INPUT_GRAD, WEIGHT_GRAD, LOSS, LOGITS_GRAD, INPUT_SUM, CLASS_GRAD };
 // Operands, and the outputs where they differ; SHORT: e4m3's own matrix
 // instruction (its sums are short, see linear_common.h).

@@ -90,6 +90,7 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     best.us = 1e30;
     // a loss's epilogues need whole sums, in large tiles or few rows
     const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
+    const bool of_loss = kind >= Product::LOSS || type == ProductType::BF16_F32;
     // (a loss of more classes than a grid of 16 to a workgroup reaches goes on tiles)
     const bool few_loss = kind == Product::LOSS && n < 1 << 26;
     if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED || few_loss)) {
@@ -106,8 +107,10 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     auto consider = [&](Plan pl, int64_t t, int bm, int bn, int slots, double step, double tile) {
         // HIP takes grids of fewer than 2^32 threads: 2^30 rows of 64 x 64 are past that
         if (t * (pl.fast ? 512 : 256) >= int64_t(1) << 32) return;
-        // weights that one or two row tiles read come from memory at its latency, two steps in flight
-        if (m <= 2 * bm) step = std::max(step, 0.9);
+        // weights that one or two row tiles read come from memory at its latency, two steps in flight; a loss's products
+        // price it by the tile: a CU takes about 46 KB a microsecond, and a step 0.72 (256 x 4096 of 1000 terms, dx of a
+        // small classifier: 256 x 128 18.5 us, 128 x 128 and 64 x 64 14)
+        if (m <= 2 * bm) step = std::max(step, of_loss ? std::max(0.72, (bm + bn) * 128 / 46.0e3) : 0.9);
         const int most = whole ? 1 : std::max(least_splits, most_splits(t));
         for (int s = least_splits; s <= most; ++s) {
             const double us = std::max(rounds(t * s, slots) * ((steps + s - 1) / s * step + tile), read_us) + join_us(s) + pl.us + 1.5;

@@ -69,12 +69,13 @@ def test_sizes(m, n, k, dtype):
 # sizes that reach each way of the logits: every tile they stay in, both ways through memory, split sums, copies of
 # unaligned rows (the name holds for aligned operands where k allows)
 WAYS = [("fused fast 256x256, 1", BF16, 1500, 8200, 64), ("fused fast 256x192, 1", BF16, 1000, 8200, 64),
-        ("fused fast 192x256, 1", BF16, 515, 20011, 40), ("fused fast 256x128, 1", BF16, 200, 2500, 64),
+        ("fused fast 192x256, 1", BF16, 515, 20011, 40), ("fused fast 256x128, 1", BF16, 129, 20011, 40),
         ("fused fast 128x256, 1", BF16, 770, 8200, 64), ("fused fast 128x128, 1", BF16, 260, 135, 256),
         ("fused fast 256x256 + fast 128x128, 1", BF16, 1024, 17003, 1024),
         ("fused fast 128x128, 1", F32, 200, 8200, 64), ("fused fast 128x64, 1", F32, 70, 130, 64),
         ("fused fast 64x128, 1", F32, 129, 8200, 64), ("fused fast 128x128 copies", BF16, 1000, 2000, 71),
-        ("fused fast 128x64 copies", F32, 1000, 1001, 65), ("any 64x64 split 4", BF16, 64, 130, 1024),
+        ("fused fast 128x64 copies", F32, 1000, 1001, 65), ("any 64x64 split 4", BF16, 33, 130, 1001), ("any 64x64", BF16, 33, 130, 33),
+        ("any 128x128 split 8", BF16, 200, 2500, 2047), ("fast 128x64 split 8 pack a pack b", F32, 33, 130, 1001),
         ("fast 128x128 split 4", BF16, 260, 130, 1024), ("fast 64x128 split 8", F32, 64, 2500, 1024), ("fused few", BF16, 2, 300, 100), ("fused few", BF16, 11, 3001, 100),
         ("fused few", F32, 20, 300, 100), ("fused few", F32, 1, 9001, 33),
         ("few", BF16, 16, 517, 2000), ("few", F32, 2, 700, 40)]
