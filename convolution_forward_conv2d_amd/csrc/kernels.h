@@ -199,6 +199,8 @@ hipError_t launch_product_fast_grad(Product kind, ProductType type, const Produc
 // LOSS, LOGITS_GRAD, INPUT_SUM, CLASS_GRAD and bf16 products with fp32 outputs (linear_fast_loss.hip).
 hipError_t launch_product_fast_loss(Product kind, ProductType type, const ProductArgs& p, FastTile tile,
                                     hipStream_t stream);
+// A whole INPUT_SUM and CLASS_GRAD in one launch, on 128 x 128 tiles.
+hipError_t launch_product_pair(ProductType type, const ProductArgs& dx, const ProductArgs& dw, hipStream_t stream);
 // Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them; and rows: LOGITS_GRAD
 // leaves one column sum for them.
 int loss_columns(ProductType type, FastTile tile);

@@ -187,15 +187,28 @@ void describe(const Plan& pl, char* text, size_t size)
 
 static bool fast_rows(const uint8_t* p, int64_t ld, int64_t bytes) { return aligned_matrix(p, ld) && bytes % 16 == 0; }
 
+// The lengths a product's operands are padded to, where the caller has not said more.
+static void fill(ProductArgs& p)
+{
+    if (p.a_K < p.K) p.a_K = p.K;
+    if (p.a_rows < p.M) p.a_rows = p.M;
+    if (p.b_rows < p.N) p.b_rows = p.N;
+}
+
+mic_status run_pair(mic_handle h, ProductType type, ProductArgs& dx, ProductArgs& dw)
+{
+    fill(dx);
+    fill(dw);
+    return launched(launch_product_pair(type, dx, dw, h->stream));
+}
+
 mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes, Sums* sums)
 {
     if (p.M == 0 || p.N == 0) return MIC_STATUS_SUCCESS;
     const int e = element_bytes(type);
     const bool a_across = kind == Product::WEIGHT_GRAD || kind == Product::CLASS_GRAD;
     const bool b_across = a_across || kind == Product::INPUT_GRAD || kind == Product::INPUT_SUM;
-    if (p.a_K < p.K) p.a_K = p.K;
-    if (p.a_rows < p.M) p.a_rows = p.M;
-    if (p.b_rows < p.N) p.b_rows = p.N;
+    fill(p);
     const bool two_b = kind == Product::GATED || p.k_segments > 1;
     bool aligned_a = fast_rows(p.a, p.lda, (int64_t)(a_across ? p.a_rows : p.a_K) * e);
     const int64_t b_bytes = (int64_t)(b_across ? p.b_rows : p.a_K) * e;

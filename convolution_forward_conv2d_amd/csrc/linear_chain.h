@@ -73,13 +73,15 @@ __device__ __forceinline__ void store_wave(Out* y, int64_t ld, int rows, int col
     }
 }
 
+template <int BM, int BN> constexpr int chain_lds() { return (3 * BM + 2 * BN) * 128; }
+
+// Tiles `start`, start + hop, ... of the product.
 template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const LossProductArgs p)
+__device__ __forceinline__ void chain(const LossProductArgs& p, uint8_t* smem, int start, int hop)
 {
     static_assert(WM * WN == 8 && BM % (32 * WM) == 0 && BN % (32 * WN) == 0, "eight waves of 32 x 32 blocks");
     constexpr int E = Mul::E, BK = 128 / E, T = Mul::T, FM = BM / WM / T, FN = BN / WN / T;
-    constexpr int A_TILE = BM * 128, B_TILE = BN * 128, LDS = 3 * A_TILE + 2 * B_TILE;
-    __shared__ __align__(1024) uint8_t smem[LDS];
+    constexpr int A_TILE = BM * 128, B_TILE = BN * 128;
 
     const int mt = (p.M + BM - 1) / BM, nt = (p.N + BN - 1) / BN, total = mt * nt;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -100,12 +102,12 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const Los
     };
     uint8_t* const b_tiles = smem + 3 * A_TILE;
     // the tile and step of A or B whose loads come next
-    int id_a = blockIdx.x, id_b = blockIdx.x, next_a = 0, next_b = 0;
+    int id_a = start, id_b = start, next_a = 0, next_b = 0;
     start_a(id_a);
     start_b(id_b);
     auto turn_a = [&] {
         if (next_a == steps) {
-            next_a = 0, id_a += gridDim.x;
+            next_a = 0, id_a += hop;
             if (id_a < total) start_a(id_a);
         }
         sa.next(id_a < total);
@@ -113,7 +115,7 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const Los
     };
     auto turn_b = [&] {
         if (next_b == steps) {
-            next_b = 0, id_b += gridDim.x;
+            next_b = 0, id_b += hop;
             if (id_b < total) start_b(id_b);
         }
         sb.next(id_b < total);
@@ -165,7 +167,7 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const Los
     int a0 = 0, a1 = A_TILE, a2 = 2 * A_TILE;                  // A of this step and the two after it
     int b0 = 0, b1 = B_TILE;
     turn_a();
-    for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    for (int id = start; id < total; id += hop) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -192,6 +194,23 @@ __global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const Los
         }
     }
     landed<0>();
+}
+
+template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(FAST_THREADS, 2) void linear_chain_kernel(const LossProductArgs p)
+{
+    __shared__ __align__(1024) uint8_t smem[chain_lds<BM, BN>()];
+    chain<Mul, AACROSS, BACROSS, EPI, BM, BN, WM, WN>(p, smem, blockIdx.x, gridDim.x);
+}
+
+// dx and dw side by side: `first` workgroups on dz W, the others on dz^T x.
+template <class Mul, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(FAST_THREADS, 2) void linear_pair_kernel(const LossProductArgs dx, const LossProductArgs dw, int first)
+{
+    __shared__ __align__(1024) uint8_t smem[chain_lds<BM, BN>()];
+    const int id = blockIdx.x;
+    if (id < first) chain<Mul, false, true, EPI_STORE, BM, BN, WM, WN>(dx, smem, id, first);
+    else chain<Mul, true, true, EPI_STORE, BM, BN, WM, WN>(dw, smem, id - first, gridDim.x - first);
 }
 
 }  // namespace miconv

@@ -64,6 +64,21 @@ hipError_t launch_product_fast_loss(Product kind, ProductType type, const Produc
     return hipErrorInvalidValue;
 }
 
+hipError_t launch_product_pair(ProductType type, const ProductArgs& dx, const ProductArgs& dw, hipStream_t stream)
+{
+    const auto& a = static_cast<const LossProductArgs&>(dx);
+    const auto& b = static_cast<const LossProductArgs&>(dw);
+    auto tiles = [](const ProductArgs& p) { return (uint32_t)((p.M + 127) / 128) * ((p.N + 127) / 128); };
+    const uint32_t first = tiles(a), grid = first + tiles(b);
+    if (type == ProductType::BF16)
+        linear_pair_kernel<MulBf16, 128, 128, 2, 4><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
+    else if (type == ProductType::F32)
+        linear_pair_kernel<MulF32, 128, 128, 2, 4><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
+    else
+        return hipErrorInvalidValue;
+    return hipGetLastError();
+}
+
 // BN / WN of launch_one's tiles
 int loss_columns(ProductType type, FastTile tile)
 {

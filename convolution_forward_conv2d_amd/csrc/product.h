@@ -54,6 +54,9 @@ struct Sums {
 mic_status run_product(mic_handle h, Product kind, ProductType type, ProductArgs& p, void* workspace, size_t bytes,
                        Sums* sums = nullptr);
 
+// Runs a cross entropy's dx and dw in one launch, on operands that are aligned.
+mic_status run_pair(mic_handle h, ProductType type, ProductArgs& dx, ProductArgs& dw);
+
 inline mic_status give_name(const char* text, char* buf, size_t buflen)
 {
     const size_t len = strlen(text);
