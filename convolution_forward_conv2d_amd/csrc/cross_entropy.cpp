@@ -41,6 +41,27 @@ Rows rows_of(ProductType type, int k, bool x, bool w)
     return {x && even, w && even};
 }
 
+// Logits that pass through memory: the parts that their reduction is cut into, at the least.  Tiles of fp32 are slow, and a
+// few more of them than the CUs are two rounds, the second all but empty; parts past what a product's own plan allows even
+// the rounds out.  33184 classes, 260 tiles: of 3920 features 48 rows 273 -> 202 us, 128 rows 392 -> 323, of 2050
+// features, whose rows whole tiles would copy, 48 rows 271 -> 124.  (Calls under a billion terms, some 30 us, are
+// not worth the search.)
+int logits_parts(int cus, ProductType type, int m, int n, int k, Rows rows)
+{
+    if (type != ProductType::F32 || (double)m * n * k < 1e9) return 1;
+    int parts = 1;
+    double us = 1e30;
+    for (int s = 1; s <= 8 && s <= k / 128; ++s) {
+        const Plan pl = plan_product(cus, Product::FORWARD, type, m, n, k, 1, rows.x, rows.w, s);
+        if (pl.us < us) us = pl.us, parts = s;
+    }
+    return parts;
+}
+Plan plan_logits(int cus, ProductType type, int m, int n, int k, Rows rows)
+{
+    return plan_product(cus, Product::FORWARD, logits_type(type), m, n, k, 1, rows.x, rows.w, logits_parts(cus, type, m, n, k, rows));
+}
+
 // A product over aligned copies of operands that are not: the whole of x once, w a piece at a time.
 struct Copies {
     int64_t pitch;                                             // bytes, 0: none
@@ -137,7 +158,7 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     const Plan few = plan_product(cus, Product::LOSS, type, m, n, k, 1, rows.x && rows.w, rows.x && rows.w);
     if (few.few && few.us <= fused.plan.us + fused.copies.us) fused.plan = few, fused.copies = {};
     memory.piece = piece_of(kLogitsBytes, m, n, 4);
-    memory.plan = plan_product(cus, Product::FORWARD, logits_type(type), m, memory.piece, k, 1, rows.x, rows.w);
+    memory.plan = plan_logits(cus, type, m, memory.piece, k, rows);
     const double pieces = (n + memory.piece - 1) / memory.piece;
     const double fused_us = fused.plan.us + fused.copies.us + 2.0 * m * ((n + 63) / 64) * 8 / kBytesPerUs;
     const double memory_us = pieces * (memory.plan.us + kLaunchUs) + 2.0 * m * (double)n * 4 / kBytesPerUs;
@@ -155,7 +176,7 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
         w.ld_logits = align_up(w.piece, 4);
         w.logits = (size_t)align_up((int64_t)m * w.ld_logits * 4, 256);
         w.product = over_pieces(n, w.piece, [&](int columns) {
-            return plan_product(cus, Product::FORWARD, logits_type(type), m, columns, k, 1, rows.x, rows.w).bytes;
+            return plan_logits(cus, type, m, columns, k, rows).bytes;
         });
         w.product = (size_t)align_up(w.product, 256);
     }
@@ -184,7 +205,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
     fused.piece = memory.piece = piece_of(kGradientBytes, m, n, e);
     fused.copies = copies_of(type, m, n, fused.piece, k, rows);
     fused.plan = plan_product(cus, Product::LOGITS_GRAD, type, m, fused.piece, k, 1, true, true);
-    memory.plan = plan_product(cus, Product::FORWARD, logits_type(type), m, memory.piece, k, 1, rows.x, rows.w);
+    memory.plan = plan_logits(cus, type, m, memory.piece, k, rows);
     const double pieces = (n + fused.piece - 1) / fused.piece;
     const double fused_us = pieces * (fused.plan.us + (bias ? kLaunchUs : 0.0)) + fused.copies.us;
     const double memory_us = pieces * (memory.plan.us + kLaunchUs) + (double)m * n * (8 + e) / kBytesPerUs;
@@ -217,7 +238,7 @@ Way backward_way(int cus, ProductType type, int m, int n, int k, Rows rows, bool
             return MIC_STATUS_SUCCESS;
         });
         if (!w.fused)
-            most = std::max(most, plan_product(cus, Product::FORWARD, logits_type(type), m, columns, k, 1, rows.x, rows.w).bytes);
+            most = std::max(most, plan_logits(cus, type, m, columns, k, rows).bytes);
         return most;
     });
     w.product = (size_t)align_up(w.product, 256);
@@ -394,6 +415,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
             LossProductArgs p = product(v, columns);
             p.y = logits, p.ldy = way.ld_logits;
             Sums sums;
+            p.splits = logits_parts(handle->num_cu, type, m, columns, k, rows);
             MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
             LossRowsArgs r = {};
             r.loss = a;
@@ -516,6 +538,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             p.bias = nullptr;
             p.y = logits, p.ldy = way.ld_logits;
             Sums sums;
+            p.splits = logits_parts(handle->num_cu, type, m, columns, k, rows);
             MIC_TRY(run_product(handle, Product::FORWARD, logits_type(type), p, space, way.product, &sums));
             r.loss = a;
             r.loss.first = v;

@@ -92,6 +92,17 @@ def test_every_way(way, dtype, m, n, k):
     run(x, w, None, classes(4, m, n), "none")
 
 
+@pytest.mark.parametrize("way,m,n,k", [("fused fast 64x128", 40, 33184, 1024), ("split", 40, 33184, 2048), ("split", 47, 33000, 1025),
+                                       ("fused fast 64x128", 130, 33184, 1000), ("fused fast 64x128", 130, 33184, 2100),
+                                       ("split", 128, 33184, 3920)])
+def test_parts_past_a_round(way, m, n, k):
+    """Few more fp32 tiles than CUs: the reduction in parts, more of them than fill the CUs twice."""
+    name = mic.mic_linear_cross_entropy_kernel_name(mic.handle_for(), mic.MIC_DTYPE_F32, m, n, k)
+    assert way in name, name
+    x, w, b = values(1, m, k), values(2, n, k, std=2 * k ** -0.5), values(3, n)
+    run(x, w, b, classes(4, m, n, ignored=5), "mean", a=0.2)
+
+
 @pytest.mark.parametrize("m,n,k", [(1000, 9000, 64), (2049, 4099, 72)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_larger(m, n, k, dtype):
