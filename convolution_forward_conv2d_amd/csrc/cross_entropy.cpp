@@ -555,9 +555,9 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             g.b = o.w, g.ldb = o.ldw;
             g.M = m, g.N = k, g.K = columns, g.a_K = (int)pitch, g.b_rows = o.columns;
             g.k_segments = 1;
-            g.m_pitch = INT32_MAX, g.m_valid = m;
             g.y = dx, g.ldy = lddx;
             g.splits = gradient_parts(type, columns);
+            g.loss = a;
             g.sum = sum, g.ld_sum = align_up(k, 8), g.sum_first = v == 0, g.sum_last = v + columns == n;
             return g;
         };
@@ -569,14 +569,15 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
             g.M = classes, g.N = k, g.K = m, g.b_rows = o.columns;
             g.a_rows = first + classes == columns ? (int)pitch - first : classes;
             g.k_segments = 1;
-            g.m_pitch = INT32_MAX, g.m_valid = classes;
             g.y = static_cast<uint8_t*>(dw) + (int64_t)(v + first) * lddw * (int64_t)e, g.ldy = lddw;
             g.splits = gradient_parts(type, m);
+            g.loss = a;
+            g.sum_first = g.sum_last = true;
             return g;
         };
         if (dx && dw && k && pairs(handle->num_cu, way, type, m, n, k, rows)) {
-            LossProductArgs a = input(), b = weights(0, columns);
-            MIC_TRY(run_pair(handle, type, a, b));
+            LossProductArgs first = input(), second = weights(0, columns);
+            MIC_TRY(run_pair(handle, type, first, second));
             continue;
         }
         if (dx && k) {

@@ -114,6 +114,7 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
     constexpr bool EXACT = sizeof(T) == 4;
     const int c = (blockIdx.x * COLS + threadIdx.x) * 8, nv = p.cols - c;
     const float every = p.loss.smooth / (float)p.loss.classes, goal = 1.0f - p.loss.smooth + every;
+    const float unit = loss_unit<EXACT>(p.loss);
     float total[8] = {};
     if (c < p.dz_pitch) {
         float bias[8] = {};
@@ -129,7 +130,7 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += more[i];
             }
-            const LossRow row = loss_row(p.loss, r);
+            const LossRow row = loss_row(p.loss, r, unit);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[i] = i < nv ? loss_gradient<EXACT>(row, v[i] + bias[i], c + i == row.at, goal, every) : 0.0f;
@@ -148,7 +149,7 @@ template <class T> __global__ __launch_bounds__(COLS * LANES) void loss_gradient
 #pragma unroll
     for (int y = 0; y < LANES; ++y) s += part[y][k];
     const int col = blockIdx.x * COLS * 8 + k;
-    if (col < p.cols) p.sums[(int64_t)blockIdx.y * p.cols + col] = s;
+    if (col < p.cols) p.sums[(int64_t)blockIdx.y * p.cols + col] = s * unit;
 }
 
 // 16 rows a block, 64 lanes of runs: 4096 rows of 782 runs in 256 blocks (32 rows a block took 16.6 us).

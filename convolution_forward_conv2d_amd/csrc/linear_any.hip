@@ -160,8 +160,8 @@ template <class Mul> hipError_t launch_type(Product kind, const ProductArgs& p, 
     case Product::FORWARD: return launch_one<Mul, false, false, EPI_LINEAR>(p, tile, stream);
     case Product::GATED: return launch_one<Mul, false, false, EPI_GATED>(p, tile, stream);
     case Product::INPUT_GRAD: return launch_one<Mul, false, true, EPI_PLAIN>(p, tile, stream);
-    case Product::WEIGHT_GRAD:
-    case Product::CLASS_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+    case Product::WEIGHT_GRAD: return launch_one<Mul, true, true, EPI_PLAIN>(p, tile, stream);
+    case Product::CLASS_GRAD: return launch_one<Mul, true, true, EPI_SUM>(p, tile, stream);
     case Product::INPUT_SUM: return launch_one<Mul, false, true, EPI_SUM>(p, tile, stream);
     default: break;
     }
@@ -209,6 +209,7 @@ template <class Out> hipError_t join_type(Product kind, const ProductArgs& p, in
     case Product::FORWARD: join_kernel<Out, EPI_LINEAR><<<blocks, 256, 0, stream>>>(p); break;
     case Product::GATED: join_kernel<Out, EPI_GATED><<<blocks, 256, 0, stream>>>(p); break;
     case Product::INPUT_SUM:
+    case Product::CLASS_GRAD:
         join_kernel<Out, EPI_SUM><<<blocks, 256, 0, stream>>>(static_cast<const LossProductArgs&>(p));
         break;
     default: join_kernel<Out, EPI_PLAIN><<<blocks, 256, 0, stream>>>(p); break;

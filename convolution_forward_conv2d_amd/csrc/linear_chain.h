@@ -189,7 +189,17 @@ __device__ __forceinline__ void chain(const LossProductArgs& p, uint8_t* smem, i
         if constexpr (EPI == EPI_LOSS) {
             loss_wave<E == 4>(p, acc, m0, j0, lane);
         } else {
-            if constexpr (EPI == EPI_LOGITS_GRAD) gradient_wave<E == 4>(p, acc, m0, j0, lane);
+            if constexpr (EPI == EPI_LOGITS_GRAD) {
+                gradient_wave<E == 4>(p, acc, m0, j0, lane);
+            } else {
+                const float unit = loss_unit<E == 4>(p.loss);
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int e = 0; e < (int)(sizeof(Block) / 4); ++e) acc[i][j][e] *= unit;
+            }
             store_wave(static_cast<Out*>(p.y), p.ldy, p.M, EPI == EPI_LOGITS_GRAD ? p.y_columns : p.N, acc, m0, j0, lane);
         }
     }

@@ -110,11 +110,12 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
     add_bias<In>(p, acc, j0, lane);
     const float every = p.loss.smooth / (float)p.loss.classes, goal = 1.0f - p.loss.smooth + every;
     const int n0 = j0 + lane_column<T>(lane), left = p.N - n0;
+    const float unit = loss_unit<EXACT>(p.loss);
     LossRow rows[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + T * i + lane % T;
-        rows[i] = loss_row(p.loss, min(m, p.M - 1));
+        rows[i] = loss_row(p.loss, min(m, p.M - 1), unit);
         if (m >= p.M) rows[i].at = NO_GRADIENT;
     }
 #pragma unroll
@@ -145,7 +146,7 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
             for (int i = 0; i < FM; ++i) s += acc[i][j][e];
 #pragma unroll
             for (int o = 1; o < T; o <<= 1) s += __shfl_xor(s, o);
-            if (lane % T == 0 && column_of<T>(j, e) < left) sums[column_of<T>(j, e)] = s;
+            if (lane % T == 0 && column_of<T>(j, e) < left) sums[column_of<T>(j, e)] = s * unit;
             __builtin_amdgcn_sched_barrier(0);
         }
 }

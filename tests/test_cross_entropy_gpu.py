@@ -247,6 +247,48 @@ def test_far_logits(m, n, k, dtype):
     run(x, w, None, best, "none")
 
 
+@pytest.mark.parametrize("m,n,k", [(512, 20011, 64), (40, 5003, 65), (700, 4096, 128)])
+@pytest.mark.parametrize("a", [0.0, 0.1])
+def test_targets_are_not_rounded_alike(m, n, k, a):
+    """Where every class is as likely, a row's gradient is nearly all its target's share, the same number in every row: it
+    must not be off the same way in all of them.
+
+    dz = unit (p' - [target]), unit = goal dloss / count, p' = (p - a / classes) / goal, off the target.  Of -1 + p' bf16
+    takes 2^-9 at most, and no more than it has (the nearest number to -1 + p' is no further from it than -1 is); of a p'
+    half a step, 2^-8 p', and e^x 2^-8 of p more.  Sums are fp32: 2^-24 a term, at most."""
+    x, w, t = values(1, m, k, dtype=BF16), values(2, n, k, std=0.01, dtype=BF16), classes(3, m, n)
+    got = mic.linear_cross_entropy(x, w, t, label_smoothing=a)
+    dloss = torch.tensor(1.2375, device=DEV)                   # 1.2375 and 0.9 times that lie between numbers of bf16
+    dx, dw, _ = mic.linear_cross_entropy_backward(dloss, x, w, t, got.lse, count=got.count, label_smoothing=a)
+    x, w, t = x.double().cpu(), w.double().cpu(), t.cpu()
+    p = torch.softmax(x @ w.T, 1)
+    hit = torch.nn.functional.one_hot(t, n).double()
+    goal = 1 - a + a / n
+    unit = goal * 1.2375 / m
+    share = (p - a / n) / goal
+    dz = share - hit * ((1 - a) / goal)
+    off = torch.where(hit > 0, torch.minimum(p / goal, torch.tensor(2.0 ** -9)), 2.0 ** -8 * share.abs()) + 2.0 ** -8 * p / goal
+    for g, want, by in ((dw, dz.T @ x, off.T @ x.abs() + m * 2.0 ** -24 * (dz.abs().T @ x.abs())),
+                        (dx, dz @ w, off @ w.abs() + n * 2.0 ** -24 * (dz.abs() @ w.abs()))):
+        apart = (g.double().cpu() - unit * want).abs()
+        bound = unit * (2.0 ** -8 * want.abs() + (1 + 2.0 ** -8) * by)
+        assert bool((apart <= bound).all()), float((apart / bound).max())
+
+
+@pytest.mark.parametrize("dtype,m,n,k", [(BF16, 256, 1000, 512), (F32, 40, 500, 64), (BF16, 1024, 17003, 128)])
+def test_gradients_of_nothing_and_of_no_number(dtype, m, n, k):
+    """A dloss of 0 leaves no gradient; one that is infinite or no number leaves rows without a target theirs, 0."""
+    x, w, b = values(1, m, k, dtype=dtype), values(2, n, k, std=2 * k ** -0.5, dtype=dtype), values(3, n, dtype=dtype)
+    t = classes(4, m, n, ignored=4)
+    got = mic.linear_cross_entropy(x, w, t, bias=b)
+    for value in (0.0, float("inf"), float("nan")):
+        grads = mic.linear_cross_entropy_backward(torch.tensor(value, device=DEV), x, w, t, got.lse, bias=b, count=got.count)
+        if value == 0:
+            assert not any(bool(g.any()) for g in grads)
+        else:
+            assert not bool(grads[0][::4].any()) and not bool(grads[0][1].isfinite().any())
+
+
 @pytest.mark.parametrize("m,n,k,dtype", KINDS)
 def test_what_is_not_needed(m, n, k, dtype):
     x, w, b = values(1, m, k, dtype=dtype), values(2, n, k, dtype=dtype), values(3, n, dtype=dtype)
