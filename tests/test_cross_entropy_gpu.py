@@ -339,6 +339,29 @@ def test_captured_and_replayed(m, n, k, dtype):
             assert torch.equal(a, e)
 
 
+@pytest.mark.parametrize("k", [4104, 4101])
+def test_offsets_past_32_bits(k):
+    """x of more than 2^32 elements, of which only the first and last rows have targets."""
+    m, n = (1 << 20) + 5, 40
+    x = torch.empty(m, k, dtype=BF16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    w, b = values(2, n, k, std=2 * k ** -0.5, dtype=BF16), values(3, n, dtype=BF16)
+    ends = torch.cat([torch.arange(50), torch.arange(m - 50, m)]).to(DEV)
+    few = classes(4, 100, n)
+    target = torch.full((m,), -100, device=DEV)
+    target[ends] = few
+    got = mic.linear_cross_entropy(x, w, target, bias=b)
+    assert float(got.count) == 100
+    want = T.cross_entropy(x[ends], w, b, few, "mean")
+    T.check(got.loss, want["loss"], "loss")
+    T.check(got.lse[ends], want["lse"], "lse")
+    dloss = torch.tensor(1.25, device=DEV)
+    dx, dw, db = mic.linear_cross_entropy_backward(dloss, x, w, target, got.lse, bias=b, count=got.count)
+    ref = T.cross_entropy_backward(dloss, x[ends], w, b, few, got.lse[ends], got.count)
+    for g, r, name in ((dx[ends], ref[0], "dx"), (dw, ref[1], "dw"), (db, ref[2], "dbias")):
+        T.check(g, r, name)
+    assert not any(bool(dx[r:r + (1 << 18)].any()) for r in range(50, m - 50 - (1 << 18), 1 << 18))
+
+
 def test_nothing():
     x, w, b = values(1, 0, 16), values(2, 10, 16), values(3, 10)
     target = torch.zeros(0, dtype=torch.int64, device=DEV)

@@ -191,6 +191,20 @@ def test_another_stream_and_repeats():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("cols", [4104, 4101])
+def test_offsets_past_32_bits(cols):
+    """More than 2^32 elements: the last rows' results, bit for bit, are those of a call on them alone."""
+    rows = (1 << 20) + 5
+    x = torch.empty(rows, cols, dtype=BF16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
+    w, b = values(2, cols, dtype=BF16), values(3, cols, dtype=BF16)
+    r = mic.layer_norm(x, w, bias=b)
+    last = mic.layer_norm(x[-300:], w, bias=b)
+    for name in ("y", "mean", "rstd"):
+        assert torch.equal(getattr(r, name)[-300:], getattr(last, name)), name
+    dx = mic.layer_norm_backward(x, r.sum, w, r.mean, r.rstd, need_dweight=False)[0]
+    assert torch.equal(dx[-300:], mic.layer_norm_backward(x[-300:], last.sum, w, last.mean, last.rstd, need_dweight=False)[0])
+
+
 def test_refusals():
     x, w = values(1, 4, 8), values(2, 8)
     mean = x.mean(1)
