@@ -455,65 +455,95 @@ __global__ __launch_bounds__(64 * WAVES * ROWS) void layer_norm_grad_kernel(cons
     }
 }
 
-// dx of rows past the registers, read twice.
-template <class T, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void layer_norm_grad_long_kernel(const LayerNormGradArgs p)
+// All of it in one launch, without partial sums, for few rows or rows past the registers: a workgroup per 64 columns walks
+// all rows for dweight and dbias, the others have dx, a row at a time.  dy and sum are read twice, by both, mostly from
+// cache; rows of more than 8192 columns again past those.
+template <class T, int END> __global__ __launch_bounds__(512) void layer_norm_grad_few_kernel(const LayerNormGradArgs p, int column_blocks)
 {
-    constexpr int SPAN = 64 * WAVES * 8;
-    __shared__ float part[2][WAVES][2];
+    constexpr int WAVES = 8, SPAN = 64 * WAVES * 8, KEPT = 2;
     const T* weight = static_cast<const T*>(p.weight);
+    auto fetch = [&](const void* from, int64_t at, int nv, float (&v)[8]) {
+        Vec<T, END> t;
+        t.load(static_cast<const T*>(from) + at, nv);
+        t.settle(nv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = t.value(i);
+    };
+    if ((int)blockIdx.x < column_blocks) {
+        // eight threads across, 64 rows at a time
+        __shared__ float part[WAVES][2][64];
+        const int x = threadIdx.x & 7, c = (int)blockIdx.x * 64 + x * 8, nv = p.cols - c;
+        float dw[8] = {}, db[8] = {};
+        if (nv > 0) {
+#pragma unroll 2
+            for (int row = threadIdx.x >> 3; row < p.rows; row += 64) {
+                float a[8], b[8];
+                fetch(p.dy, row * p.lddy + c, nv, a);
+                fetch(p.sum, row * p.lds + c, nv, b);
+                const float mean = p.mean[row], rstd = p.rstd[row];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[i] += a[i] * ((b[i] - mean) * rstd), db[i] += a[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int o = 8; o < 64; o <<= 1) dw[i] += __shfl_xor(dw[i], o), db[i] += __shfl_xor(db[i], o);
+            if ((threadIdx.x & 63) < 8) part[threadIdx.x >> 6][0][x * 8 + i] = dw[i], part[threadIdx.x >> 6][1][x * 8 + i] = db[i];
+        }
+        __syncthreads();
+        if (threadIdx.x >= 128) return;
+        const int of = threadIdx.x >> 6, column = (int)blockIdx.x * 64 + (threadIdx.x & 63);
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) s += part[w][of][threadIdx.x & 63];
+        T* out = static_cast<T*>(of ? p.dbias : p.dweight);
+        if (out && column < p.cols) out[column] = from_f32<T>(s);
+        return;
+    }
+    __shared__ float part[2][WAVES][2];
     const float per = 1.0f / (float)p.cols;
     int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-        const T* sum = static_cast<const T*>(p.sum) + row * p.lds;
+    for (int64_t row = (int)blockIdx.x - column_blocks; row < p.rows; row += (int)gridDim.x - column_blocks, turn ^= 1) {
         const float mean = p.mean[row], rstd = p.rstd[row];
-        auto each = [&](auto&& f) {
-            for (int c = threadIdx.x * 8; c < p.cols; c += SPAN) {
-                float g[8], u[8], w[8];
-                load8(dy + c, p.cols - c, g);
-                load8(sum + c, p.cols - c, u);
-                load8(weight + c, p.cols - c, w);
+        float g[KEPT][8], u[KEPT][8];
+        auto both = [&](int c, float (&gc)[8], float (&uc)[8]) {
+            float w[8];
+            fetch(p.dy, row * p.lddy + c, p.cols - c, gc);
+            fetch(p.sum, row * p.lds + c, p.cols - c, uc);
+            fetch(weight, c, p.cols - c, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] *= w[i], u[i] = (u[i] - mean) * rstd;
-                f(c, g, u);
+            for (int i = 0; i < 8; ++i) gc[i] *= w[i], uc[i] = (uc[i] - mean) * rstd;
+        };
+        // over all of this thread's columns: the kept ones, then those read again
+#pragma unroll
+        for (int j = 0; j < KEPT; ++j) both(threadIdx.x * 8 + j * SPAN, g[j], u[j]);
+        auto each = [&](auto&& f) {
+#pragma unroll
+            for (int j = 0; j < KEPT; ++j) f(threadIdx.x * 8 + j * SPAN, g[j], u[j]);
+            for (int c = threadIdx.x * 8 + KEPT * SPAN; c < p.cols; c += SPAN) {
+                float gc[8], uc[8];
+                both(c, gc, uc);
+                f(c, gc, uc);
             }
         };
         float level = 0.0f, along = 0.0f;
-        each([&](int, const float (&g)[8], const float (&u)[8]) {
+        each([&](int, const float (&gc)[8], const float (&uc)[8]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) level += g[i], along += g[i] * u[i];
+            for (int i = 0; i < 8; ++i) level += gc[i], along += gc[i] * uc[i];
         });
         block_sums<WAVES>(level, along, part[turn]);
         level *= per, along *= per;
-        each([&](int c, float (&g)[8], const float (&u)[8]) {
-            float d[8] = {};
-            if (p.dsum) load8(static_cast<const T*>(p.dsum) + row * p.ldd + c, p.cols - c, d);
+        each([&](int c, const float (&gc)[8], const float (&uc)[8]) {
+            const int nv = p.cols - c;
+            if (nv <= 0) return;
+            float d[8] = {}, v[8];
+            if (p.dsum) fetch(p.dsum, row * p.ldd + c, nv, d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = rstd * (g[i] - level - u[i] * along) + d[i];
-            store8(static_cast<T*>(p.dx) + row * p.lddx + c, p.cols - c, g);
+            for (int i = 0; i < 8; ++i) v[i] = rstd * (gc[i] - level - uc[i] * along) + d[i];
+            store8(static_cast<T*>(p.dx) + row * p.lddx + c, END == END_WHOLE ? 8 : nv, v);
         });
     }
-}
-
-// dweight's and dbias's partial column sums on their own, for rows past the
-// registers: a group walks its rows with one vector of eight columns a thread.
-template <class T> __global__ __launch_bounds__(64) void layer_norm_weight_kernel(const LayerNormGradArgs p)
-{
-    const int c = (blockIdx.y * 64 + threadIdx.x) * 8, nv = p.cols - c;
-    if (nv <= 0) return;
-    float dw[8] = {}, db[8] = {};
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        float a[8], b[8];
-        load8(static_cast<const T*>(p.dy) + row * p.lddy + c, nv, a);
-        load8(static_cast<const T*>(p.sum) + row * p.lds + c, nv, b);
-        const float mean = p.mean[row], rstd = p.rstd[row];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[i] += a[i] * ((b[i] - mean) * rstd), db[i] += a[i];
-    }
-    float* out = p.partial + (int64_t)blockIdx.x * 2 * p.cols + c;
-    if (p.dweight) store8(out, nv, dw);
-    if (p.dbias) store8(out + p.cols, nv, db);
 }
 
 // 32 columns a block, 32 lanes of groups: lines of 128 bytes (of 64, 512 groups of 4096 columns took 7 us instead of 4.8);
@@ -593,11 +623,20 @@ template <class T, int WAVES, int ROWS, int NV, bool NEXT> void launch_grad_wave
     else layer_norm_grad_kernel<T, WAVES, ROWS, NV, NEXT, END_CUT><<<p.groups, THREADS, 0, stream>>>(p);
 }
 
+constexpr int ROWS_AT_ONCE = 768;
 constexpr int SHORT_ROWS = 4;      // rows of up to 512 columns that a workgroup walks side by side
 
 template <class T> hipError_t launch_grad_type(const LayerNormGradArgs& p, hipStream_t stream)
 {
     const int v = (p.cols + 7) / 8;
+    if (!p.groups) {
+        const int columns = p.dweight || p.dbias ? (p.cols + 63) / 64 : 0;
+        const uint32_t grid = (uint32_t)(columns + std::min(p.rows, GRID_ROWS));
+        if (p.cols < 8) layer_norm_grad_few_kernel<T, END_SHORT><<<grid, 512, 0, stream>>>(p, columns);
+        else if (p.cols % 8) layer_norm_grad_few_kernel<T, END_CUT><<<grid, 512, 0, stream>>>(p, columns);
+        else layer_norm_grad_few_kernel<T, END_WHOLE><<<grid, 512, 0, stream>>>(p, columns);
+        return hipGetLastError();
+    }
     if (p.cols < 8)
         layer_norm_grad_kernel<T, 1, SHORT_ROWS, 1, true, END_SHORT><<<p.groups, 64 * SHORT_ROWS, 0, stream>>>(p);
     else if (v <= 64) launch_grad_waves<T, 1, SHORT_ROWS, 1, true>(p, stream);
@@ -605,12 +644,7 @@ template <class T> hipError_t launch_grad_type(const LayerNormGradArgs& p, hipSt
     else if (v <= 512) launch_grad_waves<T, 8, 1, 1, true>(p, stream);
     else if (v <= 1024) launch_grad_waves<T, 16, 1, 1, true>(p, stream);
     else if (v <= 1536) launch_grad_waves<T, 12, 1, 2, sizeof(T) == 2>(p, stream);
-    else if (v <= 2048) launch_grad_waves<T, 16, 1, 2, false>(p, stream);
-    else {
-        if (p.rows) layer_norm_grad_long_kernel<T, 8><<<p.groups, 512, 0, stream>>>(p);
-        if (p.dweight || p.dbias)
-            layer_norm_weight_kernel<T><<<dim3(p.groups, (v + 63) / 64), 64, 0, stream>>>(p);
-    }
+    else launch_grad_waves<T, 16, 1, 2, false>(p, stream);
     if (p.dweight || p.dbias)
         layer_norm_join_kernel<T><<<dim3((p.cols + 31) / 32, 2), dim3(32, 32), 0, stream>>>(p);
     return hipGetLastError();
@@ -624,14 +658,18 @@ hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStr
     return e4m3 ? launch_type<Bf16, true>(p, stream) : launch_type<Bf16, false>(p, stream);
 }
 
-// A group's shares of dweight and dbias are written and read again, so as few groups as keep memory busy: one of eight
-// waves a CU (8192 x 4096 bf16 takes 49 us, 56 with two), two of four waves (8192 x 2048 30, 35 with four), each walking
-// three rows at least (300 x 4096 10.4 us, 13.4 on a group a row).
+// 0: one launch.  Of few rows it saves the second launch and the walk: 64 x 4096 bf16 5.2 us (9.1), 300 x 4096 5.2 (10.9),
+// 768 x 4096 7.3 (14.3); 1024 x 4095 19.8 (17.9).  Rows past 16384 columns do not stay in a workgroup's registers, and are
+// then read as often: 8192 x 20000 bf16 385 us (863 with a walk of their own for dweight and dbias).
+// Otherwise a group's shares of dweight and dbias are written and read again, so as few groups as keep memory busy: one of
+// eight waves a CU (8192 x 4096 bf16 takes 49 us, 56 with two), two of four waves (8192 x 2048 30, 35 with four), each
+// walking three rows at least.
 int layer_norm_grad_groups(int rows, int cols, int num_cu)
 {
+    if (rows <= ROWS_AT_ONCE || cols > 16384) return 0;
     const int walks = cols <= 512 ? (rows + SHORT_ROWS - 1) / SHORT_ROWS : rows;
     const int most = std::min((cols <= 2048 ? 2 : 1) * num_cu, (walks + 2) / 3);
-    return walks > 1 ? even_groups(walks, most) : 1;
+    return even_groups(walks, most);
 }
 
 hipError_t launch_layer_norm_grad(DType dt, const LayerNormGradArgs& p, hipStream_t stream)

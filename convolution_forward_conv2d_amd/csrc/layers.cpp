@@ -62,7 +62,7 @@ mic_status mic_layer_norm_backward(mic_handle handle, mic_dtype dtype, int rows,
     if (rows && (!mean || !aligned(mean, 4) || !rstd || !aligned(rstd, 4))) return MIC_STATUS_BAD_PARAM;
     const bool sums = dweight || dbias;
     if (rows == 0 && !sums) return MIC_STATUS_SUCCESS;
-    if (sums && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return MIC_STATUS_BAD_PARAM;
+    if (sums && need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return MIC_STATUS_BAD_PARAM;
     const LayerNormGradArgs p = {rows, cols, dy, lddy, sum, lds, weight, mean, rstd, dsum, ldd, dx, lddx, dweight, dbias,
                                  static_cast<float*>(workspace), layer_norm_grad_groups(rows, cols, handle->num_cu)};
     return launched(launch_layer_norm_grad(device_type(dtype), p, handle->stream));

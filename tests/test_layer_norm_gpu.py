@@ -68,6 +68,15 @@ def test_backward(m, c, dtype):
             R.check(db, want[2], "dbias")
 
 
+# more rows than one launch takes: workgroups walk them, each width its own kernel; the last few and next widths' ends cut
+@pytest.mark.parametrize("m,c", [(769, 1), (801, 5), (2000, 8), (1100, 300), (800, 512), (900, 513), (800, 2048), (801, 2049),
+                                 (800, 4096), (800, 4097), (769, 8192), (769, 8195), (800, 12288), (800, 12295), (769, 16384),
+                                 (769, 16385), (769, 16400), (768, 4096), (768, 1001)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_backward_of_many_rows(m, c, dtype):
+    test_backward(m, c, dtype)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("m,c,pad,offset", [(3, 40, 8, 8), (5, 513, 3, 1), (7, 1001, 1, 3), (2, 16400, 5, 1)])
 def test_pitches_and_alignments(m, c, pad, offset, dtype):
@@ -193,16 +202,17 @@ def test_another_stream_and_repeats():
 
 @pytest.mark.parametrize("cols", [4104, 4101])
 def test_offsets_past_32_bits(cols):
-    """More than 2^32 elements: the last rows' results, bit for bit, are those of a call on them alone."""
+    """More than 2^32 elements: the last rows' results, bit for bit, are those of a call on them alone
+    (on more rows than one launch takes, as all are)."""
     rows = (1 << 20) + 5
     x = torch.empty(rows, cols, dtype=BF16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(1))
     w, b = values(2, cols, dtype=BF16), values(3, cols, dtype=BF16)
     r = mic.layer_norm(x, w, bias=b)
-    last = mic.layer_norm(x[-300:], w, bias=b)
+    last = mic.layer_norm(x[-1000:], w, bias=b)
     for name in ("y", "mean", "rstd"):
-        assert torch.equal(getattr(r, name)[-300:], getattr(last, name)), name
+        assert torch.equal(getattr(r, name)[-1000:], getattr(last, name)), name
     dx = mic.layer_norm_backward(x, r.sum, w, r.mean, r.rstd, need_dweight=False)[0]
-    assert torch.equal(dx[-300:], mic.layer_norm_backward(x[-300:], last.sum, w, last.mean, last.rstd, need_dweight=False)[0])
+    assert torch.equal(dx[-1000:], mic.layer_norm_backward(x[-1000:], last.sum, w, last.mean, last.rstd, need_dweight=False)[0])
 
 
 def test_refusals():

@@ -22,7 +22,7 @@ def test_norm_refusals(change, want):
 
 
 NGRAD = "h dtype rows cols dy lddy sum lds weight mean rstd dsum ldd dx lddx dweight dbias work bytes".split()
-NGRAD_OK = dict(h=None, dtype=F32, rows=4, cols=8, dy=P, lddy=8, sum=P, lds=8, weight=P, mean=P, rstd=P, dsum=0, ldd=0, dx=P,
+NGRAD_OK = dict(h=None, dtype=F32, rows=2000, cols=8, dy=P, lddy=8, sum=P, lds=8, weight=P, mean=P, rstd=P, dsum=0, ldd=0, dx=P,
                 lddx=8, dweight=P, dbias=P, work=P, bytes=BIG)
 
 
@@ -57,7 +57,9 @@ def test_nothing_to_do_is_done():
 
 
 def test_workspaces():
-    assert mic.mic_layer_norm_backward_workspace(None, 1, 9) == 72
+    # few rows have no partial sums; 1000 rows of 9 columns four side by side, at least three of those to a group
+    assert mic.mic_layer_norm_backward_workspace(None, 1, 9) == 0
+    assert mic.mic_layer_norm_backward_workspace(None, 1000, 9) == 84 * 9 * 8
     assert status("mic_layer_norm_backward_workspace", None, 4, 4, None) == BAD
     # without a handle the answer serves any number of compute units
     sizes = [(1, 1), (100, 512), (5000, 4096), (5000, 9000), (5000, 20000)]
