@@ -350,7 +350,8 @@ struct LayerNormGradArgs {
     void* dweight;
     void* dbias;
     float* partial;           // [groups][2][cols]: shares of dweight, of dbias
-    int groups;
+    int groups;               // 0: one launch
+    int num_cu;
 };
 hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStream_t stream);
 int layer_norm_grad_groups(int rows, int cols, int num_cu);

@@ -592,6 +592,7 @@ template <class T, bool E4M3> hipError_t launch_type(const LayerNormArgs& p, hip
     const int v = (p.cols + 7) / 8;                            // vectors in a row
     if (p.cols < 8) layer_norm_kernel<T, E4M3, 1, 1, END_SHORT><<<even_groups(p.rows, 24 * p.num_cu), 64, 0, stream>>>(p);
     else if (v <= 64) launch_waves<T, E4M3, 1, 1>(p, 24, stream);
+    else if (v <= 128) launch_waves<T, E4M3, 2, 1>(p, 12, stream);
     else if (v <= 256) launch_waves<T, E4M3, 4, 1>(p, 6, stream);
     else if (v <= 512) launch_waves<T, E4M3, 4, 2>(p, 4, stream);
     else if (v <= 1024) launch_waves<T, E4M3, 8, 2>(p, 2, stream);
@@ -623,7 +624,7 @@ template <class T, int WAVES, int ROWS, int NV, bool NEXT> void launch_grad_wave
     else layer_norm_grad_kernel<T, WAVES, ROWS, NV, NEXT, END_CUT><<<p.groups, THREADS, 0, stream>>>(p);
 }
 
-constexpr int ROWS_AT_ONCE = 768;
+constexpr int ROWS_AT_ONCE = 768, LONG_WALKS = 16;
 constexpr int SHORT_ROWS = 4;      // rows of up to 512 columns that a workgroup walks side by side
 
 template <class T> hipError_t launch_grad_type(const LayerNormGradArgs& p, hipStream_t stream)
@@ -640,6 +641,7 @@ template <class T> hipError_t launch_grad_type(const LayerNormGradArgs& p, hipSt
     if (p.cols < 8)
         layer_norm_grad_kernel<T, 1, SHORT_ROWS, 1, true, END_SHORT><<<p.groups, 64 * SHORT_ROWS, 0, stream>>>(p);
     else if (v <= 64) launch_grad_waves<T, 1, SHORT_ROWS, 1, true>(p, stream);
+    else if (v <= 128 && p.rows > LONG_WALKS * p.num_cu) launch_grad_waves<T, 2, 1, 1, true>(p, stream);
     else if (v <= 256) launch_grad_waves<T, 4, 1, 1, true>(p, stream);
     else if (v <= 512) launch_grad_waves<T, 8, 1, 1, true>(p, stream);
     else if (v <= 1024) launch_grad_waves<T, 16, 1, 1, true>(p, stream);
@@ -663,12 +665,13 @@ hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStr
 // then read as often: 8192 x 20000 bf16 385 us (863 with a walk of their own for dweight and dbias).
 // Otherwise a group's shares of dweight and dbias are written and read again, so as few groups as keep memory busy: one of
 // eight waves a CU (8192 x 4096 bf16 takes 49 us, 56 with two), two of four waves (8192 x 2048 30, 35 with four), each
-// walking three rows at least.
+// walking three rows at least.  Rows that fill a quarter to a half of four waves go to two where walks stay long: 8192 x
+// 768 bf16 16.6 us (21.2), 32768 x 1000 49 (70), fp32 105 (100); 2048 x 768 would take 11.9 (10.5).
 int layer_norm_grad_groups(int rows, int cols, int num_cu)
 {
     if (rows <= ROWS_AT_ONCE || cols > 16384) return 0;
     const int walks = cols <= 512 ? (rows + SHORT_ROWS - 1) / SHORT_ROWS : rows;
-    const int most = std::min((cols <= 2048 ? 2 : 1) * num_cu, (walks + 2) / 3);
+    const int most = std::min((cols > 512 && cols <= 1024 && rows > LONG_WALKS * num_cu ? 4 : cols <= 2048 ? 2 : 1) * num_cu, (walks + 2) / 3);
     return even_groups(walks, most);
 }
 

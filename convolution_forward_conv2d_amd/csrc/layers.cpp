@@ -64,7 +64,7 @@ mic_status mic_layer_norm_backward(mic_handle handle, mic_dtype dtype, int rows,
     if (rows == 0 && !sums) return MIC_STATUS_SUCCESS;
     if (sums && need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return MIC_STATUS_BAD_PARAM;
     const LayerNormGradArgs p = {rows, cols, dy, lddy, sum, lds, weight, mean, rstd, dsum, ldd, dx, lddx, dweight, dbias,
-                                 static_cast<float*>(workspace), layer_norm_grad_groups(rows, cols, handle->num_cu)};
+                                 static_cast<float*>(workspace), layer_norm_grad_groups(rows, cols, handle->num_cu), handle->num_cu};
     return launched(launch_layer_norm_grad(device_type(dtype), p, handle->stream));
 }
 

@@ -71,7 +71,8 @@ def test_backward(m, c, dtype):
 # more rows than one launch takes: workgroups walk them, each width its own kernel; the last few and next widths' ends cut
 @pytest.mark.parametrize("m,c", [(769, 1), (801, 5), (2000, 8), (1100, 300), (800, 512), (900, 513), (800, 2048), (801, 2049),
                                  (800, 4096), (800, 4097), (769, 8192), (769, 8195), (800, 12288), (800, 12295), (769, 16384),
-                                 (769, 16385), (769, 16400), (768, 4096), (768, 1001)])
+                                 (769, 16385), (769, 16400), (768, 4096), (768, 1001), (4097, 513), (5000, 1001), (4200, 1024),
+                                 (4099, 520)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_backward_of_many_rows(m, c, dtype):
     test_backward(m, c, dtype)
