@@ -44,6 +44,10 @@ Extent extent_of(Product kind, int m, int n, int k)
 // of 256 x 192; 4096 x 9216 of 4096 terms, 2.25 rounds of the one and exactly
 // three of the other, 311 and 258.
 constexpr double kReadPerUs = 4.5e6;
+// A loss's blocks of few rows, which read whole rows of the weights, then end in their own rows' exponentials.  Measured,
+// blocks and (128 x 256 tiles), us: 65536 x 4096 of 4 rows 103 (133), of 8 109 (133), of 16 137 (133); 50021 x 4096 of 8
+// 88 (104); 128000 x 1024 of 4 64 (53), of 16 92 (50).
+constexpr double kFewLossPerUs = 5.2e6, kFewLossRow = 0.12;
 struct TileCost {
     int bm, bn;
     double step, tile;
@@ -73,6 +77,9 @@ namespace miconv {
 Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int k, int k_segments, bool aligned_a,
                   bool aligned_b, int least_splits)
 {
+    // a loss's epilogues need whole sums, in large tiles or few rows
+    const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
+    const bool of_loss = kind >= Product::LOSS || type == ProductType::BF16_F32;
     const int raw_n = kind == Product::GATED ? miconv::gated_raw_columns(n) : n;
     const int e = element_bytes(type);
     const int64_t steps = (int64_t)((k + 128 / e - 1) / (128 / e)) * k_segments;
@@ -88,9 +95,6 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
     const double b_bytes = (double)raw_n * k * k_segments * e, read_us = (b_bytes + (double)m * k * k_segments * e) / kReadPerUs;
     Plan best = {};
     best.us = 1e30;
-    // a loss's epilogues need whole sums, in large tiles or few rows
-    const bool whole = kind == Product::LOSS || kind == Product::LOGITS_GRAD;
-    const bool of_loss = kind >= Product::LOSS || type == ProductType::BF16_F32;
     // (a loss of more classes than a grid of 16 to a workgroup reaches goes on tiles)
     const bool few_loss = kind == Product::LOSS && n < 1 << 26;
     if (m <= miconv::FEW_ROWS && (kind == Product::FORWARD || kind == Product::GATED || few_loss)) {
@@ -103,6 +107,8 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
             return best;
         }
         best.us = few_us(num_cu, m, raw_n, kind == Product::GATED, (double)k * e, aligned_a && aligned_b);
+        if (kind == Product::LOSS && e == 2 && aligned_a && aligned_b)
+            best.us = 2.5 + b_bytes / kFewLossPerUs + kFewLossRow * m * std::max(1.0, (double)n / 16 / num_cu);
     }
     auto consider = [&](Plan pl, int64_t t, int bm, int bn, int slots, double step, double tile) {
         // HIP takes grids of fewer than 2^32 threads: 2^30 rows of 64 x 64 are past that
@@ -113,7 +119,10 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
         if (m <= 2 * bm) step = std::max(step, of_loss ? std::max(0.72, (bm + bn) * 128 / 46.0e3) : 0.9);
         const int most = whole ? 1 : std::max(least_splits, most_splits(t));
         for (int s = least_splits; s <= most; ++s) {
-            const double us = std::max(rounds(t * s, slots) * ((steps + s - 1) / s * step + tile), read_us) + join_us(s) + pl.us + 1.5;
+            const double busy = rounds(t * s, slots) * ((steps + s - 1) / s * step + tile);
+            double us = std::max(busy, read_us) + join_us(s) + pl.us + 1.5;
+            // of tiles that all wait for memory, the one that does less beside it
+            if (of_loss) us += 0.05 * std::min(busy, read_us);
             if (us < best.us) {
                 best = pl;
                 best.splits = s;
