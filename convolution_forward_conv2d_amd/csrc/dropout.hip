@@ -10,7 +10,10 @@
 //
 // Eight lots from one block keep the generator's twenty wide products, a quarter
 // of the vector rate each, below memory's time: with four lots of 32 bits a bf16
-// row would wait for them.  p is then a multiple of 2^-16.
+// row would wait for them.  p is then a multiple of 2^-16.  Bound by memory: 8192 x
+// 4096 bf16 with a residual takes 41.7 us, 4.8 TB/s, the gradient of 4095 x 9216
+// 29.3, 5.1 TB/s, two vectors of eight a thread and no loop; a call on 128 x 4096 is
+// its launch, 4.2.
 #include "linear_common.h"
 #include "kernels.h"
 

@@ -13,7 +13,7 @@
 // the next row is on its way while this one is summed: 4095 x 4096 to e4m3 with a
 // residual takes 23.4 us, 5.0 TB/s (a workgroup per row: 40), the gradient of
 // 8192 x 4096 bf16 45 us and 4 more to join the weight's and bias's partial sums,
-// a copy's rate (104 before).
+// a copy's rate (104 before); few rows' gradients are a launch, 64 x 4096 4.5.
 //
 // The variance is a sum of squared distances, never a difference of sums: each
 // wave takes its own values' mean and their squared distances from it, and the

@@ -257,7 +257,8 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, bias=None, count=Non
     dloss: the gradient of the loss, fp32, a single value or (reduction
     "none") one per row.  dbias is None without a bias; dx, dw and dbias are
     where need_dx, need_dw and need_dbias are false: what is None is not
-    computed.
+    computed.  A row without a target has dx = 0 and adds 0 times its x to dw,
+    which is no number where x is infinite or none: pad with finite rows.
     """
     r = _native().linear_cross_entropy_backward(dloss, x, w, target, lse, bias, count, ignore_index, label_smoothing,
                                                 need_dx, need_dw, need_dbias)
