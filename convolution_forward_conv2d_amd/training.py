@@ -197,6 +197,14 @@ def _targets(target, shape, device):
     return target.data_ptr()
 
 
+def _loss_gradient(dloss, shape, rows, device):
+    """Pointer to dloss, and whether it has a value for each row."""
+    each = dloss.shape == shape and dloss.dim() > 0
+    if each and not dloss.is_contiguous() and not any(st for n, st in zip(dloss.shape, dloss.stride()) if n > 1):
+        dloss, each = dloss[(0,) * dloss.dim()], False         # one value, expanded: a sum's gradient
+    return _per_row(dloss, rows if each else 1, device, "dloss"), each
+
+
 def _smoothing(label_smoothing):
     if isinstance(label_smoothing, torch.Tensor) or not 0 <= label_smoothing < 1:
         raise ValueError("label_smoothing must be a number from 0 and below 1, got %s" % (label_smoothing,))
@@ -255,7 +263,7 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, bias=None, count=Non
     """(dx, dw, dbias) of linear_cross_entropy, from its inputs and its lse and, of a mean, its count.
 
     dloss: the gradient of the loss, fp32, a single value or (reduction
-    "none") one per row.  dbias is None without a bias; dx, dw and dbias are
+    "none") one per row, packed or a single one expanded.  dbias is None without a bias; dx, dw and dbias are
     where need_dx, need_dw and need_dbias are false: what is None is not
     computed.  A row without a target has dx = 0 and adds 0 times its x to dw,
     which is no number where x is infinite or none: pad with finite rows.
@@ -275,8 +283,7 @@ def linear_cross_entropy_backward(dloss, x, w, target, lse, bias=None, count=Non
         raise ValueError("w must have at least one class")
     bp = 0 if bias is None else _vector(bias, n, dtype, device, "bias")
     tp, lp = _targets(target, x.shape[:-1], device), _per_row(lse, m, device, "lse")
-    each = dloss.shape == x.shape[:-1] and dloss.dim() > 0
-    dp = _per_row(dloss, m if each else 1, device, "dloss")
+    dp, each = _loss_gradient(dloss, x.shape[:-1], m, device)
     cp = 0 if count is None else _per_row(count, 1, device, "count")
     smoothing, ignore_index = _smoothing(label_smoothing), _ignored(ignore_index)
     h = _handle(device)
