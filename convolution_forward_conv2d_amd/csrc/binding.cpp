@@ -13,6 +13,8 @@
 
 #include <ATen/ATen.h>
 #include <ATen/EmptyTensor.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -97,10 +99,13 @@ bool plain_scale(const Tensor& t, const Tensor& like, int64_t rows)
 void* data(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 float* floats(const Tensor* t) { return t ? static_cast<float*>(t->data_ptr()) : nullptr; }
 
-// An uninitialised tensor on the current device, from torch's own allocator without the dispatcher's way to it, which
-// takes longer than the allocation (a norm of one token allocates four).
+// An uninitialised tensor on the current device.  From torch's own allocator, without the dispatcher's way to it, which
+// takes longer than the allocation (a norm of one token allocates four); through the dispatcher where something there
+// looks at allocations or fills them: a dispatch mode, a profiler, deterministic algorithms.
 Tensor fresh(at::IntArrayRef sizes, at::ScalarType type)
 {
+    if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::hasCallbacks() || at::globalContext().deterministicAlgorithms())
+        return at::empty(sizes, at::TensorOptions().dtype(type).device(at::kCUDA));
     static c10::Allocator* const from = at::empty({0}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA)).storage().allocator();
     return Tensor(at::detail::empty_generic(sizes, from, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
 }
