@@ -169,7 +169,9 @@ Plan plan_product(int num_cu, Product kind, ProductType type, int m, int n, int 
                 consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, kF32Step * c.bm * c.bn / (128 * 128), c.tile);
             else if (!f32 && c.step > 0) {
                 // many rounds of a loss's tiles: 4096 x 50021 of 4096 terms take 1321 us in 12.25 rounds of 256 x 256
-                // and 1364 in 16.3 of 256 x 192
+                // and 1364 in 16.3 of 256 x 192.  192 x 256 costs the same: priced at 1.12, it took 48 sizes over that
+                // it should not have, 1.8 percent slower in all (618 x 80049 of 3848 terms 423 -> 478 us, 1351 x 55441
+                // of 2768 389 -> 434; others within 2 percent)
                 const double step = whole && c.bm * c.bn == 256 * 192 ? 1.18 : c.step;
                 consider(pl, tiles(c.bm, c.bn), c.bm, c.bn, num_cu, step * widened, c.tile);
             }
