@@ -131,9 +131,9 @@ template <class Bytes> size_t over_pieces(int n, int piece, Bytes bytes)
 }
 
 // Runs that a fused product over `classes` leaves.
-int runs_of(const Plan& pl, ProductType type, int classes)
+int runs_of(const Plan& pl, int classes)
 {
-    const int columns = pl.few ? 8 : loss_columns(type, pl.fast_tile);
+    const int columns = pl.few ? 8 : loss_columns(pl.fast_tile);
     return (classes + columns - 1) / columns;
 }
 
@@ -166,7 +166,7 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
     if (w.fused) {
         w.runs = 0;
         in_cuts(n, loss_cut(cus, w, type, m, n, k), [&](int first, int classes) {
-            w.runs += runs_of(loss_plan(cus, w, type, m, n, classes, k), type, classes);
+            w.runs += runs_of(loss_plan(cus, w, type, m, n, classes, k), classes);
             return MIC_STATUS_SUCCESS;
         });
         w.copy_bytes = w.copies.x + w.copies.w;
@@ -188,7 +188,7 @@ Way forward_way(int cus, ProductType type, int m, int n, int k, Rows rows)
 // Sums of each column that a fused product over `classes` leaves.
 int sum_groups(int cus, ProductType type, int m, int classes, int k)
 {
-    const int rows = loss_rows(type, plan_product(cus, Product::LOGITS_GRAD, type, m, classes, k, 1, true, true).fast_tile);
+    const int rows = loss_rows(plan_product(cus, Product::LOGITS_GRAD, type, m, classes, k, 1, true, true).fast_tile);
     return (m + rows - 1) / rows;
 }
 
@@ -406,7 +406,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
             p.loss = a;
             p.loss.first = first, p.loss.part_first = run;
             p.bias = bias_at(first);
-            run += runs_of(loss_plan(handle->num_cu, way, type, m, n, columns, k), type, columns);
+            run += runs_of(loss_plan(handle->num_cu, way, type, m, n, columns, k), columns);
             return run_product(handle, Product::LOSS, type, p, nullptr, 0);
         }));
     } else {

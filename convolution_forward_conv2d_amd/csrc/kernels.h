@@ -203,8 +203,8 @@ hipError_t launch_product_fast_loss(Product kind, ProductType type, const Produc
 hipError_t launch_product_pair(ProductType type, const ProductArgs& dx, const ProductArgs& dw, hipStream_t stream);
 // Columns that a wave of a tile holds of a row: LOSS leaves one partial result of each row for them; and rows: LOGITS_GRAD
 // leaves one column sum for them.
-int loss_columns(ProductType type, FastTile tile);
-int loss_rows(ProductType type, FastTile tile);
+int loss_columns(FastTile tile);
+int loss_rows(FastTile tile);
 // Rows of `bytes` bytes at any pitch into rows of `to_pitch` (a multiple of 16), zeros behind each (linear_pack.hip).
 constexpr int PACK_JOBS = 3;
 struct PackJob {

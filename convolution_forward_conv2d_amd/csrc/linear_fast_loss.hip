@@ -10,37 +10,63 @@ namespace miconv {
 
 namespace {
 
-template <class Mul, bool AACROSS, bool BACROSS, int EPI, int BM, int BN, int WM, int WN>
+// A tile and how its eight waves share it: rows and columns of waves.  The kernels' arguments and what the host counts
+// by (loss_columns, loss_rows) both come from here.
+struct LossTile {
+    int bm, bn, wm, wn;
+};
+constexpr LossTile loss_tile(FastTile tile)
+{
+    switch (tile) {
+    case FastTile::T256x256: return {256, 256, 2, 4};
+    case FastTile::T256x192: return {256, 192, 4, 2};
+    case FastTile::T192x256: return {192, 256, 2, 4};
+    case FastTile::T256x128: return {256, 128, 4, 2};
+    case FastTile::T128x256: return {128, 256, 2, 4};
+    case FastTile::T128x128: return {128, 128, 2, 4};
+    case FastTile::T128x64: return {128, 64, 4, 2};
+    case FastTile::T64x128: return {64, 128, 2, 4};
+    default: return {1, 1, 1, 1};
+    }
+}
+constexpr bool has_tile(bool f32, FastTile tile)
+{
+    const bool small = tile == FastTile::T128x64 || tile == FastTile::T64x128;
+    return tile == FastTile::T128x128 || small == f32;
+}
+
+template <class Mul, bool AACROSS, bool BACROSS, int EPI, FastTile TILE>
 hipError_t launch_chain(const LossProductArgs& p, hipStream_t stream)
 {
-    const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    // as many workgroups as the CUs hold: two of up to 80 KB of LDS
-    const int64_t grid = (int64_t)p.cus * (3 * BM + 2 * BN <= 640 ? 2 : 1);
-    linear_chain_kernel<Mul, AACROSS, BACROSS, EPI, BM, BN, WM, WN>
-        <<<(uint32_t)(tiles < grid ? tiles : grid), FAST_THREADS, 0, stream>>>(p);
-    return hipGetLastError();
+    if constexpr (!has_tile(Mul::E == 4, TILE)) {
+        return hipErrorInvalidValue;
+    } else {
+        constexpr LossTile t = loss_tile(TILE);
+        const int64_t tiles = (int64_t)((p.M + t.bm - 1) / t.bm) * ((p.N + t.bn - 1) / t.bn);
+        if (tiles > INT32_MAX) return hipErrorInvalidValue;
+        // as many workgroups as the CUs hold: two of up to 80 KB of LDS
+        const int64_t grid = (int64_t)p.cus * (3 * t.bm + 2 * t.bn <= 640 ? 2 : 1);
+        linear_chain_kernel<Mul, AACROSS, BACROSS, EPI, t.bm, t.bn, t.wm, t.wn>
+            <<<(uint32_t)(tiles < grid ? tiles : grid), FAST_THREADS, 0, stream>>>(p);
+        return hipGetLastError();
+    }
 }
 
 template <class Mul, bool AACROSS, bool BACROSS, int EPI>
 hipError_t launch_chains(const ProductArgs& args, FastTile tile, hipStream_t stream)
 {
     const auto& p = static_cast<const LossProductArgs&>(args);
-    if constexpr (Mul::E == 4) switch (tile) {
-    case FastTile::T128x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream);
-    case FastTile::T128x64: return launch_chain<Mul, AACROSS, BACROSS, EPI, 128, 64, 4, 2>(p, stream);
-    case FastTile::T64x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, 64, 128, 2, 4>(p, stream);
+    switch (tile) {
+    case FastTile::T256x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T256x256>(p, stream);
+    case FastTile::T256x192: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T256x192>(p, stream);
+    case FastTile::T192x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T192x256>(p, stream);
+    case FastTile::T256x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T256x128>(p, stream);
+    case FastTile::T128x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T128x256>(p, stream);
+    case FastTile::T128x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T128x128>(p, stream);
+    case FastTile::T128x64: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T128x64>(p, stream);
+    case FastTile::T64x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, FastTile::T64x128>(p, stream);
     default: return hipErrorInvalidValue;
-    } else switch (tile) {
-    case FastTile::T256x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, 256, 256, 2, 4>(p, stream);
-    case FastTile::T256x192: return launch_chain<Mul, AACROSS, BACROSS, EPI, 256, 192, 4, 2>(p, stream);
-    case FastTile::T192x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, 192, 256, 2, 4>(p, stream);
-    case FastTile::T256x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, 256, 128, 4, 2>(p, stream);
-    case FastTile::T128x256: return launch_chain<Mul, AACROSS, BACROSS, EPI, 128, 256, 2, 4>(p, stream);
-    case FastTile::T128x128: return launch_chain<Mul, AACROSS, BACROSS, EPI, 128, 128, 2, 4>(p, stream);
-    default: break;
     }
-    return hipErrorInvalidValue;
 }
 
 template <class Mul> hipError_t launch_kind(Product kind, const ProductArgs& p, FastTile tile, hipStream_t stream)
@@ -71,29 +97,19 @@ hipError_t launch_product_pair(ProductType type, const ProductArgs& dx, const Pr
 {
     const auto& a = static_cast<const LossProductArgs&>(dx);
     const auto& b = static_cast<const LossProductArgs&>(dw);
-    auto tiles = [](const ProductArgs& p) { return (uint32_t)((p.M + 127) / 128) * ((p.N + 127) / 128); };
+    constexpr LossTile t = loss_tile(FastTile::T128x128);
+    auto tiles = [](const ProductArgs& p) { return (uint32_t)((p.M + t.bm - 1) / t.bm) * ((p.N + t.bn - 1) / t.bn); };
     const uint32_t first = tiles(a), grid = first + tiles(b);
     if (type == ProductType::BF16)
-        linear_pair_kernel<MulBf16, 128, 128, 2, 4><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
+        linear_pair_kernel<MulBf16, t.bm, t.bn, t.wm, t.wn><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
     else if (type == ProductType::F32)
-        linear_pair_kernel<MulF32, 128, 128, 2, 4><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
+        linear_pair_kernel<MulF32, t.bm, t.bn, t.wm, t.wn><<<grid, FAST_THREADS, 0, stream>>>(a, b, (int)first);
     else
         return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
-// BN / WN of launch_one's tiles
-int loss_columns(ProductType type, FastTile tile)
-{
-    if (type == ProductType::F32) return 32;
-    return tile == FastTile::T256x192 ? 96 : tile == FastTile::T128x128 ? 32 : 64;
-}
-
-// BM / WM
-int loss_rows(ProductType type, FastTile tile)
-{
-    if (type == ProductType::F32) return tile == FastTile::T128x128 ? 64 : 32;
-    return tile == FastTile::T256x256 ? 128 : tile == FastTile::T192x256 ? 96 : 64;
-}
+int loss_columns(FastTile tile) { return loss_tile(tile).bn / loss_tile(tile).wn; }
+int loss_rows(FastTile tile) { return loss_tile(tile).bm / loss_tile(tile).wm; }
 
 }  // namespace miconv

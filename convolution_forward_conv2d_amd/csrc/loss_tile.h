@@ -125,7 +125,7 @@ __device__ __forceinline__ void gradient_wave(const LossProductArgs& p, Block (&
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int here = rows[i].at - n0;                      // NO_GRADIENT wraps to no column
+        const int here = (int)((uint32_t)rows[i].at - (uint32_t)n0);     // of NO_GRADIENT 2^30 at least: no column
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
