@@ -20,6 +20,10 @@ constexpr int64_t kLogitsBytes = int64_t(1) << 28, kGradientBytes = int64_t(1) <
 constexpr int kPieceStep = 1024;                               // classes; also a piece of any number of rows has as many
 constexpr int kPieceMost = 1 << 19;                            // dz's rows stay short of 4 MB
 
+// The share of all classes in fp32, below 1 there too: at 1 a target that a bias takes out would have 0 times infinity for a
+// loss.
+float share_of(double label_smoothing) { return std::min((float)label_smoothing, 0x1.fffffep-1f); }
+
 ProductType type_of(mic_dtype d) { return d == MIC_DTYPE_F32 ? ProductType::F32 : ProductType::BF16; }
 ProductType logits_type(ProductType t) { return t == ProductType::F32 ? ProductType::F32 : ProductType::BF16_F32; }
 
@@ -367,7 +371,7 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
     if (m && (!lse || !aligned(lse, 4) || !target || !aligned(target, 8))) return MIC_STATUS_BAD_PARAM;
     if (!each && (!count || !aligned(count, 4))) return MIC_STATUS_BAD_PARAM;
     LossArgs a = {};
-    a.target = target, a.ignore = ignore_index, a.classes = n, a.smooth = (float)label_smoothing;
+    a.target = target, a.ignore = ignore_index, a.classes = n, a.smooth = share_of(label_smoothing);
     if (m == 0) return launched(launch_loss_reduce(a, 0, loss, reduction == MIC_REDUCTION_MEAN, loss, count, handle->stream));
 
     const ProductType type = type_of(dtype);
@@ -494,7 +498,7 @@ mic_status mic_linear_cross_entropy_backward(mic_handle handle, mic_dtype dtype,
     uint8_t* logits = dz + way.dz + way.sums + way.sum;
     uint8_t* space = logits + way.logits;
     LossArgs a = {};
-    a.target = target, a.ignore = ignore_index, a.classes = n, a.smooth = (float)label_smoothing;
+    a.target = target, a.ignore = ignore_index, a.classes = n, a.smooth = share_of(label_smoothing);
     a.lse = lse, a.dloss = dloss, a.dloss_rows = dloss_rows, a.count = count;
     for (int v = 0; v < n; v += way.piece) {
         const int columns = std::min(way.piece, n - v);
