@@ -14,10 +14,13 @@ using namespace miconv;
 // run, finished where it is read.
 constexpr int kRun = 1024, kWholeRow = 4096;
 int run_of(int n) { return n <= kWholeRow ? kWholeRow : kRun; }
-// What is held of the logits at one time: fp32 where they pass through memory, dz in the tensors' type.  A piece is a
-// product's columns: at 4096 rows of 4096 features 16384 of them keep every tile busy 8 rounds long.
+// What is held of the logits at one time: fp32 where a loss passes them through memory, dz in the tensors' type (and, where
+// a gradient's pass through memory, fp32 logits for as many classes).  A piece is a product's columns: at 4096 rows of
+// 4096 features 16384 of them keep every tile busy 8 rounds long.
 constexpr int64_t kLogitsBytes = int64_t(1) << 28, kGradientBytes = int64_t(1) << 29;
-constexpr int kPieceStep = 1024;                               // classes; also a piece of any number of rows has as many
+constexpr int kPieceStep = 1024;                               // classes; also a piece of any number of rows has as many, each
+                                                               // piece reading all of x: more than those bytes past 65536
+                                                               // rows (a loss, fp32 gradients 131072, bf16 262144)
 constexpr int kPieceMost = 1 << 19;                            // dz's rows stay short of 4 MB
 
 // The share of all classes in fp32, below 1 there too: at 1 a target that a bias takes out would have 0 times infinity for a

@@ -559,11 +559,11 @@ mic_status mic_gated_linear_backward(mic_handle handle, mic_dtype dtype, mic_act
  *
  * x and w F32 or BF16, bias (may be null) of their type; the logits are summed
  * in fp32 and never rounded.  They are not kept: large products reduce each row
- * of a tile where it is computed, others pass at most 256 MB of them at a time
- * through the workspace.  A bias of -infinity takes a class out (of a row whose
- * target it is the loss is infinite, with smoothing every row's).  A target that
- * is neither a class nor ignore_index makes its row's loss NaN; it reads nothing
- * out of bounds. */
+ * of a tile where it is computed, others pass them through the workspace, at most
+ * 256 MB (or 1024 classes, where m rows of those are more) at a time.  A bias of
+ * -infinity takes a class out (of a row whose target it is the loss is infinite,
+ * with smoothing every row's).  A target that is neither a class nor ignore_index
+ * makes its row's loss NaN; it reads nothing out of bounds. */
 typedef enum {
     MIC_REDUCTION_NONE = 0,
     MIC_REDUCTION_SUM = 1,
@@ -586,9 +586,10 @@ mic_status mic_linear_cross_entropy(mic_handle handle, mic_dtype dtype, mic_redu
  *
  * dx, dw and dbias may each be null.  z is computed again and dz enters the
  * products in the tensors' type, at most 512 MB of it (or 1024 classes) at a
- * time; dx's sums over several such pieces are fp32.  A row whose target is
- * ignore_index, or all of whose classes a bias takes out, has dz = 0 whatever
- * its logits; x still enters dw's product, so its values there must be finite. */
+ * time; logits that pass through the workspace are as many, in fp32.  dx's sums
+ * over several such pieces are fp32.  A row whose target is ignore_index, or all
+ * of whose classes a bias takes out, has dz = 0 whatever its logits; x still
+ * enters dw's product, so its values there must be finite. */
 mic_status mic_linear_cross_entropy_backward_workspace(mic_handle handle, mic_dtype dtype, int m, int n, int k, size_t* bytes);
 mic_status mic_linear_cross_entropy_backward_workspace_aligned(mic_handle handle, mic_dtype dtype, int m, int n, int k,
                                                                size_t* bytes);
