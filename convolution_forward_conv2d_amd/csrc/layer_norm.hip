@@ -664,8 +664,8 @@ hipError_t launch_layer_norm(DType dt, bool e4m3, const LayerNormArgs& p, hipStr
 }
 
 // 0: one launch.  Of few rows it saves the second launch and the walk: 64 x 4096 bf16 5.2 us (9.1), 300 x 4096 5.2 (10.9),
-// 768 x 4096 7.3 (14.3); 1024 x 4095 19.8 (17.9).  Rows past 16384 columns do not stay in a workgroup's registers, and are
-// then read as often: 8192 x 20000 bf16 385 us (863 with a walk of their own for dweight and dbias).
+// 768 x 4096 7.3 (14.3); 1024 x 4095 19.8 (17.9).  Rows past 16384 columns do not stay in the registers of a walk's sixteen
+// waves, and are then read as often: 8192 x 20000 bf16 385 us (863 with a walk of their own for dweight and dbias).
 // Otherwise a group's shares of dweight and dbias are written and read again, so as few groups as keep memory busy: one of
 // eight waves a CU (8192 x 4096 bf16 takes 49 us, 56 with two), two of four waves (8192 x 2048 30, 35 with four), each
 // walking three rows at least.  Rows that fill a quarter to a half of four waves go to two where walks stay long: 8192 x
